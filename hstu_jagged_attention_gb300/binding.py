@@ -49,7 +49,23 @@ class _NormGate(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class _PagedBatch(ctypes.Structure):
+    """struct hstu_paged_batch"""
+    _fields_ = [("q_offsets", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("num_targets", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int), ("max_pages", ctypes.c_int), ("max_q", ctypes.c_int),
+                ("rows", ctypes.c_int)]
+
+
+class _Rotary(ctypes.Structure):
+    """struct hstu_rotary"""
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int), ("dim", ctypes.c_int),
+                ("pairs", ctypes.c_int)]
+
+
 _RABP, _NGP = ctypes.POINTER(_Rab), ctypes.POINTER(_NormGate)
+_PBP, _ROTP = ctypes.POINTER(_PagedBatch), ctypes.POINTER(_Rotary)
+_I64, _F32, _INT = ctypes.c_int64, ctypes.c_float, ctypes.c_int
 _SIGNATURES = {
     "hstu_attn_fwd": (ctypes.c_int, [_VP, _VP, _VP, _VP, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                      ctypes.c_int, ctypes.c_float, ctypes.c_float, _VP, _VP]),
@@ -114,6 +130,18 @@ _SIGNATURES = {
                                                _I32P, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                ctypes.c_int, ctypes.c_float, ctypes.c_float, _VP,
                                                _VP]),
+    "hstu_cache_create": (_INT, [_VP, _VP, _INT, _INT, _INT, _INT, _I64, ctypes.POINTER(_VP)]),
+    "hstu_cache_destroy": (_INT, [_VP]),
+    "hstu_cache_workspace": (_INT, [_VP, ctypes.POINTER(ctypes.c_size_t)]),
+    "hstu_cache_slots": (_INT, [_PBP, _INT, _INT, ctypes.POINTER(_I64), _I32P]),
+    "hstu_cache_worklist": (_INT, [_PBP, _INT, _INT, _INT, _INT, _INT, _INT, _INT, _I32P, _INT, _IP]),
+    "hstu_cache_append": (_INT, [_VP, _PBP, _VP, _I64, _VP, _I64, _VP, _I64, _ROTP, _VP, _VP]),
+    "hstu_attn_fwd_cache": (_INT, [_VP, _PBP, _VP, _I64, _F32, _F32, _VP, _VP, _VP]),
+    "hstu_norm_fwd": (_INT, [_VP, _I64, _VP, _I64, _F32, _VP, _I64, _VP, _VP, _F32, _I64, _INT, _VP, _VP,
+                             _VP]),
+    "hstu_norm_bwd_workspace": (_INT, [_INT, ctypes.POINTER(ctypes.c_size_t)]),
+    "hstu_norm_bwd": (_INT, [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _F32, _VP, _I64, _F32, _I64, _INT,
+                             _VP, _VP, _VP, _I64, _VP, _VP, _VP, _VP]),
 }
 
 HSTU_PLAN_NORM_GATE = 1
@@ -645,3 +673,286 @@ def hstu_trace_read(capacity: int = 32768) -> np.ndarray:
     out["warp"] = ((raw[:, 1] >> np.uint64(40)) & np.uint64(0xFF)).astype(np.int32)
     out["index"] = (raw[:, 1] & np.uint64((1 << 40) - 1)).astype(np.int64)
     return out
+
+
+# ------------------------------------------------------- the paged K/V cache
+def _is(t, dtype: str, what: str):
+    if str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+    return t
+
+
+def _on_gpu(t, device, what: str):
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+
+
+def _cuda_stream(stream, device):
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream or None
+    return _stream(stream)
+
+
+def _row_stride(t, shape, device, what: str) -> int:
+    """Elements between rows of a bf16 device tensor of ``shape`` whose rows
+    are packed (a slice of a wider projection has a larger row stride)."""
+    _is(t, "bfloat16", what)
+    _on_gpu(t, device, what)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
+    step, width = t.stride(), 1
+    for n, st in zip(shape[:0:-1], step[:0:-1]):
+        if n != 1 and st != width:
+            raise ValueError(f"{what}: the values of a row must be packed")
+        width *= n
+    return step[0] if shape[0] > 1 else max(step[0], width)
+
+
+def _packed(t, shape, device, what: str) -> int:
+    if _row_stride(t, shape, device, what) != _width(shape) and shape[0] > 1:
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _width(shape) -> int:
+    w = 1
+    for n in shape[1:]:
+        w *= n
+    return w
+
+
+class Cache:
+    """Owner of an ``hstu_cache*`` over the caller's page pools, which it keeps alive."""
+
+    def __init__(self, handle: int, k_pages, v_pages):
+        self.handle, self.k_pages, self.v_pages = handle, k_pages, v_pages
+        self.num_pages, self.page_size, self.heads, self.d = (int(n) for n in k_pages.shape)
+        self.device = k_pages.device
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        hstu_cache_destroy(self)
+
+    def __del__(self):
+        try:
+            hstu_cache_destroy(self)
+        except Exception:
+            pass
+
+
+class PagedBatch:
+    """A batch of new tokens against a cache (struct hstu_paged_batch): int32
+    device tensors ``q_offsets`` (batch + 1), ``kv_lens`` (batch),
+    ``page_table`` (batch, max_pages) and optionally ``num_targets`` (batch).
+    The kernels read them when they run, so a captured call follows their
+    contents.  ``max_q`` bounds the new tokens of every sequence.  With
+    numpy arrays the batch serves the host-only functions."""
+
+    def __init__(self, q_offsets, kv_lens, page_table, max_q: int, num_targets=None):
+        arrays = dict(q_offsets=q_offsets, kv_lens=kv_lens, page_table=page_table)
+        if num_targets is not None:
+            arrays["num_targets"] = num_targets
+        batch = int(q_offsets.shape[0]) - 1
+        shapes = dict(q_offsets=(batch + 1,), kv_lens=(batch,), num_targets=(batch,),
+                      page_table=(batch, int(page_table.shape[1]) if page_table.ndim == 2 else -1))
+        self.host = isinstance(q_offsets, np.ndarray)
+        self.device = None if self.host else q_offsets.device
+        for name, a in arrays.items():
+            if isinstance(a, np.ndarray) != self.host:
+                raise ValueError("the batch's arrays must all be device tensors, or all numpy arrays")
+            if str(a.dtype).replace("torch.", "") != "int32":
+                raise ValueError(f"{name} must be int32, not {a.dtype}")
+            if batch < 0 or tuple(a.shape) != shapes[name]:
+                raise ValueError(f"{name} has shape {tuple(a.shape)}, not {shapes[name]}")
+            if not (a.flags.c_contiguous if self.host else a.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous")
+            if not self.host:
+                if not a.is_cuda:
+                    raise ValueError(f"{name} must be a device tensor (or a numpy array)")
+                _on_gpu(a, self.device, name)
+        self.keep, self.batch, self.max_q = arrays, batch, int(max_q)
+        at = {n: (a.ctypes.data if self.host else a.data_ptr()) for n, a in arrays.items()}
+        self._fields = (at["q_offsets"], at["kv_lens"], at.get("num_targets"), at["page_table"], batch,
+                        shapes["page_table"][1], self.max_q)
+
+    def struct(self, rows: int):
+        return ctypes.byref(_PagedBatch(*self._fields, int(rows)))
+
+
+def hstu_cache_create(k_pages, v_pages) -> Cache:
+    """A cache over the pools ``k_pages`` and ``v_pages``: bf16 device tensors
+    (num_pages, page_size, heads, d) with packed pages (pages may lie further
+    apart, as in a pool that interleaves K and V)."""
+    shape = tuple(int(n) for n in k_pages.shape)
+    if len(shape) != 4 or not k_pages.is_cuda:
+        raise ValueError("k_pages must be a device tensor (num_pages, page_size, heads, d)")
+    stride = _row_stride(k_pages, shape, k_pages.device, "k_pages")
+    if _row_stride(v_pages, shape, k_pages.device, "v_pages") != stride:
+        raise ValueError("k_pages and v_pages must have the same page stride")
+    h = _VP()
+    _check(lib().hstu_cache_create(k_pages.data_ptr(), v_pages.data_ptr(), *shape, stride,
+                                   ctypes.byref(h)), "hstu_cache_create")
+    return Cache(h.value, k_pages, v_pages)
+
+
+def hstu_cache_destroy(cache: Cache) -> None:
+    if cache.handle:
+        h, cache.handle = cache.handle, None
+        _check(lib().hstu_cache_destroy(h), "hstu_cache_destroy")
+
+
+def hstu_cache_workspace_bytes(cache: Cache) -> int:
+    """Bytes of a workspace for hstu_attn_fwd_cache (zero it once)."""
+    n = ctypes.c_size_t()
+    _check(lib().hstu_cache_workspace(cache.handle, ctypes.byref(n)), "hstu_cache_workspace")
+    return n.value
+
+
+def hstu_cache_append(cache: Cache, batch: PagedBatch, k, v, q=None, q_out=None, rotary=None,
+                      rotary_pairs: bool = False, stream=None) -> None:
+    """Write the new tokens' ``k`` and ``v`` (rows, heads, d) into the cache.
+
+    ``rotary``: fp32 (positions, dim) table, cosines then sines: keys (and
+    ``q``, into ``q_out``) are rotated by their position on the way, channels
+    i and dim / 2 + i together, or with ``rotary_pairs`` 2 i and 2 i + 1."""
+    shape = (int(k.shape[0]), cache.heads, cache.d)
+    _on_gpu(batch.keep["q_offsets"], cache.device, "the batch")
+    ks = _row_stride(k, shape, cache.device, "k")
+    vs = _row_stride(v, shape, cache.device, "v")
+    qs = 0 if q is None else _row_stride(q, shape, cache.device, "q")
+    qo = None if q_out is None else _packed(q_out, shape, cache.device, "q_out")
+    rot = None
+    if rotary is not None:
+        _is(rotary, "float32", "rotary")
+        _on_gpu(rotary, cache.device, "rotary")
+        if rotary.ndim != 2 or not rotary.is_contiguous():
+            raise ValueError("rotary must be a contiguous (positions, dim) table")
+        rot = ctypes.byref(_Rotary(rotary.data_ptr(), int(rotary.shape[0]), int(rotary.shape[1]),
+                                   int(bool(rotary_pairs))))
+    _check(lib().hstu_cache_append(cache.handle, batch.struct(shape[0]),
+                                   None if q is None else q.data_ptr(), qs, k.data_ptr(), ks,
+                                   v.data_ptr(), vs, rot, qo, _cuda_stream(stream, cache.device)),
+           "hstu_cache_append")
+
+
+def hstu_attn_fwd_cache(cache: Cache, batch: PagedBatch, q, alpha: float, inv_n: float, out,
+                        workspace=None, stream=None) -> None:
+    """The attention of the new tokens ``q`` (rows, heads, d) over the cache,
+    which already holds their own keys and values, into ``out``.
+    ``workspace``: a zeroed uint8 device tensor of hstu_cache_workspace_bytes,
+    kept between calls (one call at a time); None allocates per call."""
+    shape = (int(q.shape[0]), cache.heads, cache.d)
+    _on_gpu(batch.keep["q_offsets"], cache.device, "the batch")
+    qs = _row_stride(q, shape, cache.device, "q")
+    o = _packed(out, shape, cache.device, "out")
+    ws = None
+    if workspace is not None:
+        _on_gpu(workspace, cache.device, "workspace")
+        if not workspace.is_contiguous() or \
+                workspace.numel() * workspace.element_size() < hstu_cache_workspace_bytes(cache):
+            raise ValueError("workspace needs hstu_cache_workspace_bytes contiguous bytes")
+        ws = workspace.data_ptr()
+    _check(lib().hstu_attn_fwd_cache(cache.handle, batch.struct(shape[0]), q.data_ptr(), qs, float(alpha),
+                                     float(inv_n), o, ws, _cuda_stream(stream, cache.device)),
+           "hstu_attn_fwd_cache")
+
+
+def hstu_cache_slots(batch: PagedBatch, num_pages: int, page_size: int, rows: int):
+    """Host-only (no CUDA call; a batch of numpy arrays): (slots int64, positions
+    int32, ok) of the rows; ok is False when the device would report the batch."""
+    if not batch.host:
+        raise ValueError("hstu_cache_slots takes a batch of numpy arrays")
+    slot = np.full(max(rows, 1), -2, dtype=np.int64)
+    pos = np.full(max(rows, 1), -2, dtype=np.int32)
+    code = lib().hstu_cache_slots(batch.struct(rows), int(num_pages), int(page_size),
+                                  slot.ctypes.data_as(ctypes.POINTER(_I64)), pos.ctypes.data_as(_I32P))
+    if code != HSTU_OK and (rows == 0 or slot[0] == -2):
+        raise HstuError(code, "hstu_cache_slots")
+    return slot[:rows], pos[:rows], code == HSTU_OK
+
+
+def hstu_cache_worklist(batch: PagedBatch, num_pages: int, page_size: int, rows: int, heads: int,
+                        tile_rows: int, block_keys: int, grid: int, min_units: int = 1) -> np.ndarray:
+    """Host-only (no CUDA call; a batch of numpy arrays): the shares of
+    hstu_attn_fwd_cache's CTAs, int32 (n, 8): CTA, sequence, head, tile, first
+    block, blocks, first CTA of the item, CTAs that share it."""
+    if not batch.host:
+        raise ValueError("hstu_cache_worklist takes a batch of numpy arrays")
+    args = (batch.struct(rows), int(num_pages), int(page_size), int(heads), int(tile_rows),
+            int(block_keys), int(grid), int(min_units))
+    n = ctypes.c_int()
+    _check(lib().hstu_cache_worklist(*args, None, 0, ctypes.byref(n)), "hstu_cache_worklist")
+    buf = np.zeros((max(n.value, 1), 8), dtype=np.int32)
+    _check(lib().hstu_cache_worklist(*args, buf.ctypes.data_as(_I32P), n.value, ctypes.byref(n)),
+           "hstu_cache_worklist")
+    return buf[:n.value]
+
+
+# ------------------------------------------- layer norm, its gate and residual
+def _vector(t, width: int, device, what: str) -> int:
+    _is(t, "float32", what)
+    _on_gpu(t, device, what)
+    if tuple(t.shape) != (width,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {width} entries")
+    return t.data_ptr()
+
+
+def hstu_norm_fwd(x, gamma, beta, eps: float, y, u=None, residual=None, scale: float = 1.0, z=None,
+                  stream=None) -> None:
+    """y = Norm(z) (.) u with z = residual + ``scale`` x (z = x without a
+    ``residual``; then ``z`` is not given, else it receives the new residual
+    stream).  x, u, residual, y, z: bf16 (rows, width), inputs with any row
+    stride; gamma, beta: fp32 (width)."""
+    if x.ndim != 2 or not x.is_cuda:
+        raise ValueError("x must be a device tensor (rows, width)")
+    shape, dev = (int(x.shape[0]), int(x.shape[1])), x.device
+    xs = _row_stride(x, shape, dev, "x")
+    us = 0 if u is None else _row_stride(u, shape, dev, "u")
+    rs = 0 if residual is None else _row_stride(residual, shape, dev, "residual")
+    _check(lib().hstu_norm_fwd(x.data_ptr(), xs, None if residual is None else residual.data_ptr(), rs,
+                               float(scale), None if u is None else u.data_ptr(), us,
+                               _vector(gamma, shape[1], dev, "gamma"),
+                               _vector(beta, shape[1], dev, "beta"), float(eps), shape[0], shape[1],
+                               _packed(y, shape, dev, "y"),
+                               None if z is None else _packed(z, shape, dev, "z"),
+                               _cuda_stream(stream, dev)), "hstu_norm_fwd")
+
+
+def hstu_norm_bwd_workspace_bytes(width: int) -> int:
+    """Bytes of a workspace for hstu_norm_bwd on the current device."""
+    n = ctypes.c_size_t()
+    _check(lib().hstu_norm_bwd_workspace(int(width), ctypes.byref(n)), "hstu_norm_bwd_workspace")
+    return n.value
+
+
+def hstu_norm_bwd(dy, z, gamma, beta, eps: float, dz, dgamma, dbeta, u=None, du=None, dz_in=None,
+                  dx=None, scale: float = 1.0, workspace=None, stream=None) -> None:
+    """Gradients of hstu_norm_fwd for ``dy``: ``dz`` of the norm's input ``z``
+    (x without a residual; with one also the residual's gradient), with
+    ``dz_in`` (the gradient reaching z past the norm) added; ``dx`` = scale
+    dz; ``du`` of the gate ``u``; ``dgamma``, ``dbeta`` (fp32, overwritten)."""
+    if dy.ndim != 2 or not dy.is_cuda:
+        raise ValueError("dy must be a device tensor (rows, width)")
+    shape, dev = (int(dy.shape[0]), int(dy.shape[1])), dy.device
+
+    def at(t, what):
+        return (None, 0) if t is None else (t.data_ptr(), _row_stride(t, shape, dev, what))
+
+    ws = None
+    if workspace is not None:
+        _on_gpu(workspace, dev, "workspace")
+        if not workspace.is_contiguous() or \
+                workspace.numel() * workspace.element_size() < hstu_norm_bwd_workspace_bytes(shape[1]):
+            raise ValueError("workspace needs hstu_norm_bwd_workspace_bytes contiguous bytes")
+        ws = workspace.data_ptr()
+    _check(lib().hstu_norm_bwd(*at(dy, "dy"), *at(z, "z"), *at(u, "u"),
+                               _vector(gamma, shape[1], dev, "gamma"),
+                               _vector(beta, shape[1], dev, "beta"), float(eps), *at(dz_in, "dz_in"),
+                               float(scale), shape[0], shape[1], _packed(dz, shape, dev, "dz"),
+                               None if dx is None else _packed(dx, shape, dev, "dx"), *at(du, "du"),
+                               _vector(dgamma, shape[1], dev, "dgamma"),
+                               _vector(dbeta, shape[1], dev, "dbeta"), ws, _cuda_stream(stream, dev)),
+           "hstu_norm_bwd")

@@ -1,6 +1,6 @@
 """Build ``libhstu.so`` (sm_103a) in-tree with nvcc.
 
-Both translation units compile in parallel; the shared library links the
+The translation units compile in parallel; the shared library links the
 CUDA runtime statically, so loading it needs no libcuda until the first CUDA
 call (the C-ABI symbol checks run on machines without a GPU).
 """
@@ -18,7 +18,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhstu.so")
-SOURCES = ["hstu_fwd.cu", "hstu_api.cpp", "hstu_noalloc.cu"]
+SOURCES = ["hstu_fwd.cu", "hstu_api.cpp", "hstu_noalloc.cu", "hstu_cache.cu", "hstu_norm.cu"]
+HEADERS = ["hstu_internal.h", "hstu_ptx.cuh", "hstu_paged.h", "hstu_bwd.cuh", "hstu_fwd_pair.cuh",
+           "hstu_bwd_t.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,12 +34,8 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, "hstu_internal.h"), os.path.join(CSRC, "hstu_bwd.cuh"),
-              os.path.join(CSRC, "hstu_fwd_pair.cuh"), os.path.join(CSRC, "hstu_bwd_t.cuh"),
-              os.path.join(INCLUDE, "hstu_attn.h"),
-              os.path.abspath(__file__)]
-    return files
+    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    return files + [os.path.join(INCLUDE, "hstu_attn.h"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:

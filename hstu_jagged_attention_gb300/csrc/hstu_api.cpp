@@ -523,6 +523,21 @@ long long schedule_items(const int32_t* cost, int n, int grid, int32_t* order, i
   return span;
 }
 
+int host_device_check(int* sm_count) { return device_check(sm_count); }
+unsigned long long host_wait_timeout_ns() { return wait_timeout_ns(); }
+
+int host_encode_map(CUtensorMap* m, void* ptr, int rank, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box, bool wide) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return HSTU_ERR_CUDA;
+  const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, ptr, dims, strides, box,
+                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
 int host_check_offsets(const int32_t* off, int batch, long long max_len) {
   return check_offsets(off, batch, max_len);
 }
@@ -1491,7 +1506,9 @@ int hstu_last_status(int* device_status, int* site) {
   if (!device_status) return HSTU_ERR_INVALID_ARG;
   unsigned st = 0, where = 0;
   if (hstu::read_and_clear_device_status(&st, &where) != cudaSuccess) return HSTU_ERR_CUDA;
-  *device_status = (st & 1u) ? HSTU_ERR_TIMEOUT : HSTU_OK;
+  *device_status = (st & hstu::kStatusTimeout)    ? HSTU_ERR_TIMEOUT
+                   : (st & hstu::kStatusBadPaged) ? HSTU_ERR_INVALID_ARG
+                                                  : HSTU_OK;
   if (site) *site = (int)where;
   return HSTU_OK;
 }

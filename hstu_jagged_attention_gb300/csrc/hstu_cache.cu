@@ -1,0 +1,964 @@
+// The paged K/V cache: appending keys and values to it (with the position
+// rotation), and the attention of a few new tokens over it.
+//
+//   append   slot = page_table[b][p / page_size] page_size + p % page_size,
+//            k_pages[slot] = R_p k, v_pages[slot] = v, q_out = R_p q
+//   attention
+//            out[t,h,:] = inv_n sum_j silu(alpha q[t,h,:].K_j) V_j over the
+//            keys j <= p(t) of the cache, candidates as in the forward
+//
+// (ai6s.net post section 1 for the formula; HSTU paper section 3.4: the
+// history's keys and values are cached and serve every microbatch.)
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <new>
+
+#include "hstu_attn.h"
+#include "hstu_internal.h"
+#include "hstu_paged.h"
+#include "hstu_ptx.cuh"
+
+namespace hstu {
+namespace {
+
+// ------------------------------------------------------------------- append
+struct AppendArgs {
+  PagedView p;
+  const uint16_t *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  uint16_t *k_pages, *v_pages, *q_out;
+  long long page_stride;
+  const float* table;  // (positions, rot): rot / 2 cosines, then as many sines; null: no rotation
+  int positions, rot, pairs;
+  int heads, d;
+  unsigned* status;
+};
+
+struct F8 {
+  float f[8];
+};
+
+__device__ __forceinline__ F8 unpack8(const uint4& p) {
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+  F8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.f[2 * i] = __uint_as_float(w[i] << 16);
+    v.f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint4 pack8(const F8& v) {
+  return make_uint4(pack_bf16x2(v.f[0], v.f[1]), pack_bf16x2(v.f[2], v.f[3]),
+                    pack_bf16x2(v.f[4], v.f[5]), pack_bf16x2(v.f[6], v.f[7]));
+}
+
+// 16 channels of one head as two vectors of 8: x = channels at c0, y = those
+// at c1.  Pairs: channels 2i and 2i + 1 turn together, so each vector turns
+// within itself; halves: x[i] turns with y[i].  One rounding, at the end.
+__device__ __forceinline__ void turn16(uint4& x, uint4& y, const F8& cs, const F8& sn, bool pairs) {
+  F8 a = unpack8(x), b = unpack8(y);
+  if (pairs) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a0 = a.f[2 * i], a1 = a.f[2 * i + 1], b0 = b.f[2 * i], b1 = b.f[2 * i + 1];
+      a.f[2 * i] = fmaf(a0, cs.f[i], -(a1 * sn.f[i]));
+      a.f[2 * i + 1] = fmaf(a1, cs.f[i], a0 * sn.f[i]);
+      b.f[2 * i] = fmaf(b0, cs.f[4 + i], -(b1 * sn.f[4 + i]));
+      b.f[2 * i + 1] = fmaf(b1, cs.f[4 + i], b0 * sn.f[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a0 = a.f[i], b0 = b.f[i];
+      a.f[i] = fmaf(a0, cs.f[i], -(b0 * sn.f[i]));
+      b.f[i] = fmaf(b0, cs.f[i], a0 * sn.f[i]);
+    }
+  }
+  x = pack8(a);
+  y = pack8(b);
+}
+
+constexpr int kAppendThreads = 256;
+
+// One thread a (token, head, 16 channels): every array is read and written
+// once, with 16-byte accesses.  Bound by memory; a step of a few tokens by
+// the chain offsets -> lengths -> page -> store.
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  const int per_head = a.d / 16, per_token = a.heads * per_head;
+  const long long unit = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
+  const long long tl = unit / per_token;
+  if (tl >= a.p.rows) return;
+  const int t = (int)tl, w = (int)(unit - tl * per_token);
+  const int h = w / per_head, c = w - h * per_head;
+  // rotated channels first, 16 a thread; then the others
+  const bool turn = a.table && c < a.rot / 16;
+  int c0 = 16 * c, c1 = 16 * c + 8;
+  if (turn && !a.pairs) {
+    c0 = 8 * c;
+    c1 = a.rot / 2 + 8 * c;
+  }
+  const long long at = (long long)h * a.d;
+  const uint16_t* kr = a.k + t * a.k_stride + at;
+  const uint16_t* vr = a.v + t * a.v_stride + at;
+  const int total = a.p.q_offsets[a.p.batch];
+  uint4 k0 = *reinterpret_cast<const uint4*>(kr + c0), k1 = *reinterpret_cast<const uint4*>(kr + c1);
+  const uint4 v0 = *reinterpret_cast<const uint4*>(vr + c0), v1 = *reinterpret_cast<const uint4*>(vr + c1);
+  uint4 q0{}, q1{};
+  if (a.q) {
+    const uint16_t* qr = a.q + t * a.q_stride + at;
+    q0 = *reinterpret_cast<const uint4*>(qr + c0);
+    q1 = *reinterpret_cast<const uint4*>(qr + c1);
+  }
+  if (t >= total) return;  // a row behind the last sequence
+  const int b = paged_find(a.p, t);
+  PagedSeq s;
+  if (b < 0 || !paged_seq(a.p, b, &s)) {
+    atomicOr(a.status, kStatusBadPaged);
+    return;
+  }
+  const int pos = s.kv - s.qn + (t - s.q0);
+  const long long slot = paged_slot(a.p, b, pos);
+  const int turned_at = pos < s.hist ? pos : s.hist;  // a candidate stands right behind the history
+  if (slot < 0 || (a.table && turned_at >= a.positions)) {
+    atomicOr(a.status, kStatusBadPaged);
+    return;
+  }
+  if (turn) {
+    const float* tab = a.table + (long long)turned_at * a.rot + 8 * c;
+    F8 cs, sn;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(tab) + i);
+      const float4 y = __ldg(reinterpret_cast<const float4*>(tab + a.rot / 2) + i);
+      cs.f[4 * i] = x.x; cs.f[4 * i + 1] = x.y; cs.f[4 * i + 2] = x.z; cs.f[4 * i + 3] = x.w;
+      sn.f[4 * i] = y.x; sn.f[4 * i + 1] = y.y; sn.f[4 * i + 2] = y.z; sn.f[4 * i + 3] = y.w;
+    }
+    turn16(k0, k1, cs, sn, a.pairs);
+    if (a.q) turn16(q0, q1, cs, sn, a.pairs);
+  }
+  const long long page = slot >> a.p.page_shift;
+  const long long in_page = slot & ((1 << a.p.page_shift) - 1);
+  const long long to = page * a.page_stride + in_page * a.heads * a.d + at;
+  *reinterpret_cast<uint4*>(a.k_pages + to + c0) = k0;
+  *reinterpret_cast<uint4*>(a.k_pages + to + c1) = k1;
+  *reinterpret_cast<uint4*>(a.v_pages + to + c0) = v0;
+  *reinterpret_cast<uint4*>(a.v_pages + to + c1) = v1;
+  if (a.q) {
+    uint16_t* qo = a.q_out + (long long)t * a.heads * a.d + at;
+    *reinterpret_cast<uint4*>(qo + c0) = q0;
+    *reinterpret_cast<uint4*>(qo + c1) = q1;
+  }
+}
+
+// ------------------------------------------------ attention of a few tokens
+// A tile is up to 16 MT new tokens of one (sequence, head); it walks blocks
+// of 64 keys.  Warp 4 copies each block's K and V rows, page by page, into a
+// ring of shared-memory stages (bulk-tensor copies, swizzled rows).  Warps
+// 0-3 take 16 of the 64 keys each: S = Q K^T, p = silu(alpha S), O += p V on
+// mma.sync m16n8k16, with p split into two bf16 terms as in the forward, so
+// that P V keeps 16 bits of p.  With so few rows the cache is read once for
+// them all and the copies, not the products, set the time: a 128-row tcgen05
+// tile would do the same reads with 8 times the products.
+constexpr int kStepKeys = 64, kStepShift = 6;
+constexpr int kStepWarps = 4;  // warps that compute
+constexpr int kStepThreads = 32 * (kStepWarps + 1);
+
+struct StepArgs {
+  PagedView p;
+  PagedWork w;     // total and per are found by the kernel
+  int min_units;
+  int stages;
+  int red_rows;    // rows of a tile that can exist: min(max_q, tile_rows)
+  const uint16_t* q;
+  long long q_stride;
+  uint16_t* out;
+  float half_alpha, inv_n;
+  unsigned* counters;
+  float* parts;
+  unsigned* status;
+  unsigned long long timeout_ns;
+};
+
+struct StepWait {
+  unsigned long long limit_ns;
+  volatile int* abort_flag;
+  unsigned* status;  // [0]: bits, [1]: the first site that gave up
+};
+
+__device__ __noinline__ void step_timeout(const StepWait& w, int site) {
+  atomicOr(w.status, kStatusTimeout);
+  atomicCAS(w.status + 1, 0u, (unsigned)site);
+  *w.abort_flag = 1;
+}
+
+// Bounded wait; false once the CTA has given up.
+__device__ __forceinline__ bool step_wait(uint32_t bar, uint32_t parity, const StepWait& w, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 3u) == 0) {
+      if (*w.abort_flag) return false;
+      if (globaltimer() - t0 > w.limit_ns) {
+        step_timeout(w, site);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                            int y, int z, int u) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+struct StepCfg {
+  static constexpr int CH = D < 64 ? D : 64;  // channels of a swizzled row
+  static constexpr int NCH = D / CH;
+  static constexpr int ROWB = CH * 2;
+  static constexpr int CHUNKB = kStepKeys * ROWB;
+  static constexpr int TILEB = NCH * CHUNKB;  // 64 rows of K, or of V
+  static constexpr int STAGEB = 2 * TILEB;
+  static constexpr int MAX_STAGES = 16;
+  // byte of 16-byte column c of row r in a tile
+  static __device__ __forceinline__ uint32_t at(int r, int c) {
+    constexpr int PER = CH / 8;  // 16-byte columns of a swizzled row
+    const int ch = c / PER, cc = c % PER;
+    const int x = ROWB == 128 ? (r & 7) : ((r >> 1) & 3);
+    return (uint32_t)(ch * CHUNKB + r * ROWB + ((cc ^ x) << 4));
+  }
+};
+
+// Shared memory behind the stages: the warps' partial sums, the barriers,
+// and the schedule's words.
+__host__ __device__ constexpr int step_red_bytes(int rows, int d) {
+  return kStepWarps * rows * d * (int)sizeof(float);
+}
+constexpr int kStepTailBytes = 2 * 16 * 8 + 64 + 16 * 8;
+
+struct StepMisc {
+  int abort_flag;
+  int last;   // this CTA arrived last at the item it shares
+  int e, r;   // where its share starts
+  long long sums[kStepWarps + 1];
+};
+static_assert(sizeof(StepMisc) <= 64 + 16 * 8, "misc");
+
+// Totals the work over all threads of the CTA and finds where its share
+// starts; false (for all) when it has none.
+__device__ bool step_locate(const StepArgs& a, PagedWork& w, PagedCursor* c, StepMisc* m) {
+  const int n = w.tiles * a.p.batch;
+  const int each = (n + kStepThreads - 1) / kStepThreads;
+  const int e0 = threadIdx.x * each, e1 = e0 + each < n ? e0 + each : n;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long sum = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int qt = e / a.p.batch, b = e - qt * a.p.batch;
+    PagedSeq s;
+    if (!paged_seq(a.p, b, &s) && blockIdx.x == 0) atomicOr(a.status, kStatusBadPaged);
+    sum += (long long)w.heads * paged_walk(s, qt, w.tile_rows, w.kb_shift).nb;
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) m->sums[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i <= kStepWarps; ++i) {
+    if (i < warp) before += m->sums[i];
+    total += m->sums[i];
+  }
+  w.total = total;
+  w.per = paged_share(total, gridDim.x, a.min_units);
+  c->u = (long long)blockIdx.x * w.per;
+  if (c->u >= total) return false;
+  c->u1 = c->u + w.per < total ? c->u + w.per : total;
+  long long at = before + incl - sum;  // the thread's first unit
+  if (at <= c->u && c->u < at + sum) {
+    for (int e = e0; e < e1; ++e) {
+      const int qt = e / a.p.batch, b = e - qt * a.p.batch;
+      PagedSeq s;
+      paged_seq(a.p, b, &s);
+      const long long units = (long long)w.heads * paged_walk(s, qt, w.tile_rows, w.kb_shift).nb;
+      if (c->u < at + units) {
+        m->e = e;
+        m->r = (int)(c->u - at);
+        break;
+      }
+      at += units;
+    }
+  }
+  __syncthreads();
+  c->e = m->e;
+  c->r = m->r;
+  return true;
+}
+
+template <int D>
+__device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const StepArgs& a,
+                             const PagedWork& w, PagedCursor c, uint32_t base, uint32_t full,
+                             uint32_t empty, const StepWait& wt) {
+  using C = StepCfg<D>;
+  const int lane = threadIdx.x & 31;
+  const int shift = a.p.page_shift, ps = 1 << shift;
+  const int box = ps < kStepKeys ? ps : kStepKeys;
+  int st = 0;
+  uint32_t ph = 1, count = 0;
+  PagedSeg g;
+  while (c.next(a.p, w, &g)) {
+    const int32_t* row = a.p.page_table + (long long)g.b * a.p.max_pages;
+    const int end = g.walk.end();
+    const int pages = (end + ps - 1) >> shift;  // of the sequence, as far as the tile sees
+    int first = -64;                             // the page ids at hand: first + lane, and 32 on
+    int ids = 0, ids2 = 0;
+    for (int i = 0; i < g.n; ++i) {
+      const int tok0 = g.walk.block(g.i0 + i) << kStepShift;
+      const int p0 = tok0 >> shift;
+      const int valid = end - tok0 < kStepKeys ? end - tok0 : kStepKeys;
+      const int npg = ps >= kStepKeys ? 1 : (valid + ps - 1) >> shift;
+      if (p0 + npg > first + 32 || p0 < first) {
+        if (p0 == first + 32) {
+          ids = ids2;
+        } else {
+          ids = p0 + lane < pages ? __ldg(row + p0 + lane) : 0;
+        }
+        first = p0;
+        ids2 = p0 + 32 + lane < pages ? __ldg(row + p0 + 32 + lane) : 0;
+      }
+      // lane: which page of the block, which chunk of channels, K or V
+      const int pg = lane / (2 * C::NCH), ch = (lane >> 1) % C::NCH;
+      int page = __shfl_sync(0xffffffffu, ids, (p0 - first + pg) & 31);
+      const uint32_t bar = full + 8u * st;
+      if (!__all_sync(0xffffffffu, step_wait(empty + 8u * st, ph, wt, kSiteStepEmpty))) goto drain;
+      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(npg * box * C::ROWB * C::NCH * 2));
+      __syncwarp();
+      if (pg < npg) {
+        if (page < 0 || page >= a.p.num_pages) {
+          // read as zeros, past the pool's end: silu(0) V = 0
+          atomicOr(a.status, kStatusBadPaged);
+          page = a.p.num_pages;
+        }
+        const uint32_t dst = base + st * C::STAGEB + (lane & 1) * C::TILEB + ch * C::CHUNKB +
+                             pg * box * C::ROWB;
+        tma_load_4d(dst, (lane & 1) ? tv : tk, bar, ch * C::CH, g.h,
+                    ps >= kStepKeys ? (tok0 & (ps - 1)) : 0, page);
+      }
+      ++count;
+      if (++st == a.stages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  }
+  return;
+drain:
+  // every copy lands before the CTA ends
+  if (lane == 0) {
+    for (int s = 0; s < a.stages; ++s)
+      if (count > (uint32_t)s) {
+        const uint32_t uses = (count - 1u - s) / a.stages + 1u;
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(full + 8u * s, (uses - 1u) & 1u))
+          if (globaltimer() - t0 > 2000000000ull) break;
+      }
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void step_barrier() {  // the computing warps
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
+}
+
+template <int D, int MT>
+__device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor c, uint32_t base,
+                             uint32_t full, uint32_t empty, float* red, StepMisc* m,
+                             const StepWait& wt) {
+  using C = StepCfg<D>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g8 = lane >> 2, t4 = lane & 3;
+  const int key0 = 16 * warp;  // this warp's keys of a block
+  // ldmatrix rows: K as (keys 0-7 | 8-15) x (channels 0-7 | 8-15), V likewise, transposed
+  const int mat = lane >> 3, mr = lane & 7;
+  const int k_row = key0 + (mat >> 1) * 8 + mr, k_col = mat & 1;
+  const int v_row = key0 + (mat & 1) * 8 + mr, v_col = mat >> 1;
+  int st = 0;
+  uint32_t ph = 0;
+  bool dead = false;  // the CTA gave up: run on without waits, store nothing
+  PagedSeg g;
+  while (c.next(a.p, w, &g)) {
+    uint32_t qf[MT][D / 16][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r0 = 16 * mt + g8, r1 = r0 + 8;
+      const long long row0 = g.seq.q0 + (long long)w.tile_rows * g.qt;
+      const uint16_t* x0 = a.q + (row0 + r0) * a.q_stride + (long long)g.h * D + 2 * t4;
+      const uint16_t* x1 = x0 + 8 * a.q_stride;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[mt][kk][0] = r0 < g.walk.rows ? *reinterpret_cast<const uint32_t*>(x0 + 16 * kk) : 0u;
+        qf[mt][kk][1] = r1 < g.walk.rows ? *reinterpret_cast<const uint32_t*>(x1 + 16 * kk) : 0u;
+        qf[mt][kk][2] = r0 < g.walk.rows ? *reinterpret_cast<const uint32_t*>(x0 + 16 * kk + 8) : 0u;
+        qf[mt][kk][3] = r1 < g.walk.rows ? *reinterpret_cast<const uint32_t*>(x1 + 16 * kk + 8) : 0u;
+      }
+    }
+    float o[MT][D / 8][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[mt][n][j] = 0.f;
+
+    for (int i = 0; i < g.n; ++i) {
+      const int kb = g.walk.block(g.i0 + i) << kStepShift;
+      if (!dead) dead = !__all_sync(0xffffffffu, step_wait(full + 8u * st, ph, wt, kSiteStepFull));
+      const uint32_t ks = base + st * C::STAGEB, vs = ks + C::TILEB;
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mt][n][j] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t kf[4];
+        ldsm4(ks + C::at(k_row, 2 * kk + k_col), kf);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816(s[mt][0], qf[mt][kk], kf[0], kf[1]);
+          mma16816(s[mt][1], qf[mt][kk], kf[2], kf[3]);
+        }
+      }
+      // p = silu(alpha S) = h + h tanh(h), h = alpha S / 2; as an A operand
+      // its columns are this thread's own score columns
+      const bool masked = kb + kStepKeys > g.walk.p0 + 1 || kb + kStepKeys > g.seq.hist;
+      uint32_t hi[MT][4], lo[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float p[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float x = s[mt][n][2 * r + j] * a.half_alpha;
+              p[j] = fmaf(x, tanh_approx(x), x);
+            }
+            if (masked) {
+              const int pos = g.walk.p0 + 16 * mt + 8 * r + g8;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int key = kb + key0 + 8 * n + 2 * t4 + j;
+                if (!(key <= pos && (key < g.seq.hist || key == pos))) p[j] = 0.f;
+              }
+            }
+            const uint32_t ph2 = pack_bf16x2(p[0], p[1]);
+            hi[mt][2 * n + r] = ph2;
+            lo[mt][2 * n + r] = pack_bf16x2(p[0] - __uint_as_float(ph2 << 16),
+                                            p[1] - __uint_as_float(ph2 & 0xffff0000u));
+          }
+      // values behind the last key any row sees may be anything, NaN too
+      const int live = g.walk.end() - kb - key0;  // of this warp's 16 keys
+      uint32_t m0 = ~0u, m1 = ~0u;
+      if (live < 16) {
+        const int k0 = 2 * t4;
+        m0 = (k0 < live ? 0xffffu : 0u) | (k0 + 1 < live ? 0xffff0000u : 0u);
+        m1 = (k0 + 8 < live ? 0xffffu : 0u) | (k0 + 9 < live ? 0xffff0000u : 0u);
+      }
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        uint32_t vf[4];
+        ldsm4_t(vs + C::at(v_row, 2 * n + v_col), vf);
+        if (live < 16) {
+          vf[0] &= m0;
+          vf[1] &= m1;
+          vf[2] &= m0;
+          vf[3] &= m1;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816(o[mt][2 * n], hi[mt], vf[0], vf[1]);
+          mma16816(o[mt][2 * n + 1], hi[mt], vf[2], vf[3]);
+          mma16816(o[mt][2 * n], lo[mt], vf[0], vf[1]);
+          mma16816(o[mt][2 * n + 1], lo[mt], vf[2], vf[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8u * st);
+      if (++st == a.stages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+
+    // the four warps' sums over their keys, then out or this CTA's part
+    const int rows = g.walk.rows;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = 16 * mt + 8 * r + g8;
+        if (row < rows) {
+          float* dst = red + (warp * a.red_rows + row) * D + 2 * t4;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[mt][n][2 * r], o[mt][n][2 * r + 1]);
+        }
+      }
+    step_barrier();
+    const bool stop = *static_cast<volatile int*>(&m->abort_flag) != 0;
+    const bool whole = g.parts == 1;
+    float* mine = a.parts + ((long long)blockIdx.x * 2 + (g.c0 == (int)blockIdx.x ? 1 : 0)) *
+                                (long long)(w.tile_rows * D);
+    uint16_t* out = a.out + ((g.seq.q0 + (long long)w.tile_rows * g.qt) * w.heads + g.h) * D;
+    const long long out_stride = (long long)w.heads * D;
+    for (int x = 2 * threadIdx.x; x < rows * D; x += 2 * 32 * kStepWarps) {
+      float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kStepWarps; ++i) {
+        const float2 y = *reinterpret_cast<const float2*>(red + i * a.red_rows * D + x);
+        v.x += y.x;
+        v.y += y.y;
+      }
+      if (stop) continue;
+      if (whole)
+        *reinterpret_cast<uint32_t*>(out + (x / D) * out_stride + x % D) =
+            pack_bf16x2(v.x * a.inv_n, v.y * a.inv_n);
+      else
+        __stcg(reinterpret_cast<float2*>(mine + x), v);
+    }
+    if (!whole) {
+      // the last CTA to arrive sums the parts in the CTAs' order, so the
+      // result does not depend on who is last
+      __threadfence();
+      step_barrier();
+      if (threadIdx.x == 0) {
+        m->last = !stop && atomicAdd(a.counters + g.c0, 1u) == (unsigned)(g.parts - 1);
+        if (m->last) a.counters[g.c0] = 0;  // ready for the next launch
+      }
+      step_barrier();
+      if (m->last) {
+        __threadfence();
+        for (int x = 2 * threadIdx.x; x < rows * D; x += 2 * 32 * kStepWarps) {
+          float2 v = make_float2(0.f, 0.f);
+          for (int i = 0; i < g.parts; ++i) {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(
+                a.parts + ((long long)(g.c0 + i) * 2 + (i == 0 ? 1 : 0)) * (long long)(w.tile_rows * D) + x));
+            v.x += y.x;
+            v.y += y.y;
+          }
+          *reinterpret_cast<uint32_t*>(out + (x / D) * out_stride + x % D) =
+              pack_bf16x2(v.x * a.inv_n, v.y * a.inv_n);
+        }
+      }
+    }
+    step_barrier();  // red is free for the next item
+  }
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kStepThreads)
+    step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                const StepArgs a) {
+  using C = StepCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* tail = smem_raw + (base - raw) + a.stages * C::STAGEB;
+  float* red = reinterpret_cast<float*>(tail);
+  uint8_t* after = tail + step_red_bytes(a.red_rows, D);
+  const uint32_t full = smem_u32(after), empty = full + 8u * C::MAX_STAGES;
+  StepMisc* m = reinterpret_cast<StepMisc*>(after + 2 * C::MAX_STAGES * 8);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(full + 8u * i, 1);
+      mbar_init(empty + 8u * i, kStepWarps);
+    }
+    m->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (threadIdx.x == 32 * kStepWarps) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tk)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tv)) : "memory");
+  }
+  PagedWork w = a.w;
+  PagedCursor c;
+  if (!step_locate(a, w, &c, m)) return;
+  const StepWait wt{a.timeout_ns, &m->abort_flag, a.status};
+  if (warp == kStepWarps)
+    step_produce<D>(&tk, &tv, a, w, c, base, full, empty, wt);
+  else
+    step_compute<D, MT>(a, w, c, base, full, empty, red, m, wt);
+}
+
+template <int D, int MT>
+cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, StepArgs a, int sms,
+                        cudaStream_t stream) {
+  using C = StepCfg<D>;
+  // two CTAs an SM share its 227 KB where the sums leave room for 3 stages each
+  const int extra = step_red_bytes(a.red_rows, D) + kStepTailBytes + 1024;
+  const int half = 113 * 1024, whole = 227 * 1024;
+  int per_sm = 2, stages = (half - extra) / C::STAGEB;
+  if (stages < 3) {
+    per_sm = 1;
+    stages = (whole - extra) / C::STAGEB;
+  }
+  a.stages = std::min(stages, (int)C::MAX_STAGES);
+  const int bytes = a.stages * C::STAGEB + extra;
+  const long long most = (long long)a.w.tiles * a.p.batch * a.w.heads *
+                         (((long long)a.p.max_pages << a.p.page_shift) / kStepKeys + 2);
+  const int grid = (int)std::min<long long>((long long)per_sm * sms,
+                                            (most + a.min_units - 1) / a.min_units);
+  const cudaError_t e = cudaFuncSetAttribute(step_kernel<D, MT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  step_kernel<D, MT><<<grid, kStepThreads, bytes, stream>>>(tk, tv, a);
+  return cudaGetLastError();
+}
+
+template <int MT>
+cudaError_t launch_step_d(int d, const CUtensorMap& tk, const CUtensorMap& tv, const StepArgs& a, int sms,
+                          cudaStream_t s) {
+  switch (d) {
+    case 32: return launch_step<32, MT>(tk, tv, a, sms, s);
+    case 64: return launch_step<64, MT>(tk, tv, a, sms, s);
+    default: return launch_step<128, MT>(tk, tv, a, sms, s);
+  }
+}
+
+int status_of(cudaError_t e) {
+  if (e == cudaErrorNoKernelImageForDevice || e == cudaErrorInvalidDeviceFunction)
+    return HSTU_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+bool bad_ptr(const void* p, unsigned align) {
+  return !p || (reinterpret_cast<uintptr_t>(p) & (align - 1u));
+}
+
+// The pool as (d, heads, page_size, num_pages) with box (min(d, 64), 1,
+// min(page_size, rows), 1) and the swizzle of a box row.
+int make_pool_map(CUtensorMap* m, void* ptr, int num_pages, int page_size, int heads, int d,
+                  long long page_stride, int rows) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)page_size,
+                              (cuuint64_t)num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)d * 2u, (cuuint64_t)heads * (cuuint64_t)d * 2u,
+                                 (cuuint64_t)page_stride * 2u};
+  const cuuint32_t box[4] = {(cuuint32_t)std::min(d, 64), 1u, (cuuint32_t)std::min(page_size, rows), 1u};
+  return host_encode_map(m, ptr, 4, dims, strides, box, d >= 64);
+}
+
+}  // namespace
+}  // namespace hstu
+
+// One pool of pages with its tensor maps; immutable after creation.
+struct hstu_cache {
+  void *k_pages, *v_pages;
+  int num_pages, page_size, page_shift, heads, d;
+  long long page_stride;
+  int device, sms;
+  unsigned* status;
+  CUtensorMap tk, tv;  // 64-row boxes
+};
+
+namespace {
+
+using hstu::PagedView;
+
+constexpr long long kCounterBytes = 8192;  // one counter a CTA, rounded up
+
+// CTAs of a launch, at most.
+int step_grid_most(int sms) { return 2 * sms; }
+long long part_bytes(const hstu_cache* c) {
+  return (long long)step_grid_most(c->sms) * 2 * 32 * c->d * (long long)sizeof(float);
+}
+size_t workspace_bytes(const hstu_cache* c) { return (size_t)(kCounterBytes + part_bytes(c)); }
+
+// The batch's fields, and (host) the view the kernels take.
+int check_batch(const hstu_paged_batch* b, PagedView* v, int num_pages, int page_shift) {
+  if (!b || b->batch < 0 || b->rows < 0 || b->max_q < 0 || b->max_pages < 0) return HSTU_ERR_INVALID_ARG;
+  if (b->batch > 0 && b->rows > 0 &&
+      (hstu::bad_ptr(b->q_offsets, 4) || hstu::bad_ptr(b->kv_lens, 4) || hstu::bad_ptr(b->page_table, 4) ||
+       (b->num_targets && hstu::bad_ptr(b->num_targets, 4)) || b->max_pages < 1))
+    return HSTU_ERR_INVALID_ARG;
+  // token positions are 32-bit
+  if (((long long)b->max_pages << page_shift) > (1LL << 30)) return HSTU_ERR_INVALID_ARG;
+  *v = PagedView{b->q_offsets, b->kv_lens, b->num_targets, b->page_table, b->batch, b->max_pages,
+                 b->max_q, b->rows, num_pages, page_shift};
+  return HSTU_OK;
+}
+
+int check_geometry(int num_pages, int page_size, int* shift) {
+  if (num_pages < 1 || page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)))
+    return HSTU_ERR_INVALID_ARG;
+  *shift = 0;
+  while ((1 << *shift) < page_size) ++*shift;
+  return HSTU_OK;
+}
+
+bool bad_rows(const void* p, int64_t stride, long long width) {
+  return hstu::bad_ptr(p, 16) || stride < width || (stride & 7);
+}
+
+int check_device(const hstu_cache* c) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return HSTU_ERR_CUDA;
+  return dev == c->device ? HSTU_OK : HSTU_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hstu_cache_create(void* k_pages, void* v_pages, int num_pages, int page_size, int heads, int d,
+                      int64_t page_stride, hstu_cache** cache) {
+  if (!cache) return HSTU_ERR_INVALID_ARG;
+  *cache = nullptr;
+  if (d != 32 && d != 64 && d != 128) return HSTU_ERR_UNSUPPORTED;
+  int shift = 0;
+  if (heads < 1 || heads > (1 << 16) || check_geometry(num_pages, page_size, &shift) != HSTU_OK)
+    return HSTU_ERR_INVALID_ARG;
+  const long long packed = (long long)page_size * heads * d;
+  if (page_stride == 0) page_stride = packed;
+  if (hstu::bad_ptr(k_pages, 16) || hstu::bad_ptr(v_pages, 16) || page_stride < packed ||
+      (page_stride & 7) || page_stride >= (1LL << 39))
+    return HSTU_ERR_INVALID_ARG;
+  hstu_cache* c = new (std::nothrow) hstu_cache{};
+  if (!c) return HSTU_ERR_NO_MEMORY;
+  c->k_pages = k_pages;
+  c->v_pages = v_pages;
+  c->num_pages = num_pages;
+  c->page_size = page_size;
+  c->page_shift = shift;
+  c->heads = heads;
+  c->d = d;
+  c->page_stride = page_stride;
+  int rc = hstu::host_device_check(&c->sms);
+  if (rc == HSTU_OK && cudaGetDevice(&c->device) != cudaSuccess) rc = HSTU_ERR_CUDA;
+  if (rc == HSTU_OK && hstu::device_status_words(&c->status) != cudaSuccess) rc = HSTU_ERR_CUDA;
+  if (rc == HSTU_OK)
+    rc = hstu::make_pool_map(&c->tk, k_pages, num_pages, page_size, heads, d, page_stride,
+                             hstu::kStepKeys);
+  if (rc == HSTU_OK)
+    rc = hstu::make_pool_map(&c->tv, v_pages, num_pages, page_size, heads, d, page_stride,
+                             hstu::kStepKeys);
+  if (rc != HSTU_OK) {
+    delete c;
+    return rc;
+  }
+  *cache = c;
+  return HSTU_OK;
+}
+
+int hstu_cache_destroy(hstu_cache* cache) {
+  delete cache;
+  return HSTU_OK;
+}
+
+int hstu_cache_workspace(const hstu_cache* cache, size_t* bytes) {
+  if (!cache || !bytes) return HSTU_ERR_INVALID_ARG;
+  *bytes = workspace_bytes(cache);
+  return HSTU_OK;
+}
+
+int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page_size, int64_t* host_slot,
+                     int32_t* host_pos) {
+  int shift = 0;
+  if (check_geometry(num_pages, page_size, &shift) != HSTU_OK) return HSTU_ERR_INVALID_ARG;
+  PagedView v;
+  const int rc = check_batch(host_batch, &v, num_pages, shift);
+  if (rc != HSTU_OK) return rc;
+  if (v.rows > 0 && (!host_slot || !host_pos)) return HSTU_ERR_INVALID_ARG;
+  int bad = 0;
+  for (int t = 0; t < v.rows; ++t) {
+    host_slot[t] = -1;
+    host_pos[t] = -1;
+    if (v.batch == 0 || t >= v.q_offsets[v.batch]) continue;
+    const int b = hstu::paged_find(v, t);
+    hstu::PagedSeq s;
+    if (b < 0 || !hstu::paged_seq(v, b, &s)) {
+      bad = 1;
+      continue;
+    }
+    const int pos = s.kv - s.qn + (t - s.q0);
+    host_slot[t] = hstu::paged_slot(v, b, pos);
+    host_pos[t] = pos < s.hist ? pos : s.hist;
+    if (host_slot[t] < 0) bad = 1;
+  }
+  return bad ? HSTU_ERR_INVALID_ARG : HSTU_OK;
+}
+
+int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int page_size, int heads,
+                        int tile_rows, int block_keys, int grid, int min_units, int32_t* host_dst,
+                        int capacity, int* n_segments) {
+  int shift = 0;
+  if (check_geometry(num_pages, page_size, &shift) != HSTU_OK) return HSTU_ERR_INVALID_ARG;
+  if (!n_segments || heads < 1 || tile_rows < 1 || block_keys < 1 || (block_keys & (block_keys - 1)) ||
+      grid < 1 || min_units < 1 || capacity < 0)
+    return HSTU_ERR_INVALID_ARG;
+  PagedView v;
+  const int rc = check_batch(host_batch, &v, num_pages, shift);
+  if (rc != HSTU_OK) return rc;
+  hstu::PagedWork w{};
+  w.heads = heads;
+  w.tile_rows = tile_rows;
+  w.tiles = v.rows > 0 && v.batch > 0 ? (v.max_q + tile_rows - 1) / tile_rows : 0;
+  while ((1 << w.kb_shift) < block_keys) ++w.kb_shift;
+  auto units_of = [&](int e) -> long long {
+    hstu::PagedSeq s;
+    hstu::paged_seq(v, e % v.batch, &s);
+    return (long long)heads * hstu::paged_walk(s, e / v.batch, tile_rows, w.kb_shift).nb;
+  };
+  for (int e = 0; e < w.tiles * v.batch; ++e) w.total += units_of(e);
+  w.per = hstu::paged_share(w.total, grid, min_units);
+  int n = 0;
+  for (int cta = 0; cta < grid && cta * w.per < w.total; ++cta) {
+    hstu::PagedCursor c{};
+    c.u = cta * w.per;
+    c.u1 = std::min(c.u + w.per, w.total);
+    long long at = 0;
+    while (at + units_of(c.e) <= c.u) at += units_of(c.e++);
+    c.r = (int)(c.u - at);
+    hstu::PagedSeg g;
+    while (c.next(v, w, &g)) {
+      if (host_dst) {
+        if (n >= capacity) return HSTU_ERR_INVALID_ARG;
+        const int32_t x[8] = {cta, g.b, g.h, g.qt, g.i0, g.n, g.c0, g.parts};
+        std::copy(x, x + 8, host_dst + 8 * (size_t)n);
+      }
+      ++n;
+    }
+  }
+  *n_segments = n;
+  return HSTU_OK;
+}
+
+int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, const void* q,
+                      int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                      const hstu_rotary* rotary, void* q_out, hstu_stream_t stream) {
+  if (!cache) return HSTU_ERR_INVALID_ARG;
+  hstu::AppendArgs a{};
+  int rc = check_batch(batch, &a.p, cache->num_pages, cache->page_shift);
+  if (rc != HSTU_OK) return rc;
+  const int width = cache->heads * cache->d;
+  if (!q != !q_out) return HSTU_ERR_INVALID_ARG;
+  if (rotary && (hstu::bad_ptr(rotary->table, 16) || rotary->positions < 1 || rotary->dim < 16 ||
+                 rotary->dim > cache->d || (rotary->dim & 15) ||
+                 (rotary->pairs != 0 && rotary->pairs != 1)))
+    return HSTU_ERR_INVALID_ARG;
+  if (a.p.rows == 0 || a.p.batch == 0) return HSTU_OK;
+  if (bad_rows(k, k_stride, width) || bad_rows(v, v_stride, width)) return HSTU_ERR_INVALID_ARG;
+  if (q && (bad_rows(q, q_stride, width) || hstu::bad_ptr(q_out, 16))) return HSTU_ERR_INVALID_ARG;
+  if ((rc = check_device(cache)) != HSTU_OK) return rc;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.k_pages = static_cast<uint16_t*>(cache->k_pages);
+  a.v_pages = static_cast<uint16_t*>(cache->v_pages);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.page_stride = cache->page_stride;
+  a.table = rotary ? rotary->table : nullptr;
+  a.positions = rotary ? rotary->positions : 0;
+  a.rot = rotary ? rotary->dim : 0;
+  a.pairs = rotary ? rotary->pairs : 0;
+  a.heads = cache->heads;
+  a.d = cache->d;
+  a.status = cache->status;
+  const long long units = (long long)a.p.rows * (width / 16);
+  const long long grid = (units + hstu::kAppendThreads - 1) / hstu::kAppendThreads;
+  if (grid > 0x7fffffffLL) return HSTU_ERR_INVALID_ARG;
+  hstu::append_kernel<<<(unsigned)grid, hstu::kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return hstu::status_of(cudaGetLastError());
+}
+
+int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, const void* q,
+                        int64_t q_stride, float alpha, float inv_n, void* out, void* workspace,
+                        hstu_stream_t stream) {
+  if (!cache) return HSTU_ERR_INVALID_ARG;
+  hstu::StepArgs a{};
+  int rc = check_batch(batch, &a.p, cache->num_pages, cache->page_shift);
+  if (rc != HSTU_OK) return rc;
+  if (workspace && hstu::bad_ptr(workspace, 16)) return HSTU_ERR_INVALID_ARG;
+  if (a.p.rows == 0 || a.p.batch == 0 || a.p.max_q == 0) return HSTU_OK;
+  const int width = cache->heads * cache->d;
+  if (bad_rows(q, q_stride, width) || hstu::bad_ptr(out, 16)) return HSTU_ERR_INVALID_ARG;
+  if ((rc = check_device(cache)) != HSTU_OK) return rc;
+  const int mt = a.p.max_q <= 16 ? 1 : 2;
+  a.w.heads = cache->heads;
+  a.w.tile_rows = 16 * mt;
+  a.w.tiles = (a.p.max_q + a.w.tile_rows - 1) / a.w.tile_rows;
+  a.w.kb_shift = hstu::kStepShift;
+  // a unit's index within an entry is 32-bit
+  const long long blocks = (((long long)a.p.max_pages << cache->page_shift) >> hstu::kStepShift) + 2;
+  if (blocks * cache->heads > 0x7fffffffLL || (long long)a.w.tiles * a.p.batch > 0x7fffffffLL)
+    return HSTU_ERR_INVALID_ARG;
+  a.min_units = 4;
+  a.red_rows = std::min(a.p.max_q, a.w.tile_rows);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.out = static_cast<uint16_t*>(out);
+  a.half_alpha = 0.5f * alpha;
+  a.inv_n = inv_n;
+  a.status = cache->status;
+  a.timeout_ns = hstu::host_wait_timeout_ns();
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char* own = nullptr;
+  if (!workspace) {
+    cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&own), workspace_bytes(cache), s);
+    if (e != cudaSuccess) return e == cudaErrorMemoryAllocation ? HSTU_ERR_NO_MEMORY : HSTU_ERR_CUDA;
+    if (cudaMemsetAsync(own, 0, (size_t)kCounterBytes, s) != cudaSuccess) {
+      cudaFreeAsync(own, s);
+      return HSTU_ERR_CUDA;
+    }
+    workspace = own;
+  }
+  a.counters = static_cast<unsigned*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
+  rc = hstu::status_of(mt == 1 ? hstu::launch_step_d<1>(cache->d, cache->tk, cache->tv, a, cache->sms, s)
+                               : hstu::launch_step_d<2>(cache->d, cache->tk, cache->tv, a, cache->sms, s));
+  if (own && cudaFreeAsync(own, s) != cudaSuccess && rc == HSTU_OK) rc = HSTU_ERR_CUDA;
+  return rc;
+}
+
+}  // extern "C"

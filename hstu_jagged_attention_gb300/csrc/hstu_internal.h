@@ -178,8 +178,23 @@ void fill_pairs(const int32_t* off, int batch, int heads, Item* dst);
 // first wait that gave up; read and cleared together.
 cudaError_t read_and_clear_device_status(unsigned* status, unsigned* site);
 
-// Host helpers defined in hstu_api.cpp (argument checks and the launch),
-// shared with hstu_noalloc.cu.
+// Bits of the status word, and the words' device address (the word, then
+// the site of the first wait that gave up) on the current device.
+constexpr unsigned kStatusTimeout = 1u;
+constexpr unsigned kStatusBadPaged = 2u;
+cudaError_t device_status_words(unsigned** words);
+// Wait sites of the cache's attention kernels (see device_status_words).
+constexpr int kSiteStepFull = 32, kSiteStepEmpty = 33;
+
+// Host helpers defined in hstu_api.cpp, shared with the other translation
+// units: argument checks, the launch, and (the current device's SMs) the
+// check that it is an sm_103.
+int host_device_check(int* sm_count);
+unsigned long long host_wait_timeout_ns();
+// A bf16 tensor map of `rank` dimensions with the 128-byte (wide) or 64-byte
+// swizzle.
+int host_encode_map(CUtensorMap* m, void* ptr, int rank, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box, bool wide);
 int host_check_offsets(const int32_t* off, int batch, long long max_len);
 int host_check_buffers(const void* q, const void* k, const void* v, const void* out);
 int host_launch(const Item* d_items, const int32_t* d_hist, int n_items, long long total, int heads,

@@ -46,6 +46,7 @@
 #ifndef HSTU_ATTN_H_
 #define HSTU_ATTN_H_
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -565,6 +566,234 @@ int hstu_attn_bwd_plan_ex(const hstu_plan* plan, const void* q, const void* k, c
                           void* dk, void* dv, float* dpos, float* dtime, hstu_stream_t stream);
 
 /*
+ * The paged K/V cache -- HSTU paper section 3.4 (M-FALCON): the history's
+ * keys and values are computed once, cached, and serve every microbatch of
+ * candidates.  Here they live in a pool of pages, so that histories grow
+ * without being moved, and each step appends its new tokens and attends
+ * from them.  No page defines the cache's layout; this is the library's own:
+ *
+ *   k_pages, v_pages  bf16 (num_pages, page_size, heads, d), the last three
+ *                     dimensions packed, pages page_stride elements apart
+ *                     (K and V pages may interleave in one buffer);
+ *   token p of sequence b is row p % page_size of page
+ *   page_table[b][p / page_size].
+ *
+ * hstu_cache_create  describes a pool the caller owns (on the current
+ *   device) and encodes its tensor maps; nothing is read or written, and the
+ *   handle is immutable: any number of streams may use it.
+ *   k_pages, v_pages  device, 16-byte aligned.
+ *   num_pages         >= 1.
+ *   page_size         a power of two, 16 .. 4096.
+ *   heads, d          heads in 1 .. 65536; d = 32, 64 or 128.
+ *   page_stride       elements, a multiple of 8, >= page_size * heads * d;
+ *                     0: packed.
+ * hstu_cache_destroy frees the handle, not the pool.  NULL is accepted.
+ * Errors: HSTU_ERR_INVALID_ARG, HSTU_ERR_UNSUPPORTED, HSTU_ERR_CUDA,
+ * HSTU_ERR_NO_MEMORY.
+ */
+typedef struct hstu_cache hstu_cache;
+int hstu_cache_create(void* k_pages, void* v_pages, int num_pages, int page_size, int heads, int d,
+                      int64_t page_stride, hstu_cache** cache);
+int hstu_cache_destroy(hstu_cache* cache);
+
+/*
+ * hstu_paged_batch -- a batch of new tokens against a cache.  The arrays are
+ * device memory (4-byte aligned) and are read by the kernels when they run,
+ * never by the host: a captured call replays with the lengths and pages that
+ * the arrays hold then.
+ *
+ *   q_offsets    int32[batch+1]: sequence b's new tokens are rows
+ *                q_offsets[b] .. q_offsets[b+1]-1 of q, k, v and out (none:
+ *                equal offsets).
+ *   kv_lens      int32[batch]: tokens of the sequence in the cache, the new
+ *                ones included.  New token i stands at position
+ *                kv_lens[b] - n_b + i (n_b new tokens).
+ *   num_targets  int32[batch] or NULL: the last num_targets[b] new tokens are
+ *                candidates, which see one another's neither keys nor values
+ *                (as hstu_attn_fwd_targets); hist = kv_lens[b] - num_targets[b].
+ *   page_table   int32[batch][max_pages]; entries past a sequence's last page
+ *                are not read.
+ *   max_q        upper bound on every n_b: it chooses the kernel's tiling.
+ *   rows         rows that q, k, v and out have.  Rows at or past
+ *                q_offsets[batch] (a padded batch) are neither read nor
+ *                written as tokens.
+ *
+ * What the device finds wrong is skipped and reported by hstu_last_status
+ * as HSTU_ERR_INVALID_ARG:
+ *   - a sequence whose offsets decrease or leave [0, rows], with n_b > max_q,
+ *     kv_lens[b] < n_b, more tokens than max_pages pages hold, or
+ *     num_targets[b] outside [0, n_b]: none of its rows is written;
+ *   - a page number outside [0, num_pages): an append there is dropped, and
+ *     the attention reads the page as zeros (its keys add nothing).
+ * max_pages * page_size is at most 2^30.
+ */
+typedef struct hstu_paged_batch {
+  const int32_t* q_offsets;
+  const int32_t* kv_lens;
+  const int32_t* num_targets;
+  const int32_t* page_table;
+  int batch;
+  int max_pages;
+  int max_q;
+  int rows;
+} hstu_paged_batch;
+
+/*
+ * hstu_cache_slots -- where each row of a batch goes, on the host only (no
+ * CUDA call; the batch's arrays are host memory): host_slot[t] = the pool row
+ * (page * page_size + row in page) of token row t and host_pos[t] the
+ * position its rotation uses, both -1 for a row behind the last sequence,
+ * of a skipped sequence, or (the slot) with a page out of range.  The kernels use the same
+ * arithmetic.  host_slot, host_pos: `rows` entries.  Returns
+ * HSTU_ERR_INVALID_ARG, with the arrays written, when the device would
+ * report the batch, and without them on an argument error.
+ */
+int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page_size,
+                     int64_t* host_slot, int32_t* host_pos);
+
+/*
+ * hstu_cache_worklist -- the shares of work hstu_attn_fwd_cache gives its
+ * CTAs, on the host only (no CUDA call; the batch's arrays are host memory).
+ * A unit is one block of block_keys keys of one (tile of tile_rows new
+ * tokens, sequence, head); units are numbered with tiles outermost, then
+ * sequences, heads and the blocks a tile walks: those with a key before
+ * hist that its last row may see, then its own keys' other blocks.  CTA c of
+ * `grid` takes units [c per, (c + 1) per), per = max(ceil(units / grid),
+ * min_units).  Segment i of host_dst is eight numbers: (CTA, sequence, head,
+ * tile, index of its first block in the walk, blocks, first CTA of the item,
+ * CTAs that share the item).  tile_rows >= 1, block_keys a power of two.
+ *   capacity    segments host_dst holds; NULL host_dst: count only.
+ *   *n_segments receives their number.
+ * Errors: HSTU_ERR_INVALID_ARG for bad arguments or a short capacity.
+ */
+int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int page_size, int heads,
+                        int tile_rows, int block_keys, int grid, int min_units, int32_t* host_dst,
+                        int capacity, int* n_segments);
+
+/*
+ * hstu_cache_append -- write the new tokens' keys and values into the cache,
+ * rotating keys (and queries) by their position on the way.
+ *
+ *   k, v    bf16 device (rows, heads, d), rows k_stride / v_stride elements
+ *           apart (slices of a fused projection need no copy): 16-byte
+ *           aligned, strides multiples of 8 and >= heads * d.
+ *   q       NULL, or likewise; q_out then receives the rotated queries, bf16
+ *           (rows, heads, d) packed.  q_out may be q when that is packed.
+ *   rotary  NULL: keys and queries are copied as they are.  Else, with
+ *           angle a(p, i) of position p and pair i,
+ *             x' = x cos a - y sin a,   y' = y cos a + x sin a
+ *           for the dim / 2 pairs (x, y) of the first dim channels of every
+ *           head: channels (i, dim / 2 + i), or with pairs = 1 channels
+ *           (2 i, 2 i + 1).  The others are copied.
+ *   rotary.table  fp32 device (positions, dim), 16-byte aligned: row p holds
+ *           the dim / 2 cosines of position p, then its sines.  dim: a
+ *           multiple of 16, <= d.
+ * A token is rotated at its position, a candidate at hist (each candidate
+ * stands right behind the history, as in its own causal pass), and products
+ * are taken in fp32 and rounded once to bf16.  A token whose position is not
+ * in the table is skipped and reported like a page out of range.  The slots
+ * of a call must differ from one another.
+ * Enqueues one kernel and allocates nothing.
+ */
+typedef struct hstu_rotary {
+  const float* table;
+  int positions;
+  int dim;
+  int pairs;
+} hstu_rotary;
+int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, const void* q,
+                      int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, const hstu_rotary* rotary, void* q_out, hstu_stream_t stream);
+
+/*
+ * hstu_attn_fwd_cache -- the attention of the new tokens over the cache,
+ * which already holds their own keys and values (hstu_cache_append first):
+ *
+ *   out[t,h,:] = inv_n * sum_j silu(alpha * <q[t,h,:], K_b[j,h,:]>) * V_b[j,h,:]
+ *
+ * over the cache rows j of t's sequence with j <= p(t) and, for candidates,
+ * (j < hist or j = p(t)).  A single new token per sequence is a decode step;
+ * all new tokens candidates is M-FALCON's microbatch; an empty cache filled
+ * by the call's own append is hstu_attn_fwd.  Precision as hstu_attn_fwd.
+ * The rows behind a sequence's end in its last page may hold anything (NaN
+ * included); within a sequence, keys and values are taken finite.
+ *
+ *   q          bf16 device (rows, heads, d), rows q_stride elements apart
+ *              (16-byte aligned, a multiple of 8).
+ *   out        bf16 device (rows, heads, d) packed; written for the rows of
+ *              the sequences only.
+ *   workspace  device memory of hstu_cache_workspace bytes, 16-byte aligned,
+ *              zeroed once before its first use: calls leave it ready for the
+ *              next.  One call at a time may use it: give each stream, and
+ *              each captured graph that may run beside another, its own, and
+ *              zero it again after a call ended in HSTU_ERR_TIMEOUT.  NULL: a
+ *              stream-ordered allocation.
+ * The keys are split evenly over the GPU's SMs; a row's parts are summed in
+ * a fixed order, so results repeat bit for bit.
+ * Errors: HSTU_ERR_INVALID_ARG (also for a cache of another device than the
+ * current one), HSTU_ERR_CUDA, HSTU_ERR_NO_MEMORY.
+ */
+int hstu_cache_workspace(const hstu_cache* cache, size_t* bytes);
+int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, const void* q,
+                        int64_t q_stride, float alpha, float inv_n, void* out, void* workspace,
+                        hstu_stream_t stream);
+
+/*
+ * Layer norm with the residual before it and the gate after it, forward and
+ * backward -- HSTU paper section 3: a layer is a residual around its
+ * sub-layers, and its pointwise transformation takes Norm(A V) (.) U.  The
+ * output stage of hstu_attn_fwd_norm_gate is fused behind that attention;
+ * these serve the attention over the cache, training (the gradient of the
+ * output stage), and the norm at a layer's entry.  Per row of `width` values:
+ *
+ *   z = residual + scale * x   (or z = x without residual)
+ *   y = ((z - mean) / sqrt(var + eps) * gamma + beta) (.) u   (or without u)
+ *
+ * with biased variance, in fp32 (z is not rounded in between).
+ *
+ *   x, residual, u  bf16 device, rows x_stride / ... elements apart: 16-byte
+ *              aligned, strides multiples of 8 and >= width.  residual and u
+ *              may be NULL.
+ *   gamma, beta  fp32 device, width entries, 16-byte aligned.
+ *   y          bf16 (rows, width) packed, written; may be x if that is packed.
+ *   z          bf16 (rows, width) packed, written: the new residual stream;
+ *              given exactly when residual is; may be residual or x if packed.
+ *   width      a multiple of 8, 8 .. HSTU_NORM_MAX_WIDTH.
+ *   scale      finite; used with residual.
+ *
+ * hstu_norm_bwd  for dy, with z the norm's input (x without residual), as
+ * stored, and g = dy (.) u, xhat the normalised row:
+ *
+ *   du = dy (.) (xhat gamma + beta),  dgamma = sum g xhat,  dbeta = sum g
+ *   dz = rstd (g gamma - mean(g gamma) - xhat mean(g gamma xhat)) + dz_in
+ *   dx = scale dz
+ *
+ *   dy, z, u, dz_in  as the forward's inputs; u, dz_in may be NULL.  dz_in:
+ *              the gradient that reaches z past the norm.
+ *   dz         bf16 (rows, width) packed: the gradient of z, so of the
+ *              residual too (of x without one).  May be dy if that is packed.
+ *   dx         NULL, or bf16 (rows, width) packed: scale * dz, rounded once.
+ *   du         bf16, rows du_stride apart; given exactly when u is.
+ *   dgamma, dbeta  fp32 device, width entries, overwritten (zeroed when rows
+ *              is 0); summed in a fixed order, so they repeat bit for bit.
+ *   workspace  device memory of hstu_norm_bwd_workspace bytes, 16-byte
+ *              aligned, its contents irrelevant; one call at a time.  NULL:
+ *              a stream-ordered allocation.
+ * Errors: HSTU_ERR_INVALID_ARG, HSTU_ERR_UNSUPPORTED (the device),
+ * HSTU_ERR_CUDA, HSTU_ERR_NO_MEMORY.
+ */
+#define HSTU_NORM_MAX_WIDTH 8192
+int hstu_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                  float scale, const void* u, int64_t u_stride, const float* gamma, const float* beta,
+                  float eps, int64_t rows, int width, void* y, void* z, hstu_stream_t stream);
+int hstu_norm_bwd_workspace(int width, size_t* bytes);
+int hstu_norm_bwd(const void* dy, int64_t dy_stride, const void* z, int64_t z_stride, const void* u,
+                  int64_t u_stride, const float* gamma, const float* beta, float eps,
+                  const void* dz_in, int64_t dz_in_stride, float scale, int64_t rows, int width,
+                  void* dz, void* dx, void* du, int64_t du_stride, float* dgamma, float* dbeta,
+                  void* workspace, hstu_stream_t stream);
+
+/*
  * hstu_launch_shape -- the grid the next launch for `plan` would use on the
  * current device: *grid persistent CTAs of *block threads with *smem_bytes
  * of dynamic shared memory.  Queries device attributes; launches nothing.
@@ -577,9 +806,10 @@ int hstu_launch_shape(const hstu_plan* plan, int* grid, int* block, int* smem_by
 /*
  * hstu_last_status -- read and clear the device-side status word of the
  * current device.  Synchronises the device.  *device_status receives
- * HSTU_OK, or HSTU_ERR_TIMEOUT if a kernel since the last call gave up on a
- * bounded wait; *site (may be NULL) receives an internal code of the first
- * wait that gave up (0 if none).  Kernels running concurrently share the
+ * HSTU_OK, HSTU_ERR_TIMEOUT if a kernel since the last call gave up on a
+ * bounded wait, or else HSTU_ERR_INVALID_ARG if one skipped a sequence, page
+ * or position out of range (see hstu_paged_batch); *site (may be NULL)
+ * receives an internal code of the first wait that gave up (0 if none).  Kernels running concurrently share the
  * word.
  */
 int hstu_last_status(int* device_status, int* site);
