@@ -676,50 +676,59 @@ def hstu_trace_read(capacity: int = 32768) -> np.ndarray:
 
 
 # ------------------------------------------------------- the paged K/V cache
-def _is(t, dtype: str, what: str):
-    if str(t.dtype) != "torch." + dtype:
-        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
-    return t
+# A decode step's kernels take a few microseconds, so these calls check their
+# tensors by comparing attributes and build nothing that they can keep.
+_torch = None
 
 
-def _on_gpu(t, device, what: str):
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
+def _load_torch():
+    global _torch, _bf16, _f32
+    import torch
+    _torch, _bf16, _f32 = torch, torch.bfloat16, torch.float32
 
 
 def _cuda_stream(stream, device):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream(device).cuda_stream or None
+        return _torch._C._cuda_getCurrentRawStream(device.index) or None
     return _stream(stream)
+
+
+def _refuse(t, dtype, shape, device, what: str):
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
 def _row_stride(t, shape, device, what: str) -> int:
     """Elements between rows of a bf16 device tensor of ``shape`` whose rows
     are packed (a slice of a wider projection has a larger row stride)."""
-    _is(t, "bfloat16", what)
-    _on_gpu(t, device, what)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
+    if t.dtype is not _bf16 or t.device != device or t.shape != shape:
+        _refuse(t, _bf16, shape, device, what)
     step, width = t.stride(), 1
-    for n, st in zip(shape[:0:-1], step[:0:-1]):
-        if n != 1 and st != width:
+    for i in range(len(shape) - 1, 0, -1):
+        if step[i] != width and shape[i] != 1:
             raise ValueError(f"{what}: the values of a row must be packed")
-        width *= n
+        width *= shape[i]
     return step[0] if shape[0] > 1 else max(step[0], width)
 
 
 def _packed(t, shape, device, what: str) -> int:
-    if _row_stride(t, shape, device, what) != _width(shape) and shape[0] > 1:
+    if t.dtype is not _bf16 or t.device != device or t.shape != shape:
+        _refuse(t, _bf16, shape, device, what)
+    if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
 
 
-def _width(shape) -> int:
-    w = 1
-    for n in shape[1:]:
-        w *= n
-    return w
+def _space(t, device, size: int, what: str):
+    if t is None:
+        return None
+    if t.device != device or not t.is_contiguous() or t.numel() * t.element_size() < size:
+        raise ValueError(f"{what} needs {size} contiguous bytes on {device}")
+    return t.data_ptr()
 
 
 class Cache:
@@ -729,6 +738,9 @@ class Cache:
         self.handle, self.k_pages, self.v_pages = handle, k_pages, v_pages
         self.num_pages, self.page_size, self.heads, self.d = (int(n) for n in k_pages.shape)
         self.device = k_pages.device
+        n = ctypes.c_size_t()
+        _check(lib().hstu_cache_workspace(handle, ctypes.byref(n)), "hstu_cache_workspace")
+        self.workspace_bytes = n.value
 
     def __enter__(self):
         return self
@@ -772,21 +784,28 @@ class PagedBatch:
             if not self.host:
                 if not a.is_cuda:
                     raise ValueError(f"{name} must be a device tensor (or a numpy array)")
-                _on_gpu(a, self.device, name)
+                if a.device != self.device:
+                    raise ValueError(f"{name} is on {a.device}, not on {self.device}")
         self.keep, self.batch, self.max_q = arrays, batch, int(max_q)
         at = {n: (a.ctypes.data if self.host else a.data_ptr()) for n, a in arrays.items()}
         self._fields = (at["q_offsets"], at["kv_lens"], at.get("num_targets"), at["page_table"], batch,
                         shapes["page_table"][1], self.max_q)
+        self._structs = {}
 
     def struct(self, rows: int):
-        return ctypes.byref(_PagedBatch(*self._fields, int(rows)))
+        """A pointer to the C struct for tensors of ``rows`` rows."""
+        s = self._structs.get(rows)
+        if s is None:
+            s = self._structs[rows] = ctypes.byref(_PagedBatch(*self._fields, int(rows)))
+        return s
 
 
 def hstu_cache_create(k_pages, v_pages) -> Cache:
     """A cache over the pools ``k_pages`` and ``v_pages``: bf16 device tensors
     (num_pages, page_size, heads, d) with packed pages (pages may lie further
     apart, as in a pool that interleaves K and V)."""
-    shape = tuple(int(n) for n in k_pages.shape)
+    _load_torch()
+    shape = k_pages.shape
     if len(shape) != 4 or not k_pages.is_cuda:
         raise ValueError("k_pages must be a device tensor (num_pages, page_size, heads, d)")
     stride = _row_stride(k_pages, shape, k_pages.device, "k_pages")
@@ -806,9 +825,12 @@ def hstu_cache_destroy(cache: Cache) -> None:
 
 def hstu_cache_workspace_bytes(cache: Cache) -> int:
     """Bytes of a workspace for hstu_attn_fwd_cache (zero it once)."""
-    n = ctypes.c_size_t()
-    _check(lib().hstu_cache_workspace(cache.handle, ctypes.byref(n)), "hstu_cache_workspace")
-    return n.value
+    return cache.workspace_bytes
+
+
+def _batch_on(batch: PagedBatch, device):
+    if batch.device != device:
+        raise ValueError(f"the batch is on {batch.device or 'the host'}, not on {device}")
 
 
 def hstu_cache_append(cache: Cache, batch: PagedBatch, k, v, q=None, q_out=None, rotary=None,
@@ -818,24 +840,26 @@ def hstu_cache_append(cache: Cache, batch: PagedBatch, k, v, q=None, q_out=None,
     ``rotary``: fp32 (positions, dim) table, cosines then sines: keys (and
     ``q``, into ``q_out``) are rotated by their position on the way, channels
     i and dim / 2 + i together, or with ``rotary_pairs`` 2 i and 2 i + 1."""
-    shape = (int(k.shape[0]), cache.heads, cache.d)
-    _on_gpu(batch.keep["q_offsets"], cache.device, "the batch")
-    ks = _row_stride(k, shape, cache.device, "k")
-    vs = _row_stride(v, shape, cache.device, "v")
-    qs = 0 if q is None else _row_stride(q, shape, cache.device, "q")
-    qo = None if q_out is None else _packed(q_out, shape, cache.device, "q_out")
-    rot = None
+    dev, rows = cache.device, k.shape[0]
+    shape = (rows, cache.heads, cache.d)
+    _batch_on(batch, dev)
+    ks = _row_stride(k, shape, dev, "k")
+    vs = _row_stride(v, shape, dev, "v")
+    qa, qs, qo, rot = None, 0, None, None
+    if q is not None:
+        qa, qs = q.data_ptr(), _row_stride(q, shape, dev, "q")
+    if q_out is not None:
+        qo = _packed(q_out, shape, dev, "q_out")
     if rotary is not None:
-        _is(rotary, "float32", "rotary")
-        _on_gpu(rotary, cache.device, "rotary")
-        if rotary.ndim != 2 or not rotary.is_contiguous():
-            raise ValueError("rotary must be a contiguous (positions, dim) table")
-        rot = ctypes.byref(_Rotary(rotary.data_ptr(), int(rotary.shape[0]), int(rotary.shape[1]),
-                                   int(bool(rotary_pairs))))
-    _check(lib().hstu_cache_append(cache.handle, batch.struct(shape[0]),
-                                   None if q is None else q.data_ptr(), qs, k.data_ptr(), ks,
-                                   v.data_ptr(), vs, rot, qo, _cuda_stream(stream, cache.device)),
-           "hstu_cache_append")
+        if rotary.dtype is not _f32 or rotary.device != dev or rotary.ndim != 2 or \
+                not rotary.is_contiguous():
+            raise ValueError(f"rotary must be a contiguous fp32 (positions, dim) table on {dev}")
+        rot = ctypes.byref(_Rotary(rotary.data_ptr(), rotary.shape[0], rotary.shape[1],
+                                   1 if rotary_pairs else 0))
+    code = lib().hstu_cache_append(cache.handle, batch.struct(rows), qa, qs, k.data_ptr(), ks,
+                                   v.data_ptr(), vs, rot, qo, _cuda_stream(stream, dev))
+    if code:
+        _check(code, "hstu_cache_append")
 
 
 def hstu_attn_fwd_cache(cache: Cache, batch: PagedBatch, q, alpha: float, inv_n: float, out,
@@ -844,20 +868,16 @@ def hstu_attn_fwd_cache(cache: Cache, batch: PagedBatch, q, alpha: float, inv_n:
     which already holds their own keys and values, into ``out``.
     ``workspace``: a zeroed uint8 device tensor of hstu_cache_workspace_bytes,
     kept between calls (one call at a time); None allocates per call."""
-    shape = (int(q.shape[0]), cache.heads, cache.d)
-    _on_gpu(batch.keep["q_offsets"], cache.device, "the batch")
-    qs = _row_stride(q, shape, cache.device, "q")
-    o = _packed(out, shape, cache.device, "out")
-    ws = None
-    if workspace is not None:
-        _on_gpu(workspace, cache.device, "workspace")
-        if not workspace.is_contiguous() or \
-                workspace.numel() * workspace.element_size() < hstu_cache_workspace_bytes(cache):
-            raise ValueError("workspace needs hstu_cache_workspace_bytes contiguous bytes")
-        ws = workspace.data_ptr()
-    _check(lib().hstu_attn_fwd_cache(cache.handle, batch.struct(shape[0]), q.data_ptr(), qs, float(alpha),
-                                     float(inv_n), o, ws, _cuda_stream(stream, cache.device)),
-           "hstu_attn_fwd_cache")
+    dev, rows = cache.device, q.shape[0]
+    shape = (rows, cache.heads, cache.d)
+    _batch_on(batch, dev)
+    qs = _row_stride(q, shape, dev, "q")
+    o = _packed(out, shape, dev, "out")
+    ws = _space(workspace, dev, cache.workspace_bytes, "workspace")
+    code = lib().hstu_attn_fwd_cache(cache.handle, batch.struct(rows), q.data_ptr(), qs, alpha, inv_n, o,
+                                     ws, _cuda_stream(stream, dev))
+    if code:
+        _check(code, "hstu_attn_fwd_cache")
 
 
 def hstu_cache_slots(batch: PagedBatch, num_pages: int, page_size: int, rows: int):
@@ -893,11 +913,19 @@ def hstu_cache_worklist(batch: PagedBatch, num_pages: int, page_size: int, rows:
 
 # ------------------------------------------- layer norm, its gate and residual
 def _vector(t, width: int, device, what: str) -> int:
-    _is(t, "float32", what)
-    _on_gpu(t, device, what)
-    if tuple(t.shape) != (width,) or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous with {width} entries")
+    if t.dtype is not _f32 or t.device != device or t.shape != (width,):
+        _refuse(t, _f32, (width,), device, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
+
+
+def _rows_of(t, what: str):
+    if _torch is None:
+        _load_torch()
+    if t.ndim != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor (rows, width)")
+    return t.shape, t.device
 
 
 def hstu_norm_fwd(x, gamma, beta, eps: float, y, u=None, residual=None, scale: float = 1.0, z=None,
@@ -906,19 +934,21 @@ def hstu_norm_fwd(x, gamma, beta, eps: float, y, u=None, residual=None, scale: f
     ``residual``; then ``z`` is not given, else it receives the new residual
     stream).  x, u, residual, y, z: bf16 (rows, width), inputs with any row
     stride; gamma, beta: fp32 (width)."""
-    if x.ndim != 2 or not x.is_cuda:
-        raise ValueError("x must be a device tensor (rows, width)")
-    shape, dev = (int(x.shape[0]), int(x.shape[1])), x.device
+    shape, dev = _rows_of(x, "x")
+    rows, width = shape
     xs = _row_stride(x, shape, dev, "x")
-    us = 0 if u is None else _row_stride(u, shape, dev, "u")
-    rs = 0 if residual is None else _row_stride(residual, shape, dev, "residual")
-    _check(lib().hstu_norm_fwd(x.data_ptr(), xs, None if residual is None else residual.data_ptr(), rs,
-                               float(scale), None if u is None else u.data_ptr(), us,
-                               _vector(gamma, shape[1], dev, "gamma"),
-                               _vector(beta, shape[1], dev, "beta"), float(eps), shape[0], shape[1],
-                               _packed(y, shape, dev, "y"),
-                               None if z is None else _packed(z, shape, dev, "z"),
-                               _cuda_stream(stream, dev)), "hstu_norm_fwd")
+    ra, rs, ua, us, za = None, 0, None, 0, None
+    if residual is not None:
+        ra, rs = residual.data_ptr(), _row_stride(residual, shape, dev, "residual")
+    if u is not None:
+        ua, us = u.data_ptr(), _row_stride(u, shape, dev, "u")
+    if z is not None:
+        za = _packed(z, shape, dev, "z")
+    code = lib().hstu_norm_fwd(x.data_ptr(), xs, ra, rs, scale, ua, us, _vector(gamma, width, dev, "gamma"),
+                               _vector(beta, width, dev, "beta"), eps, rows, width,
+                               _packed(y, shape, dev, "y"), za, _cuda_stream(stream, dev))
+    if code:
+        _check(code, "hstu_norm_fwd")
 
 
 def hstu_norm_bwd_workspace_bytes(width: int) -> int:
@@ -934,25 +964,25 @@ def hstu_norm_bwd(dy, z, gamma, beta, eps: float, dz, dgamma, dbeta, u=None, du=
     (x without a residual; with one also the residual's gradient), with
     ``dz_in`` (the gradient reaching z past the norm) added; ``dx`` = scale
     dz; ``du`` of the gate ``u``; ``dgamma``, ``dbeta`` (fp32, overwritten)."""
-    if dy.ndim != 2 or not dy.is_cuda:
-        raise ValueError("dy must be a device tensor (rows, width)")
-    shape, dev = (int(dy.shape[0]), int(dy.shape[1])), dy.device
-
-    def at(t, what):
-        return (None, 0) if t is None else (t.data_ptr(), _row_stride(t, shape, dev, what))
-
-    ws = None
+    shape, dev = _rows_of(dy, "dy")
+    rows, width = shape
+    dys = _row_stride(dy, shape, dev, "dy")
+    zs = _row_stride(z, shape, dev, "z")
+    ua, us, dua, dus, da, ds, dxa, ws = None, 0, None, 0, None, 0, None, None
+    if u is not None:
+        ua, us = u.data_ptr(), _row_stride(u, shape, dev, "u")
+    if du is not None:
+        dua, dus = du.data_ptr(), _row_stride(du, shape, dev, "du")
+    if dz_in is not None:
+        da, ds = dz_in.data_ptr(), _row_stride(dz_in, shape, dev, "dz_in")
+    if dx is not None:
+        dxa = _packed(dx, shape, dev, "dx")
     if workspace is not None:
-        _on_gpu(workspace, dev, "workspace")
-        if not workspace.is_contiguous() or \
-                workspace.numel() * workspace.element_size() < hstu_norm_bwd_workspace_bytes(shape[1]):
-            raise ValueError("workspace needs hstu_norm_bwd_workspace_bytes contiguous bytes")
-        ws = workspace.data_ptr()
-    _check(lib().hstu_norm_bwd(*at(dy, "dy"), *at(z, "z"), *at(u, "u"),
-                               _vector(gamma, shape[1], dev, "gamma"),
-                               _vector(beta, shape[1], dev, "beta"), float(eps), *at(dz_in, "dz_in"),
-                               float(scale), shape[0], shape[1], _packed(dz, shape, dev, "dz"),
-                               None if dx is None else _packed(dx, shape, dev, "dx"), *at(du, "du"),
-                               _vector(dgamma, shape[1], dev, "dgamma"),
-                               _vector(dbeta, shape[1], dev, "dbeta"), ws, _cuda_stream(stream, dev)),
-           "hstu_norm_bwd")
+        ws = _space(workspace, dev, hstu_norm_bwd_workspace_bytes(width), "workspace")
+    code = lib().hstu_norm_bwd(dy.data_ptr(), dys, z.data_ptr(), zs, ua, us,
+                               _vector(gamma, width, dev, "gamma"), _vector(beta, width, dev, "beta"), eps,
+                               da, ds, scale, rows, width, _packed(dz, shape, dev, "dz"), dxa, dua, dus,
+                               _vector(dgamma, width, dev, "dgamma"), _vector(dbeta, width, dev, "dbeta"),
+                               ws, _cuda_stream(stream, dev))
+    if code:
+        _check(code, "hstu_norm_bwd")

@@ -19,8 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhstu.so")
 SOURCES = ["hstu_fwd.cu", "hstu_api.cpp", "hstu_noalloc.cu", "hstu_cache.cu", "hstu_norm.cu"]
-HEADERS = ["hstu_internal.h", "hstu_ptx.cuh", "hstu_paged.h", "hstu_bwd.cuh", "hstu_fwd_pair.cuh",
-           "hstu_bwd_t.cuh"]
+HEADERS = ["hstu_internal.h", "hstu_ptx.cuh", "hstu_paged.h", "hstu_paged.cuh",
+           "hstu_fwd_paged.cuh", "hstu_bwd.cuh", "hstu_fwd_pair.cuh", "hstu_bwd_t.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -525,6 +525,10 @@ long long schedule_items(const int32_t* cost, int n, int grid, int32_t* order, i
 
 int host_device_check(int* sm_count) { return device_check(sm_count); }
 unsigned long long host_wait_timeout_ns() { return wait_timeout_ns(); }
+unsigned host_debug_flags() {
+  std::lock_guard<std::mutex> lk(g_mu);
+  return g_debug_flags;
+}
 
 int host_encode_map(CUtensorMap* m, void* ptr, int rank, const cuuint64_t* dims,
                     const cuuint64_t* strides, const cuuint32_t* box, bool wide) {

@@ -18,7 +18,7 @@
 
 #include "hstu_attn.h"
 #include "hstu_internal.h"
-#include "hstu_paged.h"
+#include "hstu_paged.cuh"
 #include "hstu_ptx.cuh"
 
 namespace hstu {
@@ -212,15 +212,6 @@ __device__ __forceinline__ bool step_wait(uint32_t bar, uint32_t parity, const S
   }
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
-                                            int y, int z, int u) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
-      : "memory");
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -269,64 +260,9 @@ constexpr int kStepTailBytes = 2 * 16 * 8 + 64 + 16 * 8;
 struct StepMisc {
   int abort_flag;
   int last;   // this CTA arrived last at the item it shares
-  int e, r;   // where its share starts
-  long long sums[kStepWarps + 1];
+  PagedStart<kStepWarps + 1> start;
 };
 static_assert(sizeof(StepMisc) <= 64 + 16 * 8, "misc");
-
-// Totals the work over all threads of the CTA and finds where its share
-// starts; false (for all) when it has none.
-__device__ bool step_locate(const StepArgs& a, PagedWork& w, PagedCursor* c, StepMisc* m) {
-  const int n = w.tiles * a.p.batch;
-  const int each = (n + kStepThreads - 1) / kStepThreads;
-  const int e0 = threadIdx.x * each, e1 = e0 + each < n ? e0 + each : n;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long sum = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int qt = e / a.p.batch, b = e - qt * a.p.batch;
-    PagedSeq s;
-    if (!paged_seq(a.p, b, &s) && blockIdx.x == 0) atomicOr(a.status, kStatusBadPaged);
-    sum += (long long)w.heads * paged_walk(s, qt, w.tile_rows, w.kb_shift).nb;
-  }
-  long long incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) m->sums[warp] = incl;
-  __syncthreads();
-  long long before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i <= kStepWarps; ++i) {
-    if (i < warp) before += m->sums[i];
-    total += m->sums[i];
-  }
-  w.total = total;
-  w.per = paged_share(total, gridDim.x, a.min_units);
-  c->u = (long long)blockIdx.x * w.per;
-  if (c->u >= total) return false;
-  c->u1 = c->u + w.per < total ? c->u + w.per : total;
-  long long at = before + incl - sum;  // the thread's first unit
-  if (at <= c->u && c->u < at + sum) {
-    for (int e = e0; e < e1; ++e) {
-      const int qt = e / a.p.batch, b = e - qt * a.p.batch;
-      PagedSeq s;
-      paged_seq(a.p, b, &s);
-      const long long units = (long long)w.heads * paged_walk(s, qt, w.tile_rows, w.kb_shift).nb;
-      if (c->u < at + units) {
-        m->e = e;
-        m->r = (int)(c->u - at);
-        break;
-      }
-      at += units;
-    }
-  }
-  __syncthreads();
-  c->e = m->e;
-  c->r = m->r;
-  return true;
-}
 
 template <int D>
 __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const StepArgs& a,
@@ -343,25 +279,16 @@ __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const
     const int32_t* row = a.p.page_table + (long long)g.b * a.p.max_pages;
     const int end = g.walk.end();
     const int pages = (end + ps - 1) >> shift;  // of the sequence, as far as the tile sees
-    int first = -64;                             // the page ids at hand: first + lane, and 32 on
-    int ids = 0, ids2 = 0;
+    PageIds ids;
     for (int i = 0; i < g.n; ++i) {
       const int tok0 = g.walk.block(g.i0 + i) << kStepShift;
       const int p0 = tok0 >> shift;
       const int valid = end - tok0 < kStepKeys ? end - tok0 : kStepKeys;
       const int npg = ps >= kStepKeys ? 1 : (valid + ps - 1) >> shift;
-      if (p0 + npg > first + 32 || p0 < first) {
-        if (p0 == first + 32) {
-          ids = ids2;
-        } else {
-          ids = p0 + lane < pages ? __ldg(row + p0 + lane) : 0;
-        }
-        first = p0;
-        ids2 = p0 + 32 + lane < pages ? __ldg(row + p0 + 32 + lane) : 0;
-      }
+      ids.cover(row, p0, npg, pages);
       // lane: which page of the block, which chunk of channels, K or V
       const int pg = lane / (2 * C::NCH), ch = (lane >> 1) % C::NCH;
-      int page = __shfl_sync(0xffffffffu, ids, (p0 - first + pg) & 31);
+      int page = ids.get(p0 + pg);
       const uint32_t bar = full + 8u * st;
       if (!__all_sync(0xffffffffu, step_wait(empty + 8u * st, ph, wt, kSiteStepEmpty))) goto drain;
       if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(npg * box * C::ROWB * C::NCH * 2));
@@ -621,7 +548,7 @@ __global__ void __launch_bounds__(kStepThreads)
   }
   PagedWork w = a.w;
   PagedCursor c;
-  if (!step_locate(a, w, &c, m)) return;
+  if (!paged_locate(a.p, &w, a.min_units, &m->start, a.status, &c)) return;
   const StepWait wt{a.timeout_ns, &m->abort_flag, a.status};
   if (warp == kStepWarps)
     step_produce<D>(&tk, &tv, a, w, c, base, full, empty, wt);
@@ -696,7 +623,8 @@ struct hstu_cache {
   long long page_stride;
   int device, sms;
   unsigned* status;
-  CUtensorMap tk, tv;  // 64-row boxes
+  CUtensorMap tk, tv;            // 64-row boxes (a few new tokens)
+  CUtensorMap tk_tile, tv_tile;  // 128-row boxes (many)
 };
 
 namespace {
@@ -705,10 +633,9 @@ using hstu::PagedView;
 
 constexpr long long kCounterBytes = 8192;  // one counter a CTA, rounded up
 
-// CTAs of a launch, at most.
-int step_grid_most(int sms) { return 2 * sms; }
+// Two parts a CTA: 2 CTAs an SM with tiles of up to 32 rows, or one with 128.
 long long part_bytes(const hstu_cache* c) {
-  return (long long)step_grid_most(c->sms) * 2 * 32 * c->d * (long long)sizeof(float);
+  return (long long)c->sms * 2 * HSTU_BLOCK_M * c->d * (long long)sizeof(float);
 }
 size_t workspace_bytes(const hstu_cache* c) { return (size_t)(kCounterBytes + part_bytes(c)); }
 
@@ -780,6 +707,12 @@ int hstu_cache_create(void* k_pages, void* v_pages, int num_pages, int page_size
   if (rc == HSTU_OK)
     rc = hstu::make_pool_map(&c->tv, v_pages, num_pages, page_size, heads, d, page_stride,
                              hstu::kStepKeys);
+  if (rc == HSTU_OK)
+    rc = hstu::make_pool_map(&c->tk_tile, k_pages, num_pages, page_size, heads, d, page_stride,
+                             HSTU_BLOCK_N);
+  if (rc == HSTU_OK)
+    rc = hstu::make_pool_map(&c->tv_tile, v_pages, num_pages, page_size, heads, d, page_stride,
+                             HSTU_BLOCK_N);
   if (rc != HSTU_OK) {
     delete c;
     return rc;
@@ -852,6 +785,7 @@ int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int p
   int n = 0;
   for (int cta = 0; cta < grid && cta * w.per < w.total; ++cta) {
     hstu::PagedCursor c{};
+    c.at = -1;
     c.u = cta * w.per;
     c.u1 = std::min(c.u + w.per, w.total);
     long long at = 0;
@@ -916,33 +850,34 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
                         int64_t q_stride, float alpha, float inv_n, void* out, void* workspace,
                         hstu_stream_t stream) {
   if (!cache) return HSTU_ERR_INVALID_ARG;
-  hstu::StepArgs a{};
-  int rc = check_batch(batch, &a.p, cache->num_pages, cache->page_shift);
+  PagedView p;
+  int rc = check_batch(batch, &p, cache->num_pages, cache->page_shift);
   if (rc != HSTU_OK) return rc;
   if (workspace && hstu::bad_ptr(workspace, 16)) return HSTU_ERR_INVALID_ARG;
-  if (a.p.rows == 0 || a.p.batch == 0 || a.p.max_q == 0) return HSTU_OK;
-  const int width = cache->heads * cache->d;
-  if (bad_rows(q, q_stride, width) || hstu::bad_ptr(out, 16)) return HSTU_ERR_INVALID_ARG;
+  if (p.rows == 0 || p.batch == 0 || p.max_q == 0) return HSTU_OK;
+  const int heads = cache->heads, d = cache->d;
+  if (bad_rows(q, q_stride, (long long)heads * d) || hstu::bad_ptr(out, 16)) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_device(cache)) != HSTU_OK) return rc;
-  const int mt = a.p.max_q <= 16 ? 1 : 2;
-  a.w.heads = cache->heads;
-  a.w.tile_rows = 16 * mt;
-  a.w.tiles = (a.p.max_q + a.w.tile_rows - 1) / a.w.tile_rows;
-  a.w.kb_shift = hstu::kStepShift;
-  // a unit's index within an entry is 32-bit
-  const long long blocks = (((long long)a.p.max_pages << cache->page_shift) >> hstu::kStepShift) + 2;
-  if (blocks * cache->heads > 0x7fffffffLL || (long long)a.w.tiles * a.p.batch > 0x7fffffffLL)
+  hstu::PagedWork w{};
+  const bool tiled = p.max_q > 32;
+  w.heads = heads;
+  w.tile_rows = tiled ? HSTU_BLOCK_M : p.max_q > 16 ? 32 : 16;
+  w.tiles = (p.max_q + w.tile_rows - 1) / w.tile_rows;
+  w.kb_shift = tiled ? 7 : hstu::kStepShift;
+  // a unit's index within an entry, and an entry's, are 32-bit
+  const long long blocks = (((long long)p.max_pages << cache->page_shift) >> w.kb_shift) + 3;
+  if (blocks * heads > 0x7fffffffLL || (long long)w.tiles * p.batch > 0x7fffffffLL)
     return HSTU_ERR_INVALID_ARG;
-  a.min_units = 4;
-  a.red_rows = std::min(a.p.max_q, a.w.tile_rows);
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_stride = q_stride;
-  a.out = static_cast<uint16_t*>(out);
-  a.half_alpha = 0.5f * alpha;
-  a.inv_n = inv_n;
-  a.status = cache->status;
-  a.timeout_ns = hstu::host_wait_timeout_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  CUtensorMap tq;
+  if (tiled) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)p.rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2u, (cuuint64_t)q_stride * 2u};
+    const cuuint32_t box[3] = {(cuuint32_t)std::min(d, 64), 1u, (cuuint32_t)HSTU_BLOCK_M};
+    if (q_stride >= (1LL << 39)) return HSTU_ERR_INVALID_ARG;
+    if ((rc = hstu::host_encode_map(&tq, const_cast<void*>(q), 3, dims, strides, box, d >= 64)) != HSTU_OK)
+      return rc;
+  }
   char* own = nullptr;
   if (!workspace) {
     cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&own), workspace_bytes(cache), s);
@@ -953,10 +888,43 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     }
     workspace = own;
   }
-  a.counters = static_cast<unsigned*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
-  rc = hstu::status_of(mt == 1 ? hstu::launch_step_d<1>(cache->d, cache->tk, cache->tv, a, cache->sms, s)
-                               : hstu::launch_step_d<2>(cache->d, cache->tk, cache->tv, a, cache->sms, s));
+  unsigned* counters = static_cast<unsigned*>(workspace);
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
+  cudaError_t e;
+  if (tiled) {
+    hstu::PagedFwdArgs a{};
+    a.p = p;
+    a.w = w;
+    a.min_units = 4;
+    a.out = static_cast<uint16_t*>(out);
+    a.half_alpha = 0.5f * alpha;
+    a.inv_n = inv_n;
+    a.counters = counters;
+    a.parts = parts;
+    a.timeout_ns = hstu::host_wait_timeout_ns();
+    a.debug_flags = hstu::host_debug_flags();
+    const long long most = (long long)w.tiles * p.batch * heads * blocks;
+    const int grid = (int)std::min<long long>(cache->sms, (most + a.min_units - 1) / a.min_units);
+    e = hstu::launch_fwd_paged(d, tq, cache->tk_tile, cache->tv_tile, a, grid, s);
+  } else {
+    hstu::StepArgs a{};
+    a.p = p;
+    a.w = w;
+    a.min_units = 4;
+    a.red_rows = std::min(p.max_q, w.tile_rows);
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_stride = q_stride;
+    a.out = static_cast<uint16_t*>(out);
+    a.half_alpha = 0.5f * alpha;
+    a.inv_n = inv_n;
+    a.counters = counters;
+    a.parts = parts;
+    a.status = cache->status;
+    a.timeout_ns = hstu::host_wait_timeout_ns();
+    e = w.tile_rows == 16 ? hstu::launch_step_d<1>(d, cache->tk, cache->tv, a, cache->sms, s)
+                          : hstu::launch_step_d<2>(d, cache->tk, cache->tv, a, cache->sms, s);
+  }
+  rc = hstu::status_of(e);
   if (own && cudaFreeAsync(own, s) != cudaSuccess && rc == HSTU_OK) rc = HSTU_ERR_CUDA;
   return rc;
 }

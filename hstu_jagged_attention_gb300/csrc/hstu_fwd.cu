@@ -62,6 +62,7 @@
 #include <type_traits>
 
 #include "hstu_internal.h"
+#include "hstu_paged.cuh"
 #include "hstu_ptx.cuh"
 
 namespace hstu {
@@ -1305,6 +1306,7 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
 #include "hstu_bwd.cuh"
 #include "hstu_bwd_t.cuh"
 #include "hstu_fwd_pair.cuh"
+#include "hstu_fwd_paged.cuh"
 
 }  // namespace
 
@@ -1321,6 +1323,16 @@ cudaError_t launch_fwd_pairs(int d, const CUtensorMap& tq, const CUtensorMap& tk
   switch (d) {
     case 64: return launch_pair_d<64>(tq, tk, tv, a, grid, stream);
     case 128: return launch_pair_d<128>(tq, tk, tv, a, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_fwd_paged(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedFwdArgs& a, int grid, cudaStream_t stream) {
+  switch (d) {
+    case 32: return launch_paged_d<32>(tq, tk, tv, a, grid, stream);
+    case 64: return launch_paged_d<64>(tq, tk, tv, a, grid, stream);
+    case 128: return launch_paged_d<128>(tq, tk, tv, a, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -1,0 +1,533 @@
+// The attention of many new tokens over the paged cache, on tcgen05: the
+// roles and the TMEM layout of the forward kernel (hstu_fwd.cu), with
+//   - K and V blocks of 128 keys gathered page by page (one bulk-tensor copy
+//     a page and 64-channel chunk);
+//   - tiles of 128 new tokens at any position: the keys a row may see end
+//     anywhere in a block, and candidates see the history and themselves;
+//   - equal shares of (tile, sequence, head, key block) units per CTA, so an
+//     item may be cut between CTAs; its parts are summed in their order by
+//     the CTA that arrives last.
+// Included by hstu_fwd.cu.
+
+// A cursor over a CTA's key-block steps: block i of segment g (the it-th).
+struct PagedSteps {
+  PagedCursor c;
+  PagedSeg g;
+  int i, it;
+  uint32_t tc;
+  bool valid;
+  __device__ __forceinline__ void start(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from) {
+    c = from;
+    i = it = 0;
+    tc = 0;
+    valid = c.next(a.p, w, &g);
+  }
+  __device__ __forceinline__ void advance(const PagedFwdArgs& a, const PagedWork& w) {
+    ++tc;
+    if (++i == g.n) {
+      i = 0;
+      ++it;
+      valid = c.next(a.p, w, &g);
+    }
+  }
+  __device__ __forceinline__ bool last() const { return i == g.n - 1; }
+  __device__ __forceinline__ int key0() const { return kBN * g.walk.block(g.i0 + i); }
+  // Keys of the block that some row sees, up to the MMA's steps of 16.
+  __device__ __forceinline__ int cols() const {
+    const int r = g.walk.end() - key0();
+    return r >= kBN ? kBN : ((r + 15) & ~15);
+  }
+  // Every row sees every key of the block.
+  __device__ __forceinline__ bool plain() const {
+    const int e = key0() + kBN;
+    return e <= g.walk.p0 + 1 && e <= g.seq.hist;
+  }
+};
+
+// One warp: the K stream with each item's Q tile, or the V stream.
+template <int D, bool KQ>
+__device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, const PagedFwdArgs& a,
+                               const PagedWork& w, const PagedCursor& from, uint32_t base,
+                               const WaitCtx& wt) {
+  using C = Cfg<D>;
+  constexpr int FULL = KQ ? C::B_QKREADY : C::B_VFULL;
+  constexpr int OFF = KQ ? C::K_OFF : C::V_OFF;
+  const uint32_t bars = base + C::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  const int lane = threadIdx.x & 31;
+  const int shift = a.p.page_shift, ps = 1 << shift;
+  const int box = ps < kBN ? ps : kBN;
+  uint32_t c = 0, qc = 0;
+  bool ok = true;
+  PagedCursor cur = from;
+  PagedSeg g;
+  while (ok && cur.next(a.p, w, &g)) {
+    if (KQ) {
+      const int qs = (int)(qc % C::QS);
+      if (!(ok = wait_warp(bar(C::B_QEMPTY + qs), ((qc / C::QS) & 1u) ^ 1u, wt, kSiteQEmpty))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(C::B_QFULL + qs), C::TILEB);
+#pragma unroll
+        for (int ch = 0; ch < C::NCHUNK; ++ch)
+          tma_load_3d(base + C::Q_OFF + qs * C::TILEB + ch * C::CHUNKB, tm_q, bar(C::B_QFULL + qs),
+                      ch * C::CHUNK, g.h, g.seq.q0 + kBM * g.qt);
+      }
+      ++qc;
+    }
+    const int32_t* row = a.p.page_table + (long long)g.b * a.p.max_pages;
+    const int end = g.walk.end();
+    const int pages = (end + ps - 1) >> shift;
+    PageIds ids;
+    for (int i = 0; i < g.n; ++i) {
+      const int tok0 = kBN * g.walk.block(g.i0 + i);
+      const int p0 = tok0 >> shift;
+      const int valid = end - tok0 < kBN ? end - tok0 : kBN;
+      const int npg = ps >= kBN ? 1 : (valid + ps - 1) >> shift;
+      ids.cover(row, p0, npg, pages);
+      const int pg = lane / C::NCHUNK, ch = lane % C::NCHUNK;  // npg NCHUNK <= 16 lanes copy
+      int page = ids.get(p0 + pg);
+      const int slot = (int)(c % C::P);
+      ok = KQ ? wait_warp(bar(C::B_SFULL + slot), ((c / C::P) & 1u) ^ 1u, wt, kSiteKEmpty)
+              : wait_warp(bar(C::B_QKREADY + slot), (c / C::P) & 1u, wt, kSiteVEmpty);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(bar(FULL + slot), (uint32_t)(npg * box * C::ROWB * C::NCHUNK));
+      __syncwarp();
+      if (pg < npg) {
+        if (page < 0 || page >= a.p.num_pages) {
+          // read as zeros, past the pool's end: silu(0) V = 0
+          atomicOr(&g_dev_words[0], kStatusBadPaged);
+          page = a.p.num_pages;
+        }
+        tma_load_4d(base + OFF + slot * C::TILEB + ch * C::CHUNKB + pg * box * C::ROWB, tm,
+                    bar(FULL + slot), ch * C::CHUNK, g.h, ps >= kBN ? (tok0 & (ps - 1)) : 0, page);
+      }
+      ++c;
+    }
+  }
+  if (!ok && lane == 0) {
+    drain_copies(bar(FULL), C::P, c);
+    if (KQ) drain_copies(bar(C::B_QFULL), C::QS, qc);
+  }
+  __syncwarp();
+}
+
+// QK issuer: as role_mma_qk.
+template <int D>
+__device__ void paged_mma_qk(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from,
+                             uint32_t base, uint32_t tmem, const WaitCtx& wt) {
+  using C = Cfg<D>;
+  constexpr int P = C::P;
+  const uint32_t bars = base + C::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  constexpr uint32_t IDESC_QK = make_idesc(kBM, kBN, 0);
+  constexpr int QK_STEPS = D / 16;
+  constexpr int STEPS_PER_CHUNK = C::CHUNK / 16;
+  const uint64_t q_desc0 = smem_desc(base + C::Q_OFF, 16, C::ATOMB, C::LAYOUT);
+  const uint64_t k_desc0 = smem_desc(base + C::K_OFF, 16, C::ATOMB, C::LAYOUT);
+  bool ok = true;
+  if (a.debug_flags & kDebugUnsignalledWait) ok = wait_one(bar(C::B_DRAIN), 0u, wt, kSiteUnsignalled);
+  PagedSteps qc;
+  qc.start(a, w, from);
+  uint32_t ph = 0;
+  auto step = [&](auto jc) -> bool {
+    constexpr int J = decltype(jc)::value;
+    if (!ok || !qc.valid) return false;
+    const int qs = C::QS == 1 ? 0 : (qc.it & 1);
+    if (qc.i == 0 &&
+        !(ok = wait_one(bar(C::B_QFULL + qs), (uint32_t)(qc.it / C::QS) & 1u, wt, kSiteQFull)))
+      return false;
+    if (!(ok = wait_one(bar(C::B_QKREADY + J), ph, wt, kSiteKFull))) return false;
+    tc_fence_after();
+    const int cols = qc.cols();
+    const uint32_t s_tmem = pin32(tmem + (uint32_t)(J * 128));
+    const uint32_t idesc = pin32(cols == kBN ? IDESC_QK : make_idesc(kBM, cols, 0));
+    const uint64_t qd0 = q_desc0 + (uint64_t)((qs * C::TILEB) >> 4);
+    uint64_t qd[QK_STEPS], kd[QK_STEPS];
+#pragma unroll
+    for (int kk = 0; kk < QK_STEPS; ++kk) {
+      const uint32_t off = (kk / STEPS_PER_CHUNK) * C::CHUNKB + (kk % STEPS_PER_CHUNK) * 32;
+      qd[kk] = pin64(qd0 + (uint64_t)(off >> 4));
+      kd[kk] = pin64(k_desc0 + (uint64_t)((J * C::TILEB + off) >> 4));
+    }
+    mma_ss_c<0>(s_tmem, qd[0], kd[0], idesc);
+#pragma unroll
+    for (int kk = 1; kk < QK_STEPS; ++kk) mma_ss_c<1>(s_tmem, qd[kk], kd[kk], idesc);
+    mma_commit(bar(C::B_SFULL + J));
+    if (qc.last()) mma_commit(bar(C::B_QEMPTY + qs));
+    qc.advance(a, w);
+    if (J == P - 1) ph ^= 1u;
+    return true;
+  };
+  run_unrolled<P>(step);
+  if (!ok) {
+    mma_commit(bar(C::B_DRAIN));
+    wait_drain(bar(C::B_DRAIN), 0);
+  }
+}
+
+// PV issuer: as role_mma_pv, with the block that holds the tile's last keys
+// cut at the first key that no row sees.
+template <int D>
+__device__ void paged_mma_pv(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from,
+                             uint32_t base, uint32_t tmem, const WaitCtx& wt) {
+  using C = Cfg<D>;
+  constexpr int P = C::P;
+  const uint32_t bars = base + C::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  constexpr uint32_t IDESC_PV = make_idesc(kBM, D, 1);
+  const uint64_t v_desc0 = smem_desc(base + C::V_OFF, C::CHUNKB, C::ATOMB, C::LAYOUT);
+  bool ok = true;
+  PagedSteps pc;
+  pc.start(a, w, from);
+  uint32_t ph = 0;
+
+  auto issue_pv = [&](auto jc, auto hc, int ob, int cols) {
+    constexpr int J = decltype(jc)::value;
+    constexpr int H = decltype(hc)::value;
+    const uint32_t o_tmem = pin32(tmem + C::O_COL + (uint32_t)(ob * D));
+    uint32_t pa[8];
+    uint64_t vb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int kk = 4 * H + i;
+      const int hi_col = kWideSilu<D, 0> ? 16 * kk : 32 * (kk >> 1) + 8 * (kk & 1);
+      constexpr int lo_off = kWideSilu<D, 0> ? 8 : 16;
+      pa[2 * i] = pin32(tmem + (uint32_t)(J * 128 + hi_col));
+      pa[2 * i + 1] = pin32(tmem + (uint32_t)(J * 128 + hi_col + lo_off));
+      vb[i] = pin64(v_desc0 + (uint64_t)((J * C::TILEB + kk * 2 * C::ATOMB) >> 4));
+    }
+    if (cols == kBN && (H == 1 || pc.i != 0)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mma_ts_c<1>(o_tmem, pa[2 * i], vb[i], IDESC_PV);
+        mma_ts_c<1>(o_tmem, pa[2 * i + 1], vb[i], IDESC_PV);
+      }
+    } else {
+      const int n_steps = (cols - 64 * H) / 16;
+      const bool first = H == 0 && pc.i == 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < n_steps) {
+          if (i == 0 && first)
+            mma_ts_c<0>(o_tmem, pa[0], vb[0], IDESC_PV);
+          else
+            mma_ts_c<1>(o_tmem, pa[2 * i], vb[i], IDESC_PV);
+          mma_ts_c<1>(o_tmem, pa[2 * i + 1], vb[i], IDESC_PV);
+        }
+      }
+    }
+  };
+
+  bool pa_ready = false, v_ready = false;
+  auto step = [&](auto ic) -> bool {
+    constexpr int J = decltype(ic)::value;
+    constexpr int JN = (J + 1) % P;
+    if (!ok || !pc.valid) return false;
+    const int ob = C::OB == 1 ? 0 : (pc.it & 1);
+    const bool last = pc.last();
+    const int cols = pc.cols();
+    if (!pa_ready && !(ok = wait_one(bar(C::B_PFULL + J), ph, wt, kSitePFull))) return false;
+    if (pc.i == 0 &&
+        !(ok = wait_one(bar(C::B_OEMPTY + ob), ((uint32_t)(pc.it / C::OB) & 1u) ^ 1u, wt, kSiteOEmpty)))
+      return false;
+    if (!v_ready && !(ok = wait_one(bar(C::B_VFULL + J), ph, wt, kSiteVFull))) return false;
+    if (cols < kBN || pc.key0() + kBN > pc.g.walk.end()) {
+      // keys that no row sees: their P is zero, their V may be anything
+      const int r_end = pc.g.walk.end() - pc.key0();
+      if (r_end < cols) {
+        const uint32_t v_addr = base + C::V_OFF + J * C::TILEB;
+#pragma unroll
+        for (int ch = 0; ch < C::NCHUNK; ++ch) {
+          const uint32_t z0 = v_addr + ch * C::CHUNKB + r_end * C::ROWB;
+          const uint32_t z1 = v_addr + ch * C::CHUNKB + cols * C::ROWB;
+          for (uint32_t z = z0; z < z1; z += 16)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(z), "r"(0) : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+    }
+    tc_fence_after();
+    const uint32_t npar = J + 1 == P ? ph ^ 1u : ph;
+    pa_ready = mbar_test(bar(C::B_PFULL + JN), npar);
+    v_ready = mbar_test(bar(C::B_VFULL + JN), npar);
+    issue_pv(std::integral_constant<int, J>{}, std::integral_constant<int, 0>{}, ob, cols);
+    issue_pv(std::integral_constant<int, J>{}, std::integral_constant<int, 1>{}, ob, cols);
+    mma_commit(bar(C::B_QKREADY + J));
+    if (last) mma_commit(bar(C::B_OFULL + ob));
+    pc.advance(a, w);
+    if (J == P - 1) ph ^= 1u;
+    return true;
+  };
+  run_unrolled<P>(step);
+  if (!ok) {
+    mma_commit(bar(C::B_DRAIN + 1));
+    wait_drain(bar(C::B_DRAIN + 1), 0);
+  }
+}
+
+// SiLU warpgroups: as role_silu.  A masked block keeps key k for the row at
+// lim iff k <= lim and (k < lim_hist or k == lim); 16- or 32-key steps none
+// of whose keys a warp's rows keep are zeros without a load.
+template <int D>
+__device__ void paged_silu(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from,
+                           uint32_t base, uint32_t tmem, const WaitCtx& wt, int warp, int lane) {
+  using C = Cfg<D>;
+  constexpr int P = C::P;
+  const uint32_t bars = base + C::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  constexpr bool WIDE = kWideSilu<D, 0>;
+  constexpr int W = WIDE ? 16 : 32;  // keys of a step
+  const int wg = (warp - kEwWarp0) >> 2;
+  const int e = WIDE ? wg >> 1 : wg;
+  const int half = WIDE ? wg & 1 : 0;
+  const int quarter = warp & 3;
+  const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+  const float2 ha2 = make_float2(a.half_alpha, a.half_alpha);
+  PagedSteps cur;
+  cur.start(a, w, from);
+  while (cur.valid) {
+    if ((int)(cur.tc & 1u) != e) {
+      cur.advance(a, w);
+      continue;
+    }
+    const int j = (int)(cur.tc % P);
+    {
+      const bool ok = wait_one(bar(C::B_SFULL + j), (cur.tc / P) & 1u, wt, kSiteSFull);
+      if (!__all_sync(0xffffffffu, ok)) return;
+    }
+    tc_fence_after();
+    const uint32_t t_s = lane_base + (uint32_t)(j * 128);
+    if (quarter * 32 < cur.g.walk.rows) {
+      if (cur.plain()) {
+        if constexpr (WIDE) {
+          uint32_t w0[16], w1[16];
+          const uint32_t t_h = t_s + 64u * (uint32_t)half;
+          tmem_ld16_async(t_h, w0);
+          tmem_wait_ld16(w0);
+#pragma unroll 1
+          for (int u = 0; u < 4; u += 2) {
+            tmem_ld16_async(t_h + 16u * (u + 1), w1);
+            silu_store16<0>(w0, ha2, 0, 0, t_h + 16u * u);
+            tmem_wait_ld16(w1);
+            if (u + 2 < 4) tmem_ld16_async(t_h + 16u * (u + 2), w0);
+            silu_store16<0>(w1, ha2, 0, 0, t_h + 16u * (u + 1));
+            if (u + 2 < 4) tmem_wait_ld16(w0);
+          }
+        } else {
+          uint32_t s0[32], s1[32];
+          tmem_ld32_async(t_s, s0);
+          tmem_wait_ld(s0);
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tmem_ld32_async(t_s + 32u * (c + 1), s1);
+            silu_store32<0>(s0, ha2, 0, 0, t_s + 32u * c);
+            tmem_wait_ld(s1);
+            if (c + 2 < 4) tmem_ld32_async(t_s + 32u * (c + 2), s0);
+            silu_store32<0>(s1, ha2, 0, 0, t_s + 32u * (c + 1));
+            if (c + 2 < 4) tmem_wait_ld(s0);
+          }
+        }
+      } else {
+        const int cols = cur.cols(), key0 = cur.key0();
+        // the warp's rows stand at lim0 .. lim0 + 31, this lane's at lim0 + lane
+        const int lim0 = cur.g.walk.p0 + 32 * quarter - key0;
+        const int hist0 = cur.g.seq.hist - key0;
+        const int k0 = WIDE ? 64 * half : 0, k1 = WIDE ? 64 * half + 64 : kBN;
+#pragma unroll 1
+        for (int k = k0; k < k1 && k < cols; k += W) {
+          const uint32_t t_k = t_s + (uint32_t)k;
+          if (k > lim0 + 31 || (k >= hist0 && k + W <= lim0)) {
+            uint32_t z[16];
+#pragma unroll
+            for (int m = 0; m < 16; ++m) z[m] = 0u;
+            tmem_st16(t_k, z);
+            if constexpr (!WIDE) tmem_st16(t_k + 16u, z);
+          } else if constexpr (WIDE) {
+            uint32_t s[16];
+            tmem_ld16_async(t_k, s);
+            tmem_wait_ld16(s);
+            silu_store16<2>(s, ha2, lim0 + lane - k, hist0 - k, t_k);
+          } else {
+            uint32_t s[32];
+            tmem_ld32(t_k, s);
+            silu_store32<2>(s, ha2, lim0 + lane - k, hist0 - k, t_k);
+          }
+        }
+      }
+      tmem_wait_st();
+    }
+    tc_fence_before();
+    mbar_arrive(bar(C::B_PFULL + j));
+    cur.advance(a, w);
+  }
+}
+
+__device__ __forceinline__ void paged_epi_barrier() {  // the epilogue's four warps
+  asm volatile("bar.sync 2, 128;" ::: "memory");
+}
+
+// Epilogue: O x inv_n -> bf16 rows, or this CTA's part of a cut item, fp32 as
+// [D / 4][128 rows] float4 (consecutive lanes, consecutive 16 bytes).  The
+// CTA that arrives last sums the parts in the CTAs' order.
+template <int D>
+__device__ void paged_epilogue(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from,
+                               uint32_t base, uint32_t tmem, const WaitCtx& wt, int warp, int lane,
+                               int* last_flag) {
+  using C = Cfg<D>;
+  const uint32_t bars = base + C::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  const int quarter = warp & 3;
+  const int row = quarter * 32 + lane;
+  const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+  bool dead = false;  // the CTA gave up: meet the barriers, store nothing
+  PagedCursor c = from;
+  PagedSeg g;
+  for (int it = 0; c.next(a.p, w, &g); ++it) {
+    const int ob = it % C::OB;
+    if (!dead) dead = !wait_warp(bar(C::B_OFULL + ob), (uint32_t)(it / C::OB) & 1u, wt, kSiteOFull);
+    tc_fence_after();
+    const uint32_t o_t = tmem + lane_off + C::O_COL + (uint32_t)(ob * D);
+    const bool live = !dead && row < g.walk.rows;
+    uint4* dst = reinterpret_cast<uint4*>(
+        a.out + ((size_t)(g.seq.q0 + kBM * g.qt + row) * (size_t)w.heads + (size_t)g.h) * D);
+    if (g.parts == 1) {
+      uint32_t packed[D / 2];
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(o_t + 32u * cc, o);
+#pragma unroll
+        for (int m = 0; m < 16; ++m)
+          packed[16 * cc + m] =
+              pack_bf16x2(__uint_as_float(o[2 * m]) * a.inv_n, __uint_as_float(o[2 * m + 1]) * a.inv_n);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + ob));
+      if (live) {
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u)
+          dst[u] = make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
+      }
+      continue;
+    }
+    constexpr long long PART = (long long)kBM * D / 4;  // float4s of a part
+    float4* parts = reinterpret_cast<float4*>(a.parts);
+    float4* mine = parts + ((long long)blockIdx.x * 2 + (g.c0 == (int)blockIdx.x ? 1 : 0)) * PART + row;
+#pragma unroll 1
+    for (int cc = 0; cc < D / 32; ++cc) {
+      uint32_t o[32];
+      tmem_ld32(o_t + 32u * cc, o);
+      if (live) {
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          __stcg(mine + (8 * cc + m) * kBM,
+                 make_float4(__uint_as_float(o[4 * m]), __uint_as_float(o[4 * m + 1]),
+                             __uint_as_float(o[4 * m + 2]), __uint_as_float(o[4 * m + 3])));
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + ob));
+    __threadfence();
+    paged_epi_barrier();
+    if (threadIdx.x == 0) {
+      *last_flag = !dead && !*wt.abort_flag && atomicAdd(a.counters + g.c0, 1u) == (unsigned)(g.parts - 1);
+      if (*last_flag) a.counters[g.c0] = 0;  // ready for the next launch
+    }
+    paged_epi_barrier();
+    const bool sum = *last_flag != 0;
+    paged_epi_barrier();  // read before the next item writes it
+    if (!sum) continue;
+    __threadfence();
+    if (live) {
+#pragma unroll 1
+      for (int u = 0; u < D / 8; ++u) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        for (int i = 0; i < g.parts; ++i) {
+          const float4* src = parts + ((long long)(g.c0 + i) * 2 + (i == 0 ? 1 : 0)) * PART + row;
+          const float4 p = __ldcg(src + 2 * u * kBM), q = __ldcg(src + (2 * u + 1) * kBM);
+          x.x += p.x; x.y += p.y; x.z += p.z; x.w += p.w;
+          y.x += q.x; y.y += q.y; y.z += q.z; y.w += q.w;
+        }
+        dst[u] = make_uint4(pack_bf16x2(x.x * a.inv_n, x.y * a.inv_n), pack_bf16x2(x.z * a.inv_n, x.w * a.inv_n),
+                            pack_bf16x2(y.x * a.inv_n, y.y * a.inv_n), pack_bf16x2(y.z * a.inv_n, y.w * a.inv_n));
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreadsOf<D, 0>, 1)
+    hstu_fwd_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const PagedFwdArgs a) {
+  using C = Cfg<D>;
+  constexpr int WARPS = kFwdThreadsOf<D, 0> / 32;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PagedStart<WARPS> start;
+  __shared__ int last_flag;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bars = base + C::BAR_OFF;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NBARS; ++i) mbar_init(bars + 8u * i, C::arrivals(i, kWideSilu<D, 0>));
+    for (int j = 0; j < C::P; ++j) mbar_arrive(bars + 8u * (C::B_QKREADY + j));
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  PagedWork w = a.w;
+  PagedCursor from;
+  // a CTA without work leaves before it allocates TMEM
+  if (!paged_locate(a.p, &w, a.min_units, &start, &g_dev_words[0], &from)) return;
+  if (warp == kMmaWarpQK) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wt{a.timeout_ns, abort_flag};
+  if (warp == kTmaWarpK) {
+    paged_producer<D, true>(&tm_k, &tm_q, a, w, from, base, wt);
+  } else if (warp == kTmaWarpV) {
+    paged_producer<D, false>(&tm_v, &tm_q, a, w, from, base, wt);
+  } else if (warp == kMmaWarpQK) {
+    if (lane == 0) paged_mma_qk<D>(a, w, from, base, tmem, wt);
+    __syncwarp();
+  } else if (warp == kMmaWarpPV) {
+    if (lane == 0) paged_mma_pv<D>(a, w, from, base, tmem, wt);
+    __syncwarp();
+  } else if (warp >= kEwWarp0) {
+    paged_silu<D>(a, w, from, base, tmem, wt, warp, lane);
+  } else {
+    paged_epilogue<D>(a, w, from, base, tmem, wt, warp, lane, &last_flag);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarpQK) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+template <int D>
+cudaError_t launch_paged_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const PagedFwdArgs& a, int grid, cudaStream_t stream) {
+  using C = Cfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(
+      hstu_fwd_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_LAUNCH);
+  if (e != cudaSuccess) return e;
+  hstu_fwd_paged_kernel<D><<<grid, kFwdThreadsOf<D, 0>, C::SMEM_LAUNCH, stream>>>(tq, tk, tv, a);
+  return cudaGetLastError();
+}

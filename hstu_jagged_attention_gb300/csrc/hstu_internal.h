@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "hstu_paged.h"
+
 namespace hstu {
 
 // One work item: 128 query rows of one (sequence, head).
@@ -178,6 +180,25 @@ void fill_pairs(const int32_t* off, int batch, int heads, Item* dst);
 // first wait that gave up; read and cleared together.
 cudaError_t read_and_clear_device_status(unsigned* status, unsigned* site);
 
+// The attention over the paged cache on 128-row tcgen05 tiles
+// (hstu_fwd_paged.cuh).  w.total and w.per are found by the kernel.
+struct PagedFwdArgs {
+  PagedView p;
+  PagedWork w;
+  int min_units;
+  uint16_t* out;
+  float half_alpha, inv_n;
+  unsigned* counters;
+  float* parts;
+  unsigned long long timeout_ns;
+  unsigned debug_flags;
+};
+// tq describes q as (d, heads, rows) with box (min(d, 64), 1, 128); tk and tv
+// the pools as (d, heads, page_size, num_pages) with box (min(d, 64), 1,
+// min(page_size, 128), 1); all with the swizzle of fwd_swizzle_bytes.
+cudaError_t launch_fwd_paged(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedFwdArgs& a, int grid, cudaStream_t stream);
+
 // Bits of the status word, and the words' device address (the word, then
 // the site of the first wait that gave up) on the current device.
 constexpr unsigned kStatusTimeout = 1u;
@@ -191,6 +212,7 @@ constexpr int kSiteStepFull = 32, kSiteStepEmpty = 33;
 // check that it is an sm_103.
 int host_device_check(int* sm_count);
 unsigned long long host_wait_timeout_ns();
+unsigned host_debug_flags();
 // A bf16 tensor map of `rank` dimensions with the 128-byte (wide) or 64-byte
 // swizzle.
 int host_encode_map(CUtensorMap* m, void* ptr, int rank, const cuuint64_t* dims,

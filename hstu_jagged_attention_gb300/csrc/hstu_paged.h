@@ -126,16 +126,21 @@ struct PagedSeg {
   int c0, parts;        // the first CTA with a part of this item, and their number
 };
 
-// The segments of one CTA, from unit u (unit r of entry e) to u1.
+// The segments of one CTA, from unit u (unit r of entry e) to u1.  The
+// entry's lengths are read once for all its heads: `at` is the entry that the
+// segment handed to next() holds (-1 before the first).
 struct PagedCursor {
   long long u, u1;
-  int e, r;
+  int e, r, at;
   HSTU_HD bool next(const PagedView& p, const PagedWork& w, PagedSeg* g) {
     while (u < u1 && e < w.tiles * p.batch) {
-      g->qt = e / p.batch;
-      g->b = e - g->qt * p.batch;
-      paged_seq(p, g->b, &g->seq);
-      g->walk = paged_walk(g->seq, g->qt, w.tile_rows, w.kb_shift);
+      if (at != e) {
+        at = e;
+        g->qt = e / p.batch;
+        g->b = e - g->qt * p.batch;
+        paged_seq(p, g->b, &g->seq);
+        g->walk = paged_walk(g->seq, g->qt, w.tile_rows, w.kb_shift);
+      }
       const int nb = g->walk.nb;
       if (r >= w.heads * nb) {
         ++e;
