@@ -9,46 +9,56 @@
 //     the CTA that arrives last.
 // Included by hstu_fwd.cu.
 
-// A cursor over a CTA's key-block steps: block i of segment g (the it-th).
-struct PagedSteps {
-  PagedCursor c;
-  PagedSeg g;
-  int i, it;
-  uint32_t tc;
-  bool valid;
-  __device__ __forceinline__ void start(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from) {
-    c = from;
-    i = it = 0;
-    tc = 0;
-    valid = c.next(a.p, w, &g);
-  }
-  __device__ __forceinline__ void advance(const PagedFwdArgs& a, const PagedWork& w) {
-    ++tc;
-    if (++i == g.n) {
-      i = 0;
-      ++it;
-      valid = c.next(a.p, w, &g);
-    }
-  }
-  __device__ __forceinline__ bool last() const { return i == g.n - 1; }
-  __device__ __forceinline__ int key0() const { return kBN * g.walk.block(g.i0 + i); }
+// What the K producer, which runs ahead of every other role, leaves in shared
+// memory for them: a word per step (key block) and one per item.  Each role
+// then follows the CTA's steps 0 .. n - 1 with no schedule of its own: with
+// the cursor inlined in every role, the kernel missed the instruction cache
+// (73.7% hits, 88% of the cache's fill bandwidth) and 1024 candidates of 32
+// users took 494 us.
+// A word is written before its step's K copy is armed, so a role that has
+// waited for the step's barrier finds it.  When the word of step c is
+// written, QK(c - 3) and so PV(c - 6) are done: 8 step words are enough.  An
+// item is at most 6 steps ahead of the PV issuer, and that at most two items
+// ahead of the epilogue: 16 item words are enough.
+constexpr int kStepWords = 8, kItemWords = 16;
+struct PagedStep {
+  int lim;    // position of the tile's first row, less the block's first key
+  int hist;   // history end, less the block's first key
+  int rows;   // valid rows
+  int edge;   // bit 0: the item's first step, bit 1: its last
+  // First key (of the block) that no row sees; may be past the block.
+  __device__ __forceinline__ int end() const { return lim + rows; }
   // Keys of the block that some row sees, up to the MMA's steps of 16.
   __device__ __forceinline__ int cols() const {
-    const int r = g.walk.end() - key0();
+    const int r = end();
     return r >= kBN ? kBN : ((r + 15) & ~15);
   }
   // Every row sees every key of the block.
-  __device__ __forceinline__ bool plain() const {
-    const int e = key0() + kBN;
-    return e <= g.walk.p0 + 1 && e <= g.seq.hist;
-  }
+  __device__ __forceinline__ bool plain() const { return lim >= kBN - 1 && hist >= kBN; }
+  __device__ __forceinline__ bool first() const { return edge & 1; }
+  __device__ __forceinline__ bool last() const { return edge & 2; }
 };
+struct PagedItem {
+  int row0, h, rows, blocks, c0, parts;
+};
+struct PagedWords {
+  int4 step[kStepWords];
+  PagedItem item[kItemWords];
+};
+__device__ __forceinline__ PagedStep read_step(const PagedWords* words, uint32_t tc) {
+  PagedStep s;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(s.lim), "=r"(s.hist), "=r"(s.rows), "=r"(s.edge)
+               : "r"(smem_u32(words->step + tc % kStepWords))
+               : "memory");
+  return s;
+}
 
 // One warp: the K stream with each item's Q tile, or the V stream.
 template <int D, bool KQ>
 __device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, const PagedFwdArgs& a,
-                               const PagedWork& w, const PagedCursor& from, uint32_t base,
-                               const WaitCtx& wt) {
+                               const PagedWork& w, const PagedCursor& from, PagedWords* words,
+                               uint32_t base, const WaitCtx& wt) {
   using C = Cfg<D>;
   constexpr int FULL = KQ ? C::B_QKREADY : C::B_VFULL;
   constexpr int OFF = KQ ? C::K_OFF : C::V_OFF;
@@ -66,6 +76,8 @@ __device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, c
       const int qs = (int)(qc % C::QS);
       if (!(ok = wait_warp(bar(C::B_QEMPTY + qs), ((qc / C::QS) & 1u) ^ 1u, wt, kSiteQEmpty))) break;
       if (lane == 0) {
+        words->item[qc % kItemWords] =
+            PagedItem{g.seq.q0 + kBM * g.qt, g.h, g.walk.rows, g.n, g.c0, g.parts};
         mbar_arrive_expect_tx(bar(C::B_QFULL + qs), C::TILEB);
 #pragma unroll
         for (int ch = 0; ch < C::NCHUNK; ++ch)
@@ -90,7 +102,12 @@ __device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, c
       ok = KQ ? wait_warp(bar(C::B_SFULL + slot), ((c / C::P) & 1u) ^ 1u, wt, kSiteKEmpty)
               : wait_warp(bar(C::B_QKREADY + slot), (c / C::P) & 1u, wt, kSiteVEmpty);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(bar(FULL + slot), (uint32_t)(npg * box * C::ROWB * C::NCHUNK));
+      if (lane == 0) {
+        if (KQ)
+          words->step[c % kStepWords] = make_int4(g.walk.p0 - tok0, g.seq.hist - tok0, g.walk.rows,
+                                                  (i == 0 ? 1 : 0) | (i == g.n - 1 ? 2 : 0));
+        mbar_arrive_expect_tx(bar(FULL + slot), (uint32_t)(npg * box * C::ROWB * C::NCHUNK));
+      }
       __syncwarp();
       if (pg < npg) {
         if (page < 0 || page >= a.p.num_pages) {
@@ -113,7 +130,7 @@ __device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, c
 
 // QK issuer: as role_mma_qk.
 template <int D>
-__device__ void paged_mma_qk(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from,
+__device__ void paged_mma_qk(const PagedFwdArgs& a, uint32_t steps, const PagedWords* words,
                              uint32_t base, uint32_t tmem, const WaitCtx& wt) {
   using C = Cfg<D>;
   constexpr int P = C::P;
@@ -126,19 +143,18 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, const PagedWork& w, const Pa
   const uint64_t k_desc0 = smem_desc(base + C::K_OFF, 16, C::ATOMB, C::LAYOUT);
   bool ok = true;
   if (a.debug_flags & kDebugUnsignalledWait) ok = wait_one(bar(C::B_DRAIN), 0u, wt, kSiteUnsignalled);
-  PagedSteps qc;
-  qc.start(a, w, from);
+  uint32_t tc = 0, it = 0;
   uint32_t ph = 0;
   auto step = [&](auto jc) -> bool {
     constexpr int J = decltype(jc)::value;
-    if (!ok || !qc.valid) return false;
-    const int qs = C::QS == 1 ? 0 : (qc.it & 1);
-    if (qc.i == 0 &&
-        !(ok = wait_one(bar(C::B_QFULL + qs), (uint32_t)(qc.it / C::QS) & 1u, wt, kSiteQFull)))
-      return false;
+    if (!ok || tc == steps) return false;
+    const int qs = C::QS == 1 ? 0 : (int)(it & 1u);
     if (!(ok = wait_one(bar(C::B_QKREADY + J), ph, wt, kSiteKFull))) return false;
+    const PagedStep st = read_step(words, tc);
+    if (st.first() && !(ok = wait_one(bar(C::B_QFULL + qs), (it / C::QS) & 1u, wt, kSiteQFull)))
+      return false;
     tc_fence_after();
-    const int cols = qc.cols();
+    const int cols = st.cols();
     const uint32_t s_tmem = pin32(tmem + (uint32_t)(J * 128));
     const uint32_t idesc = pin32(cols == kBN ? IDESC_QK : make_idesc(kBM, cols, 0));
     const uint64_t qd0 = q_desc0 + (uint64_t)((qs * C::TILEB) >> 4);
@@ -153,8 +169,11 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, const PagedWork& w, const Pa
 #pragma unroll
     for (int kk = 1; kk < QK_STEPS; ++kk) mma_ss_c<1>(s_tmem, qd[kk], kd[kk], idesc);
     mma_commit(bar(C::B_SFULL + J));
-    if (qc.last()) mma_commit(bar(C::B_QEMPTY + qs));
-    qc.advance(a, w);
+    if (st.last()) {
+      mma_commit(bar(C::B_QEMPTY + qs));
+      ++it;
+    }
+    ++tc;
     if (J == P - 1) ph ^= 1u;
     return true;
   };
@@ -168,8 +187,8 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, const PagedWork& w, const Pa
 // PV issuer: as role_mma_pv, with the block that holds the tile's last keys
 // cut at the first key that no row sees.
 template <int D>
-__device__ void paged_mma_pv(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from,
-                             uint32_t base, uint32_t tmem, const WaitCtx& wt) {
+__device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t base, uint32_t tmem,
+                             const WaitCtx& wt) {
   using C = Cfg<D>;
   constexpr int P = C::P;
   const uint32_t bars = base + C::BAR_OFF;
@@ -177,11 +196,10 @@ __device__ void paged_mma_pv(const PagedFwdArgs& a, const PagedWork& w, const Pa
   constexpr uint32_t IDESC_PV = make_idesc(kBM, D, 1);
   const uint64_t v_desc0 = smem_desc(base + C::V_OFF, C::CHUNKB, C::ATOMB, C::LAYOUT);
   bool ok = true;
-  PagedSteps pc;
-  pc.start(a, w, from);
+  uint32_t tc = 0, it = 0;
   uint32_t ph = 0;
 
-  auto issue_pv = [&](auto jc, auto hc, int ob, int cols) {
+  auto issue_pv = [&](auto jc, auto hc, int ob, int cols, bool start) {
     constexpr int J = decltype(jc)::value;
     constexpr int H = decltype(hc)::value;
     const uint32_t o_tmem = pin32(tmem + C::O_COL + (uint32_t)(ob * D));
@@ -196,7 +214,7 @@ __device__ void paged_mma_pv(const PagedFwdArgs& a, const PagedWork& w, const Pa
       pa[2 * i + 1] = pin32(tmem + (uint32_t)(J * 128 + hi_col + lo_off));
       vb[i] = pin64(v_desc0 + (uint64_t)((J * C::TILEB + kk * 2 * C::ATOMB) >> 4));
     }
-    if (cols == kBN && (H == 1 || pc.i != 0)) {
+    if (cols == kBN && (H == 1 || !start)) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         mma_ts_c<1>(o_tmem, pa[2 * i], vb[i], IDESC_PV);
@@ -204,7 +222,7 @@ __device__ void paged_mma_pv(const PagedFwdArgs& a, const PagedWork& w, const Pa
       }
     } else {
       const int n_steps = (cols - 64 * H) / 16;
-      const bool first = H == 0 && pc.i == 0;
+      const bool first = H == 0 && start;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < n_steps) {
@@ -222,39 +240,39 @@ __device__ void paged_mma_pv(const PagedFwdArgs& a, const PagedWork& w, const Pa
   auto step = [&](auto ic) -> bool {
     constexpr int J = decltype(ic)::value;
     constexpr int JN = (J + 1) % P;
-    if (!ok || !pc.valid) return false;
-    const int ob = C::OB == 1 ? 0 : (pc.it & 1);
-    const bool last = pc.last();
-    const int cols = pc.cols();
+    if (!ok || tc == steps) return false;
+    const int ob = C::OB == 1 ? 0 : (int)(it & 1u);
     if (!pa_ready && !(ok = wait_one(bar(C::B_PFULL + J), ph, wt, kSitePFull))) return false;
-    if (pc.i == 0 &&
-        !(ok = wait_one(bar(C::B_OEMPTY + ob), ((uint32_t)(pc.it / C::OB) & 1u) ^ 1u, wt, kSiteOEmpty)))
+    const PagedStep st = read_step(words, tc);
+    const int cols = st.cols();
+    if (st.first() &&
+        !(ok = wait_one(bar(C::B_OEMPTY + ob), ((it / C::OB) & 1u) ^ 1u, wt, kSiteOEmpty)))
       return false;
     if (!v_ready && !(ok = wait_one(bar(C::B_VFULL + J), ph, wt, kSiteVFull))) return false;
-    if (cols < kBN || pc.key0() + kBN > pc.g.walk.end()) {
+    if (st.end() < cols) {
       // keys that no row sees: their P is zero, their V may be anything
-      const int r_end = pc.g.walk.end() - pc.key0();
-      if (r_end < cols) {
-        const uint32_t v_addr = base + C::V_OFF + J * C::TILEB;
+      const uint32_t v_addr = base + C::V_OFF + J * C::TILEB;
 #pragma unroll
-        for (int ch = 0; ch < C::NCHUNK; ++ch) {
-          const uint32_t z0 = v_addr + ch * C::CHUNKB + r_end * C::ROWB;
-          const uint32_t z1 = v_addr + ch * C::CHUNKB + cols * C::ROWB;
-          for (uint32_t z = z0; z < z1; z += 16)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(z), "r"(0) : "memory");
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      for (int ch = 0; ch < C::NCHUNK; ++ch) {
+        const uint32_t z0 = v_addr + ch * C::CHUNKB + st.end() * C::ROWB;
+        const uint32_t z1 = v_addr + ch * C::CHUNKB + cols * C::ROWB;
+        for (uint32_t z = z0; z < z1; z += 16)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(z), "r"(0) : "memory");
       }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     tc_fence_after();
     const uint32_t npar = J + 1 == P ? ph ^ 1u : ph;
     pa_ready = mbar_test(bar(C::B_PFULL + JN), npar);
     v_ready = mbar_test(bar(C::B_VFULL + JN), npar);
-    issue_pv(std::integral_constant<int, J>{}, std::integral_constant<int, 0>{}, ob, cols);
-    issue_pv(std::integral_constant<int, J>{}, std::integral_constant<int, 1>{}, ob, cols);
+    issue_pv(std::integral_constant<int, J>{}, std::integral_constant<int, 0>{}, ob, cols, st.first());
+    issue_pv(std::integral_constant<int, J>{}, std::integral_constant<int, 1>{}, ob, cols, st.first());
     mma_commit(bar(C::B_QKREADY + J));
-    if (last) mma_commit(bar(C::B_OFULL + ob));
-    pc.advance(a, w);
+    if (st.last()) {
+      mma_commit(bar(C::B_OFULL + ob));
+      ++it;
+    }
+    ++tc;
     if (J == P - 1) ph ^= 1u;
     return true;
   };
@@ -269,8 +287,8 @@ __device__ void paged_mma_pv(const PagedFwdArgs& a, const PagedWork& w, const Pa
 // lim iff k <= lim and (k < lim_hist or k == lim); 16- or 32-key steps none
 // of whose keys a warp's rows keep are zeros without a load.
 template <int D>
-__device__ void paged_silu(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from,
-                           uint32_t base, uint32_t tmem, const WaitCtx& wt, int warp, int lane) {
+__device__ void paged_silu(const PagedFwdArgs& a, uint32_t steps, const PagedWords* words, uint32_t base,
+                           uint32_t tmem, const WaitCtx& wt, int warp, int lane) {
   using C = Cfg<D>;
   constexpr int P = C::P;
   const uint32_t bars = base + C::BAR_OFF;
@@ -283,22 +301,17 @@ __device__ void paged_silu(const PagedFwdArgs& a, const PagedWork& w, const Page
   const int quarter = warp & 3;
   const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
   const float2 ha2 = make_float2(a.half_alpha, a.half_alpha);
-  PagedSteps cur;
-  cur.start(a, w, from);
-  while (cur.valid) {
-    if ((int)(cur.tc & 1u) != e) {
-      cur.advance(a, w);
-      continue;
-    }
-    const int j = (int)(cur.tc % P);
+  for (uint32_t tc = (uint32_t)e; tc < steps; tc += 2) {
+    const int j = (int)(tc % P);
     {
-      const bool ok = wait_one(bar(C::B_SFULL + j), (cur.tc / P) & 1u, wt, kSiteSFull);
+      const bool ok = wait_one(bar(C::B_SFULL + j), (tc / P) & 1u, wt, kSiteSFull);
       if (!__all_sync(0xffffffffu, ok)) return;
     }
     tc_fence_after();
+    const PagedStep st = read_step(words, tc);
     const uint32_t t_s = lane_base + (uint32_t)(j * 128);
-    if (quarter * 32 < cur.g.walk.rows) {
-      if (cur.plain()) {
+    if (quarter * 32 < st.rows) {
+      if (st.plain()) {
         if constexpr (WIDE) {
           uint32_t w0[16], w1[16];
           const uint32_t t_h = t_s + 64u * (uint32_t)half;
@@ -328,10 +341,10 @@ __device__ void paged_silu(const PagedFwdArgs& a, const PagedWork& w, const Page
           }
         }
       } else {
-        const int cols = cur.cols(), key0 = cur.key0();
+        const int cols = st.cols();
         // the warp's rows stand at lim0 .. lim0 + 31, this lane's at lim0 + lane
-        const int lim0 = cur.g.walk.p0 + 32 * quarter - key0;
-        const int hist0 = cur.g.seq.hist - key0;
+        const int lim0 = st.lim + 32 * quarter;
+        const int hist0 = st.hist;
         const int k0 = WIDE ? 64 * half : 0, k1 = WIDE ? 64 * half + 64 : kBN;
 #pragma unroll 1
         for (int k = k0; k < k1 && k < cols; k += W) {
@@ -358,38 +371,34 @@ __device__ void paged_silu(const PagedFwdArgs& a, const PagedWork& w, const Page
     }
     tc_fence_before();
     mbar_arrive(bar(C::B_PFULL + j));
-    cur.advance(a, w);
   }
 }
 
-__device__ __forceinline__ void paged_epi_barrier() {  // the epilogue's four warps
-  asm volatile("bar.sync 2, 128;" ::: "memory");
-}
-
 // Epilogue: O x inv_n -> bf16 rows, or this CTA's part of a cut item, fp32 as
-// [D / 4][128 rows] float4 (consecutive lanes, consecutive 16 bytes).  The
-// CTA that arrives last sums the parts in the CTAs' order.
+// [D / 4][128 rows] float4 (consecutive lanes, consecutive 16 bytes).  Each
+// warp hands over its own 32 rows: the warp that arrives last among the CTAs'
+// sums their parts in the CTAs' order, so no warp waits for another and the
+// result does not depend on who is last.
 template <int D>
-__device__ void paged_epilogue(const PagedFwdArgs& a, const PagedWork& w, const PagedCursor& from,
-                               uint32_t base, uint32_t tmem, const WaitCtx& wt, int warp, int lane,
-                               int* last_flag) {
+__device__ void paged_epilogue(const PagedFwdArgs& a, uint32_t steps, const PagedWords* words,
+                               uint32_t base, uint32_t tmem, const WaitCtx& wt, int warp, int lane) {
   using C = Cfg<D>;
   const uint32_t bars = base + C::BAR_OFF;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   const int quarter = warp & 3;
   const int row = quarter * 32 + lane;
   const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-  bool dead = false;  // the CTA gave up: meet the barriers, store nothing
-  PagedCursor c = from;
-  PagedSeg g;
-  for (int it = 0; c.next(a.p, w, &g); ++it) {
-    const int ob = it % C::OB;
-    if (!dead) dead = !wait_warp(bar(C::B_OFULL + ob), (uint32_t)(it / C::OB) & 1u, wt, kSiteOFull);
+  for (uint32_t it = 0, done = 0; done < steps; ++it) {
+    const int ob = (int)(it % C::OB);
+    if (!wait_warp(bar(C::B_OFULL + ob), (it / C::OB) & 1u, wt, kSiteOFull)) return;
     tc_fence_after();
+    const volatile PagedItem& x = words->item[it % kItemWords];
+    const PagedItem g{x.row0, x.h, x.rows, x.blocks, x.c0, x.parts};
+    done += (uint32_t)g.blocks;
     const uint32_t o_t = tmem + lane_off + C::O_COL + (uint32_t)(ob * D);
-    const bool live = !dead && row < g.walk.rows;
+    const bool live = row < g.rows;
     uint4* dst = reinterpret_cast<uint4*>(
-        a.out + ((size_t)(g.seq.q0 + kBM * g.qt + row) * (size_t)w.heads + (size_t)g.h) * D);
+        a.out + ((size_t)(g.row0 + row) * (size_t)a.w.heads + (size_t)g.h) * D);
     if (g.parts == 1) {
       uint32_t packed[D / 2];
 #pragma unroll
@@ -427,31 +436,29 @@ __device__ void paged_epilogue(const PagedFwdArgs& a, const PagedWork& w, const 
       }
     }
     tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + ob));
     __threadfence();
-    paged_epi_barrier();
-    if (threadIdx.x == 0) {
-      *last_flag = !dead && !*wt.abort_flag && atomicAdd(a.counters + g.c0, 1u) == (unsigned)(g.parts - 1);
-      if (*last_flag) a.counters[g.c0] = 0;  // ready for the next launch
+    __syncwarp();
+    int last = 0;
+    if (lane == 0) {
+      mbar_arrive(bar(C::B_OEMPTY + ob));
+      unsigned* counter = a.counters + 4 * g.c0 + quarter;
+      last = atomicAdd(counter, 1u) == (unsigned)(g.parts - 1);
+      if (last) *counter = 0;  // ready for the next launch
     }
-    paged_epi_barrier();
-    const bool sum = *last_flag != 0;
-    paged_epi_barrier();  // read before the next item writes it
-    if (!sum) continue;
+    if (!__shfl_sync(0xffffffffu, last, 0)) continue;
     __threadfence();
     if (live) {
 #pragma unroll 1
       for (int u = 0; u < D / 8; ++u) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
         for (int i = 0; i < g.parts; ++i) {
           const float4* src = parts + ((long long)(g.c0 + i) * 2 + (i == 0 ? 1 : 0)) * PART + row;
-          const float4 p = __ldcg(src + 2 * u * kBM), q = __ldcg(src + (2 * u + 1) * kBM);
-          x.x += p.x; x.y += p.y; x.z += p.z; x.w += p.w;
-          y.x += q.x; y.y += q.y; y.z += q.z; y.w += q.w;
+          const float4 y = __ldcg(src + 2 * u * kBM), z = __ldcg(src + (2 * u + 1) * kBM);
+          p.x += y.x; p.y += y.y; p.z += y.z; p.w += y.w;
+          q.x += z.x; q.y += z.y; q.z += z.z; q.w += z.w;
         }
-        dst[u] = make_uint4(pack_bf16x2(x.x * a.inv_n, x.y * a.inv_n), pack_bf16x2(x.z * a.inv_n, x.w * a.inv_n),
-                            pack_bf16x2(y.x * a.inv_n, y.y * a.inv_n), pack_bf16x2(y.z * a.inv_n, y.w * a.inv_n));
+        dst[u] = make_uint4(pack_bf16x2(p.x * a.inv_n, p.y * a.inv_n), pack_bf16x2(p.z * a.inv_n, p.w * a.inv_n),
+                            pack_bf16x2(q.x * a.inv_n, q.y * a.inv_n), pack_bf16x2(q.z * a.inv_n, q.w * a.inv_n));
       }
     }
   }
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(kFwdThreadsOf<D, 0>, 1)
   constexpr int WARPS = kFwdThreadsOf<D, 0> / 32;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PagedStart<WARPS> start;
-  __shared__ int last_flag;
+  __shared__ PagedWords words;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
@@ -496,20 +503,21 @@ __global__ void __launch_bounds__(kFwdThreadsOf<D, 0>, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wt{a.timeout_ns, abort_flag};
+  const uint32_t steps = (uint32_t)(from.u1 - from.u);
   if (warp == kTmaWarpK) {
-    paged_producer<D, true>(&tm_k, &tm_q, a, w, from, base, wt);
+    paged_producer<D, true>(&tm_k, &tm_q, a, w, from, &words, base, wt);
   } else if (warp == kTmaWarpV) {
-    paged_producer<D, false>(&tm_v, &tm_q, a, w, from, base, wt);
+    paged_producer<D, false>(&tm_v, &tm_q, a, w, from, &words, base, wt);
   } else if (warp == kMmaWarpQK) {
-    if (lane == 0) paged_mma_qk<D>(a, w, from, base, tmem, wt);
+    if (lane == 0) paged_mma_qk<D>(a, steps, &words, base, tmem, wt);
     __syncwarp();
   } else if (warp == kMmaWarpPV) {
-    if (lane == 0) paged_mma_pv<D>(a, w, from, base, tmem, wt);
+    if (lane == 0) paged_mma_pv<D>(steps, &words, base, tmem, wt);
     __syncwarp();
   } else if (warp >= kEwWarp0) {
-    paged_silu<D>(a, w, from, base, tmem, wt, warp, lane);
+    paged_silu<D>(a, steps, &words, base, tmem, wt, warp, lane);
   } else {
-    paged_epilogue<D>(a, w, from, base, tmem, wt, warp, lane, &last_flag);
+    paged_epilogue<D>(a, steps, &words, base, tmem, wt, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
