@@ -143,16 +143,14 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, uint32_t steps, const PagedW
   const uint64_t k_desc0 = smem_desc(base + C::K_OFF, 16, C::ATOMB, C::LAYOUT);
   bool ok = true;
   if (a.debug_flags & kDebugUnsignalledWait) ok = wait_one(bar(C::B_DRAIN), 0u, wt, kSiteUnsignalled);
+  if (!ok) steps = 0;
   uint32_t tc = 0, it = 0;
   uint32_t ph = 0;
-  auto step = [&](auto jc) -> bool {
-    constexpr int J = decltype(jc)::value;
-    if (!ok || tc == steps) return false;
+  for (int J = 0; tc < steps; J = J + 1 == P ? 0 : J + 1) {
     const int qs = C::QS == 1 ? 0 : (int)(it & 1u);
-    if (!(ok = wait_one(bar(C::B_QKREADY + J), ph, wt, kSiteKFull))) return false;
+    if (!(ok = wait_one(bar(C::B_QKREADY + J), ph, wt, kSiteKFull))) break;
     const PagedStep st = read_step(words, tc);
-    if (st.first() && !(ok = wait_one(bar(C::B_QFULL + qs), (it / C::QS) & 1u, wt, kSiteQFull)))
-      return false;
+    if (st.first() && !(ok = wait_one(bar(C::B_QFULL + qs), (it / C::QS) & 1u, wt, kSiteQFull))) break;
     tc_fence_after();
     const int cols = st.cols();
     const uint32_t s_tmem = pin32(tmem + (uint32_t)(J * 128));
@@ -175,9 +173,7 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, uint32_t steps, const PagedW
     }
     ++tc;
     if (J == P - 1) ph ^= 1u;
-    return true;
-  };
-  run_unrolled<P>(step);
+  }
   if (!ok) {
     mma_commit(bar(C::B_DRAIN));
     wait_drain(bar(C::B_DRAIN), 0);
@@ -199,8 +195,7 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
   uint32_t tc = 0, it = 0;
   uint32_t ph = 0;
 
-  auto issue_pv = [&](auto jc, auto hc, int ob, int cols, bool start) {
-    constexpr int J = decltype(jc)::value;
+  auto issue_pv = [&](int J, auto hc, int ob, int cols, bool start) {
     constexpr int H = decltype(hc)::value;
     const uint32_t o_tmem = pin32(tmem + C::O_COL + (uint32_t)(ob * D));
     uint32_t pa[8];
@@ -237,18 +232,16 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
   };
 
   bool pa_ready = false, v_ready = false;
-  auto step = [&](auto ic) -> bool {
-    constexpr int J = decltype(ic)::value;
-    constexpr int JN = (J + 1) % P;
-    if (!ok || tc == steps) return false;
+  for (int J = 0; tc < steps; J = J + 1 == P ? 0 : J + 1) {
+    const int JN = J + 1 == P ? 0 : J + 1;
     const int ob = C::OB == 1 ? 0 : (int)(it & 1u);
-    if (!pa_ready && !(ok = wait_one(bar(C::B_PFULL + J), ph, wt, kSitePFull))) return false;
+    if (!pa_ready && !(ok = wait_one(bar(C::B_PFULL + J), ph, wt, kSitePFull))) break;
     const PagedStep st = read_step(words, tc);
     const int cols = st.cols();
     if (st.first() &&
         !(ok = wait_one(bar(C::B_OEMPTY + ob), ((it / C::OB) & 1u) ^ 1u, wt, kSiteOEmpty)))
-      return false;
-    if (!v_ready && !(ok = wait_one(bar(C::B_VFULL + J), ph, wt, kSiteVFull))) return false;
+      break;
+    if (!v_ready && !(ok = wait_one(bar(C::B_VFULL + J), ph, wt, kSiteVFull))) break;
     if (st.end() < cols) {
       // keys that no row sees: their P is zero, their V may be anything
       const uint32_t v_addr = base + C::V_OFF + J * C::TILEB;
@@ -265,8 +258,8 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
     const uint32_t npar = J + 1 == P ? ph ^ 1u : ph;
     pa_ready = mbar_test(bar(C::B_PFULL + JN), npar);
     v_ready = mbar_test(bar(C::B_VFULL + JN), npar);
-    issue_pv(std::integral_constant<int, J>{}, std::integral_constant<int, 0>{}, ob, cols, st.first());
-    issue_pv(std::integral_constant<int, J>{}, std::integral_constant<int, 1>{}, ob, cols, st.first());
+    issue_pv(J, std::integral_constant<int, 0>{}, ob, cols, st.first());
+    issue_pv(J, std::integral_constant<int, 1>{}, ob, cols, st.first());
     mma_commit(bar(C::B_QKREADY + J));
     if (st.last()) {
       mma_commit(bar(C::B_OFULL + ob));
@@ -274,9 +267,7 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
     }
     ++tc;
     if (J == P - 1) ph ^= 1u;
-    return true;
-  };
-  run_unrolled<P>(step);
+  }
   if (!ok) {
     mma_commit(bar(C::B_DRAIN + 1));
     wait_drain(bar(C::B_DRAIN + 1), 0);
