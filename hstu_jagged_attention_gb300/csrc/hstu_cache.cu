@@ -14,6 +14,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <climits>
 #include <new>
 
 #include "hstu_attn.h"
@@ -156,17 +157,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 }
 
 // ------------------------------------------------ attention of a few tokens
-// A tile is up to 16 MT new tokens of one (sequence, head); it walks blocks
-// of 64 keys.  Warp 4 copies each block's K and V rows, page by page, into a
-// ring of shared-memory stages (bulk-tensor copies, swizzled rows).  Warps
-// 0-3 take 16 of the 64 keys each: S = Q K^T, p = silu(alpha S), O += p V on
-// mma.sync m16n8k16, with p split into two bf16 terms as in the forward, so
-// that P V keeps 16 bits of p.  With so few rows the cache is read once for
-// them all and the copies, not the products, set the time: a 128-row tcgen05
-// tile would do the same reads with 8 times the products.
-constexpr int kStepKeys = 64, kStepShift = 6;
+// A tile is up to 16 new tokens of one (sequence, head); it walks blocks of 128
+// keys (64 at d = 128).  Warp 4 copies each block's K and V rows, page by page,
+// into a ring of shared-memory stages (bulk-tensor copies, swizzled rows).
+// Warps 0-3 take a quarter of the keys each: S = Q K^T, p = silu(alpha S),
+// O += p V on mma.sync m16n8k16, with p split into two bf16 terms as in the
+// forward, so that P V keeps 16 bits of p.  With so few rows the cache is read
+// once for them all and the copies, not the products, set the time: a 128-row
+// tcgen05 tile would do the same reads with 8 times the products.
+constexpr int kStepRows = 16;
 constexpr int kStepWarps = 4;  // warps that compute
 constexpr int kStepThreads = 32 * (kStepWarps + 1);
+// Keys of a block: 32 a warp, two k16 steps whose chains of products overlap;
+// at d = 128 one step has as many products.
+constexpr int step_shift(int d) { return d == 128 ? 6 : 7; }
 
 struct StepArgs {
   PagedView p;
@@ -234,59 +238,68 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 template <int D>
 struct StepCfg {
-  static constexpr int CH = D < 64 ? D : 64;  // channels of a swizzled row
+  static constexpr int SHIFT = step_shift(D);
+  static constexpr int KEYS = 1 << SHIFT;
+  static constexpr int KW = KEYS / kStepWarps;  // keys of a warp: 16 or 32
+  static constexpr int CH = D < 64 ? D : 64;    // channels of a swizzled row
   static constexpr int NCH = D / CH;
   static constexpr int ROWB = CH * 2;
-  static constexpr int CHUNKB = kStepKeys * ROWB;
-  static constexpr int TILEB = NCH * CHUNKB;  // 64 rows of K, or of V
+  static constexpr int CHUNKB = KEYS * ROWB;
+  static constexpr int TILEB = NCH * CHUNKB;    // a block's rows of K, or of V
   static constexpr int STAGEB = 2 * TILEB;
   static constexpr int MAX_STAGES = 16;
-  // byte of 16-byte column c of row r in a tile
+  // Byte of 16-byte column c of row r in a tile.  The columns' swizzle is an
+  // exclusive or below the row's bytes, so with c0 < 2 even columns c away:
+  // at(r, c0 + c) = at(r, c0) ^ (c << 4), within a chunk.
   static __device__ __forceinline__ uint32_t at(int r, int c) {
-    constexpr int PER = CH / 8;  // 16-byte columns of a swizzled row
-    const int ch = c / PER, cc = c % PER;
     const int x = ROWB == 128 ? (r & 7) : ((r >> 1) & 3);
-    return (uint32_t)(ch * CHUNKB + r * ROWB + ((cc ^ x) << 4));
+    return (uint32_t)(r * ROWB + ((c ^ x) << 4));
+  }
+  // from at(r, c0), c0 < 2, to 16-byte column c0 + 2 k
+  static __device__ __forceinline__ uint32_t step(uint32_t base, int k) {
+    constexpr int PER = CH / 16;
+    return (base ^ (uint32_t)((k % PER) << 5)) + (uint32_t)((k / PER) * CHUNKB);
   }
 };
 
 // Shared memory behind the stages: the warps' partial sums, the barriers,
 // and the schedule's words.
+// 8 floats between rows, so that eight rows' 8-byte stores meet all banks
+__host__ __device__ constexpr int step_red_stride(int d) { return d + 8; }
 __host__ __device__ constexpr int step_red_bytes(int rows, int d) {
-  return kStepWarps * rows * d * (int)sizeof(float);
+  return kStepWarps * rows * step_red_stride(d) * (int)sizeof(float);
 }
 constexpr int kStepTailBytes = 2 * 16 * 8 + 64 + 16 * 8;
 
 struct StepMisc {
   int abort_flag;
-  int last;   // this CTA arrived last at the item it shares
+  unsigned last;  // bits: this CTA arrived last at the items it shares
   PagedStart<kStepWarps + 1> start;
 };
 static_assert(sizeof(StepMisc) <= 64 + 16 * 8, "misc");
 
 template <int D>
 __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const StepArgs& a,
-                             const PagedWork& w, PagedCursor c, uint32_t base, uint32_t full,
+                             const PagedWork& w, PagedCursor c, PagedSeg g, uint32_t base, uint32_t full,
                              uint32_t empty, const StepWait& wt) {
   using C = StepCfg<D>;
   const int lane = threadIdx.x & 31;
   const int shift = a.p.page_shift, ps = 1 << shift;
-  const int box = ps < kStepKeys ? ps : kStepKeys;
+  const int box = ps < C::KEYS ? ps : C::KEYS;
   int st = 0;
   uint32_t ph = 1, count = 0;
-  PagedSeg g;
   while (c.next(a.p, w, &g)) {
     const int32_t* row = a.p.page_table + (long long)g.b * a.p.max_pages;
     const int end = g.walk.end();
     const int pages = (end + ps - 1) >> shift;  // of the sequence, as far as the tile sees
     PageIds ids;
     for (int i = 0; i < g.n; ++i) {
-      const int tok0 = g.walk.block(g.i0 + i) << kStepShift;
+      const int tok0 = g.walk.block(g.i0 + i) << C::SHIFT;
       const int p0 = tok0 >> shift;
-      const int valid = end - tok0 < kStepKeys ? end - tok0 : kStepKeys;
-      const int npg = ps >= kStepKeys ? 1 : (valid + ps - 1) >> shift;
+      const int valid = end - tok0 < C::KEYS ? end - tok0 : C::KEYS;
+      const int npg = ps >= C::KEYS ? 1 : (valid + ps - 1) >> shift;
       ids.cover(row, p0, npg, pages);
-      // lane: which page of the block, which chunk of channels, K or V
+      // npg 2 NCH <= 16 lanes copy; lane: which page of the block, which chunk of channels, K or V
       const int pg = lane / (2 * C::NCH), ch = (lane >> 1) % C::NCH;
       int page = ids.get(p0 + pg);
       const uint32_t bar = full + 8u * st;
@@ -302,7 +315,7 @@ __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const
         const uint32_t dst = base + st * C::STAGEB + (lane & 1) * C::TILEB + ch * C::CHUNKB +
                              pg * box * C::ROWB;
         tma_load_4d(dst, (lane & 1) ? tv : tk, bar, ch * C::CH, g.h,
-                    ps >= kStepKeys ? (tok0 & (ps - 1)) : 0, page);
+                    ps >= C::KEYS ? (tok0 & (ps - 1)) : 0, page);
       }
       ++count;
       if (++st == a.stages) {
@@ -330,120 +343,148 @@ __device__ __forceinline__ void step_barrier() {  // the computing warps
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
 }
 
-template <int D, int MT>
-__device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor c, uint32_t base,
+// An item whose blocks several CTAs share.
+struct StepCut {
+  uint16_t* out;  // its first row
+  int rows, c0, parts;
+};
+// CTA `cta`'s part of the item that it starts, or that an earlier one does.
+template <int D>
+__device__ __forceinline__ float* step_part(const StepArgs& a, int cta, bool starts) {
+  return a.parts + ((long long)cta * 2 + (starts ? 1 : 0)) * (kStepRows * D);
+}
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x;
+  a.y += b.y;
+  a.z += b.z;
+  a.w += b.w;
+}
+// Values x .. x + 3 of an item's (rows, D) sums.
+template <int D>
+__device__ __forceinline__ void step_store(uint16_t* out, int heads, int x, const float4& v, float inv_n) {
+  *reinterpret_cast<uint2*>(out + (long long)(x / D) * heads * D + x % D) =
+      make_uint2(pack_bf16x2(v.x * inv_n, v.y * inv_n), pack_bf16x2(v.z * inv_n, v.w * inv_n));
+}
+
+template <int D>
+__device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor c, PagedSeg g, uint32_t base,
                              uint32_t full, uint32_t empty, float* red, StepMisc* m,
                              const StepWait& wt) {
   using C = StepCfg<D>;
+  constexpr int KS = C::KW / 16;  // k16 steps of the P V product
+  constexpr int RS = step_red_stride(D);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
-  const int key0 = 16 * warp;  // this warp's keys of a block
+  const int key0 = C::KW * warp;  // this warp's keys of a block
   // ldmatrix rows: K as (keys 0-7 | 8-15) x (channels 0-7 | 8-15), V likewise, transposed
   const int mat = lane >> 3, mr = lane & 7;
-  const int k_row = key0 + (mat >> 1) * 8 + mr, k_col = mat & 1;
-  const int v_row = key0 + (mat & 1) * 8 + mr, v_col = mat >> 1;
+  const uint32_t k_at = C::at(key0 + (mat >> 1) * 8 + mr, mat & 1);
+  const uint32_t v_at = C::TILEB + C::at(key0 + (mat & 1) * 8 + mr, mat >> 1);
+  const float2 ha2 = make_float2(a.half_alpha, a.half_alpha);
   int st = 0;
   uint32_t ph = 0;
   bool dead = false;  // the CTA gave up: run on without waits, store nothing
-  PagedSeg g;
+  StepCut cut0{}, cut1{};  // items shared with earlier, and with later, CTAs
   while (c.next(a.p, w, &g)) {
-    uint32_t qf[MT][D / 16][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r0 = 16 * mt + g8, r1 = r0 + 8;
-      const long long row0 = g.seq.q0 + (long long)w.tile_rows * g.qt;
-      const uint16_t* x0 = a.q + (row0 + r0) * a.q_stride + (long long)g.h * D + 2 * t4;
+    const int rows = g.walk.rows;
+    uint32_t qf[D / 16][4];
+    {
+      const int r0 = g8, r1 = r0 + 8;
+      const uint16_t* x0 = a.q + (long long)(g.seq.q0 + r0) * a.q_stride + (long long)g.h * D + 2 * t4;
       const uint16_t* x1 = x0 + 8 * a.q_stride;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        qf[mt][kk][0] = r0 < g.walk.rows ? *reinterpret_cast<const uint32_t*>(x0 + 16 * kk) : 0u;
-        qf[mt][kk][1] = r1 < g.walk.rows ? *reinterpret_cast<const uint32_t*>(x1 + 16 * kk) : 0u;
-        qf[mt][kk][2] = r0 < g.walk.rows ? *reinterpret_cast<const uint32_t*>(x0 + 16 * kk + 8) : 0u;
-        qf[mt][kk][3] = r1 < g.walk.rows ? *reinterpret_cast<const uint32_t*>(x1 + 16 * kk + 8) : 0u;
+        qf[kk][0] = r0 < rows ? *reinterpret_cast<const uint32_t*>(x0 + 16 * kk) : 0u;
+        qf[kk][1] = r1 < rows ? *reinterpret_cast<const uint32_t*>(x1 + 16 * kk) : 0u;
+        qf[kk][2] = r0 < rows ? *reinterpret_cast<const uint32_t*>(x0 + 16 * kk + 8) : 0u;
+        qf[kk][3] = r1 < rows ? *reinterpret_cast<const uint32_t*>(x1 + 16 * kk + 8) : 0u;
       }
     }
-    float o[MT][D / 8][4];
+    float o[D / 8][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[mt][n][j] = 0.f;
+      for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
 
     for (int i = 0; i < g.n; ++i) {
-      const int kb = g.walk.block(g.i0 + i) << kStepShift;
+      const int kb = g.walk.block(g.i0 + i) << C::SHIFT;
       if (!dead) dead = !__all_sync(0xffffffffu, step_wait(full + 8u * st, ph, wt, kSiteStepFull));
-      const uint32_t ks = base + st * C::STAGEB, vs = ks + C::TILEB;
-      float s[MT][2][4];
+      const uint32_t ks = base + st * C::STAGEB + k_at, vs = base + st * C::STAGEB + v_at;
+      float s[2 * KS][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int n = 0; n < 2 * KS; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[mt][n][j] = 0.f;
+        for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t kf[4];
-        ldsm4(ks + C::at(k_row, 2 * kk + k_col), kf);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816(s[mt][0], qf[mt][kk], kf[0], kf[1]);
-          mma16816(s[mt][1], qf[mt][kk], kf[2], kf[3]);
+        for (int y = 0; y < KS; ++y) {
+          uint32_t kf[4];
+          ldsm4(C::step(ks + 16 * y * C::ROWB, kk), kf);
+          mma16816(s[2 * y], qf[kk], kf[0], kf[1]);
+          mma16816(s[2 * y + 1], qf[kk], kf[2], kf[3]);
         }
       }
       // p = silu(alpha S) = h + h tanh(h), h = alpha S / 2; as an A operand
-      // its columns are this thread's own score columns
-      const bool masked = kb + kStepKeys > g.walk.p0 + 1 || kb + kStepKeys > g.seq.hist;
-      uint32_t hi[MT][4], lo[MT][4];
+      // its columns are this thread's own score columns.  Rows 8 .. 15 only
+      // where they exist.
+      const bool masked = kb + C::KEYS > g.walk.p0 + 1 || kb + C::KEYS > g.seq.hist;
+      uint32_t hi[KS][4], lo[KS][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int r = 0; r < 2; ++r) {
+        if (r == 0 || rows > 8) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float p[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float x = s[mt][n][2 * r + j] * a.half_alpha;
-              p[j] = fmaf(x, tanh_approx(x), x);
-            }
+          for (int n = 0; n < 2 * KS; ++n) {
+            const float2 x = __fmul2_rn(make_float2(s[n][2 * r], s[n][2 * r + 1]), ha2);
+            float2 p = __ffma2_rn(x, make_float2(tanh_approx(x.x), tanh_approx(x.y)), x);
             if (masked) {
-              const int pos = g.walk.p0 + 16 * mt + 8 * r + g8;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int key = kb + key0 + 8 * n + 2 * t4 + j;
-                if (!(key <= pos && (key < g.seq.hist || key == pos))) p[j] = 0.f;
-              }
+              const int pos = g.walk.p0 + 8 * r + g8, key = kb + key0 + 8 * n + 2 * t4;
+              if (!(key <= pos && (key < g.seq.hist || key == pos))) p.x = 0.f;
+              if (!(key + 1 <= pos && (key + 1 < g.seq.hist || key + 1 == pos))) p.y = 0.f;
             }
-            const uint32_t ph2 = pack_bf16x2(p[0], p[1]);
-            hi[mt][2 * n + r] = ph2;
-            lo[mt][2 * n + r] = pack_bf16x2(p[0] - __uint_as_float(ph2 << 16),
-                                            p[1] - __uint_as_float(ph2 & 0xffff0000u));
+            const uint32_t ph2 = pack_bf16x2(p.x, p.y);
+            const float2 rest = __fadd2_rn(
+                p, make_float2(-__uint_as_float(ph2 << 16), -__uint_as_float(ph2 & 0xffff0000u)));
+            hi[n >> 1][2 * (n & 1) + r] = ph2;
+            lo[n >> 1][2 * (n & 1) + r] = pack_bf16x2(rest.x, rest.y);
           }
-      // values behind the last key any row sees may be anything, NaN too
-      const int live = g.walk.end() - kb - key0;  // of this warp's 16 keys
-      uint32_t m0 = ~0u, m1 = ~0u;
-      if (live < 16) {
-        const int k0 = 2 * t4;
-        m0 = (k0 < live ? 0xffffu : 0u) | (k0 + 1 < live ? 0xffff0000u : 0u);
-        m1 = (k0 + 8 < live ? 0xffffu : 0u) | (k0 + 9 < live ? 0xffff0000u : 0u);
-      }
+        } else {
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
-        uint32_t vf[4];
-        ldsm4_t(vs + C::at(v_row, 2 * n + v_col), vf);
+          for (int n = 0; n < 2 * KS; ++n) hi[n >> 1][2 * (n & 1) + 1] = lo[n >> 1][2 * (n & 1) + 1] = 0u;
+        }
+      }
+      // values behind the last key any row sees may be anything, NaN too
+#pragma unroll
+      for (int y = 0; y < KS; ++y) {
+        const int live = g.walk.end() - kb - key0 - 16 * y;  // of these 16 keys
+        uint32_t m0 = ~0u, m1 = ~0u;
         if (live < 16) {
-          vf[0] &= m0;
-          vf[1] &= m1;
-          vf[2] &= m0;
-          vf[3] &= m1;
+          const int k0 = 2 * t4;
+          m0 = (k0 < live ? 0xffffu : 0u) | (k0 + 1 < live ? 0xffff0000u : 0u);
+          m1 = (k0 + 8 < live ? 0xffffu : 0u) | (k0 + 9 < live ? 0xffff0000u : 0u);
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816(o[mt][2 * n], hi[mt], vf[0], vf[1]);
-          mma16816(o[mt][2 * n + 1], hi[mt], vf[2], vf[3]);
-          mma16816(o[mt][2 * n], lo[mt], vf[0], vf[1]);
-          mma16816(o[mt][2 * n + 1], lo[mt], vf[2], vf[3]);
+        for (int half = 0; half < 2; ++half) {
+          constexpr int N = D / 32;  // 16-channel steps of a half: their values stay in registers
+          uint32_t vf[N][4];
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            ldsm4_t(C::step(vs + 16 * y * C::ROWB, half * N + n), vf[n]);
+            vf[n][0] &= m0;
+            vf[n][1] &= m1;
+            vf[n][2] &= m0;
+            vf[n][3] &= m1;
+          }
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            mma16816(o[2 * (half * N + n)], hi[y], vf[n][0], vf[n][1]);
+            mma16816(o[2 * (half * N + n) + 1], hi[y], vf[n][2], vf[n][3]);
+          }
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            mma16816(o[2 * (half * N + n)], lo[y], vf[n][0], vf[n][1]);
+            mma16816(o[2 * (half * N + n) + 1], lo[y], vf[n][2], vf[n][3]);
+          }
         }
       }
       __syncwarp();
@@ -455,71 +496,81 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
     }
 
     // the four warps' sums over their keys, then out or this CTA's part
-    const int rows = g.walk.rows;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int r = 0; r < 2; ++r) {
+      const int row = 8 * r + g8;
+      if (row < rows) {
+        float* dst = red + (warp * a.red_rows + row) * RS + 2 * t4;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 16 * mt + 8 * r + g8;
-        if (row < rows) {
-          float* dst = red + (warp * a.red_rows + row) * D + 2 * t4;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[mt][n][2 * r], o[mt][n][2 * r + 1]);
-        }
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
       }
-    step_barrier();
-    const bool stop = *static_cast<volatile int*>(&m->abort_flag) != 0;
-    const bool whole = g.parts == 1;
-    float* mine = a.parts + ((long long)blockIdx.x * 2 + (g.c0 == (int)blockIdx.x ? 1 : 0)) *
-                                (long long)(w.tile_rows * D);
-    uint16_t* out = a.out + ((g.seq.q0 + (long long)w.tile_rows * g.qt) * w.heads + g.h) * D;
-    const long long out_stride = (long long)w.heads * D;
-    for (int x = 2 * threadIdx.x; x < rows * D; x += 2 * 32 * kStepWarps) {
-      float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kStepWarps; ++i) {
-        const float2 y = *reinterpret_cast<const float2*>(red + i * a.red_rows * D + x);
-        v.x += y.x;
-        v.y += y.y;
-      }
-      if (stop) continue;
-      if (whole)
-        *reinterpret_cast<uint32_t*>(out + (x / D) * out_stride + x % D) =
-            pack_bf16x2(v.x * a.inv_n, v.y * a.inv_n);
-      else
-        __stcg(reinterpret_cast<float2*>(mine + x), v);
     }
-    if (!whole) {
-      // the last CTA to arrive sums the parts in the CTAs' order, so the
-      // result does not depend on who is last
-      __threadfence();
-      step_barrier();
-      if (threadIdx.x == 0) {
-        m->last = !stop && atomicAdd(a.counters + g.c0, 1u) == (unsigned)(g.parts - 1);
-        if (m->last) a.counters[g.c0] = 0;  // ready for the next launch
-      }
-      step_barrier();
-      if (m->last) {
-        __threadfence();
-        for (int x = 2 * threadIdx.x; x < rows * D; x += 2 * 32 * kStepWarps) {
-          float2 v = make_float2(0.f, 0.f);
-          for (int i = 0; i < g.parts; ++i) {
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(
-                a.parts + ((long long)(g.c0 + i) * 2 + (i == 0 ? 1 : 0)) * (long long)(w.tile_rows * D) + x));
-            v.x += y.x;
-            v.y += y.y;
-          }
-          *reinterpret_cast<uint32_t*>(out + (x / D) * out_stride + x % D) =
-              pack_bf16x2(v.x * a.inv_n, v.y * a.inv_n);
-        }
-      }
+    step_barrier();
+    dead = *static_cast<volatile int*>(&m->abort_flag) != 0;
+    uint16_t* out = a.out + ((long long)g.seq.q0 * w.heads + g.h) * D;
+    const bool before = g.c0 != (int)blockIdx.x;
+    float* part = step_part<D>(a, blockIdx.x, !before);
+    for (int x = 4 * threadIdx.x; x < rows * D; x += 4 * 32 * kStepWarps) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kStepWarps; ++i)
+        add4(v, *reinterpret_cast<const float4*>(red + (i * a.red_rows + x / D) * RS + x % D));
+      if (dead) continue;
+      if (g.parts == 1)
+        step_store<D>(out, w.heads, x, v, a.inv_n);
+      else
+        __stcg(reinterpret_cast<float4*>(part + x), v);
+    }
+    if (g.parts > 1) {
+      const StepCut cut{out, rows, g.c0, g.parts};
+      if (before)
+        cut0 = cut;
+      else
+        cut1 = cut;
     }
     step_barrier();  // red is free for the next item
   }
+  if (cut0.parts == 0 && cut1.parts == 0) return;
+  // The last CTA to arrive at a cut item sums its parts in the CTAs' order, so
+  // that the result does not depend on who is last.  One fence a CTA, after
+  // the barrier and so for all the warps' stores.
+  if (threadIdx.x == 0) {
+    __threadfence();
+    unsigned last = 0;
+    if (cut0.parts && !dead && atomicAdd(a.counters + cut0.c0, 1u) == (unsigned)(cut0.parts - 1)) last |= 1u;
+    if (cut1.parts && !dead && atomicAdd(a.counters + cut1.c0, 1u) == (unsigned)(cut1.parts - 1)) last |= 2u;
+    // ready for the next launch
+    if (last & 1u) a.counters[cut0.c0] = 0;
+    if (last & 2u) a.counters[cut1.c0] = 0;
+    m->last = last;
+  }
+  step_barrier();
+  const unsigned last = m->last;
+  if (last) __threadfence();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    if (!(last >> k & 1u)) continue;
+    const StepCut cut = k ? cut1 : cut0;
+    for (int x = 4 * threadIdx.x; x < cut.rows * D; x += 4 * 32 * kStepWarps) {
+      float4 v = __ldcg(reinterpret_cast<const float4*>(step_part<D>(a, cut.c0, true) + x));
+#pragma unroll 1
+      for (int i = 1; i < cut.parts; i += 8) {  // eight loads in flight
+        float4 y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          y[j] = i + j < cut.parts
+                     ? __ldcg(reinterpret_cast<const float4*>(step_part<D>(a, cut.c0 + i + j, false) + x))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) add4(v, y[j]);
+      }
+      step_store<D>(cut.out, w.heads, x, v, a.inv_n);
+    }
+  }
 }
 
-template <int D, int MT>
+template <int D>
 __global__ void __launch_bounds__(kStepThreads)
     step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                 const StepArgs a) {
@@ -533,12 +584,10 @@ __global__ void __launch_bounds__(kStepThreads)
   const uint32_t full = smem_u32(after), empty = full + 8u * C::MAX_STAGES;
   StepMisc* m = reinterpret_cast<StepMisc*>(after + 2 * C::MAX_STAGES * 8);
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(full + 8u * i, 1);
-      mbar_init(empty + 8u * i, kStepWarps);
-    }
-    m->abort_flag = 0;
+  if (threadIdx.x < a.stages) {
+    mbar_init(full + 8u * threadIdx.x, 1);
+    mbar_init(empty + 8u * threadIdx.x, kStepWarps);
+    if (threadIdx.x == 0) m->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -548,46 +597,43 @@ __global__ void __launch_bounds__(kStepThreads)
   }
   PagedWork w = a.w;
   PagedCursor c;
-  if (!paged_locate(a.p, &w, a.min_units, &m->start, a.status, &c)) return;
+  PagedSeg g;
+  if (!paged_locate(a.p, &w, a.min_units, &m->start, a.status, &c, &g)) return;
   const StepWait wt{a.timeout_ns, &m->abort_flag, a.status};
   if (warp == kStepWarps)
-    step_produce<D>(&tk, &tv, a, w, c, base, full, empty, wt);
+    step_produce<D>(&tk, &tv, a, w, c, g, base, full, empty, wt);
   else
-    step_compute<D, MT>(a, w, c, base, full, empty, red, m, wt);
+    step_compute<D>(a, w, c, g, base, full, empty, red, m, wt);
 }
 
-template <int D, int MT>
-cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, StepArgs a, int sms,
-                        cudaStream_t stream) {
+template <int D>
+cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, long long most, StepArgs a,
+                        int sms, cudaStream_t stream) {
   using C = StepCfg<D>;
-  // two CTAs an SM share its 227 KB where the sums leave room for 3 stages each
+  // Two CTAs an SM, 64 KB of copies in flight each.  More stages make every
+  // CTA's first block wait for the others' queued copies and leave more
+  // blocks to compute once the last bytes have landed: 512 sequences of
+  // log-normal lengths took 42.2 us with 2 stages of 32 KB, 44.2 with 3.
+  constexpr int kPerSm = 2;
+  a.stages = (64 * 1024) / C::STAGEB;
+  static_assert((64 * 1024) / C::STAGEB >= 2 && (64 * 1024) / C::STAGEB <= C::MAX_STAGES, "stages");
   const int extra = step_red_bytes(a.red_rows, D) + kStepTailBytes + 1024;
-  const int half = 113 * 1024, whole = 227 * 1024;
-  int per_sm = 2, stages = (half - extra) / C::STAGEB;
-  if (stages < 3) {
-    per_sm = 1;
-    stages = (whole - extra) / C::STAGEB;
-  }
-  a.stages = std::min(stages, (int)C::MAX_STAGES);
   const int bytes = a.stages * C::STAGEB + extra;
-  const long long most = (long long)a.w.tiles * a.p.batch * a.w.heads *
-                         (((long long)a.p.max_pages << a.p.page_shift) / kStepKeys + 2);
-  const int grid = (int)std::min<long long>((long long)per_sm * sms,
+  const int grid = (int)std::min<long long>((long long)kPerSm * sms,
                                             (most + a.min_units - 1) / a.min_units);
-  const cudaError_t e = cudaFuncSetAttribute(step_kernel<D, MT>,
+  const cudaError_t e = cudaFuncSetAttribute(step_kernel<D>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  step_kernel<D, MT><<<grid, kStepThreads, bytes, stream>>>(tk, tv, a);
+  step_kernel<D><<<grid, kStepThreads, bytes, stream>>>(tk, tv, a);
   return cudaGetLastError();
 }
 
-template <int MT>
-cudaError_t launch_step_d(int d, const CUtensorMap& tk, const CUtensorMap& tv, const StepArgs& a, int sms,
-                          cudaStream_t s) {
+cudaError_t launch_step_d(int d, const CUtensorMap& tk, const CUtensorMap& tv, long long most,
+                          const StepArgs& a, int sms, cudaStream_t s) {
   switch (d) {
-    case 32: return launch_step<32, MT>(tk, tv, a, sms, s);
-    case 64: return launch_step<64, MT>(tk, tv, a, sms, s);
-    default: return launch_step<128, MT>(tk, tv, a, sms, s);
+    case 32: return launch_step<32>(tk, tv, most, a, sms, s);
+    case 64: return launch_step<64>(tk, tv, most, a, sms, s);
+    default: return launch_step<128>(tk, tv, most, a, sms, s);
   }
 }
 
@@ -623,8 +669,8 @@ struct hstu_cache {
   long long page_stride;
   int device, sms;
   unsigned* status;
-  CUtensorMap tk, tv;            // 64-row boxes (a few new tokens)
-  CUtensorMap tk_tile, tv_tile;  // 128-row boxes (many)
+  // boxes of 128 keys, and of a block of a few new tokens' kernel
+  CUtensorMap tk_tile, tv_tile, tk, tv;
 };
 
 namespace {
@@ -651,6 +697,14 @@ int check_batch(const hstu_paged_batch* b, PagedView* v, int num_pages, int page
   *v = PagedView{b->q_offsets, b->kv_lens, b->num_targets, b->page_table, b->batch, b->max_pages,
                  b->max_q, b->rows, num_pages, page_shift};
   return HSTU_OK;
+}
+
+constexpr long long kMostUnits = 1 << 30;
+// Units of a launch, at most: a tile walks every block of its sequence once.
+long long units_bound(const PagedView& v, int heads, int tiles, int kb_shift) {
+  const long long blocks = (((long long)v.max_pages << v.page_shift) >> kb_shift) + 2;
+  const long long entries = (long long)tiles * v.batch;
+  return entries > INT32_MAX || entries * heads > INT32_MAX ? LLONG_MAX : entries * heads * blocks;
 }
 
 int check_geometry(int num_pages, int page_size, int* shift) {
@@ -703,10 +757,10 @@ int hstu_cache_create(void* k_pages, void* v_pages, int num_pages, int page_size
   if (rc == HSTU_OK && hstu::device_status_words(&c->status) != cudaSuccess) rc = HSTU_ERR_CUDA;
   if (rc == HSTU_OK)
     rc = hstu::make_pool_map(&c->tk, k_pages, num_pages, page_size, heads, d, page_stride,
-                             hstu::kStepKeys);
+                             1 << hstu::step_shift(d));
   if (rc == HSTU_OK)
     rc = hstu::make_pool_map(&c->tv, v_pages, num_pages, page_size, heads, d, page_stride,
-                             hstu::kStepKeys);
+                             1 << hstu::step_shift(d));
   if (rc == HSTU_OK)
     rc = hstu::make_pool_map(&c->tk_tile, k_pages, num_pages, page_size, heads, d, page_stride,
                              HSTU_BLOCK_N);
@@ -775,23 +829,27 @@ int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int p
   w.tile_rows = tile_rows;
   w.tiles = v.rows > 0 && v.batch > 0 ? (v.max_q + tile_rows - 1) / tile_rows : 0;
   while ((1 << w.kb_shift) < block_keys) ++w.kb_shift;
-  auto units_of = [&](int e) -> long long {
+  if (units_bound(v, heads, w.tiles, w.kb_shift) > kMostUnits) return HSTU_ERR_INVALID_ARG;
+  auto units_of = [&](int e) {
     hstu::PagedSeq s;
     hstu::paged_seq(v, e % v.batch, &s);
-    return (long long)heads * hstu::paged_walk(s, e / v.batch, tile_rows, w.kb_shift).nb;
+    return heads * hstu::paged_walk(s, e / v.batch, tile_rows, w.kb_shift).nb;
   };
   for (int e = 0; e < w.tiles * v.batch; ++e) w.total += units_of(e);
-  w.per = hstu::paged_share(w.total, grid, min_units);
+  w.per = hstu::paged_share(w, v.batch, grid, min_units);
   int n = 0;
-  for (int cta = 0; cta < grid && cta * w.per < w.total; ++cta) {
+  for (int cta = 0; cta < grid && (long long)cta * w.per < w.total; ++cta) {
     hstu::PagedCursor c{};
-    c.at = -1;
-    c.u = cta * w.per;
-    c.u1 = std::min(c.u + w.per, w.total);
-    long long at = 0;
+    c.cta = cta;
+    c.u = c.u0 = cta * w.per;
+    c.u1 = (int)std::min<long long>((long long)c.u + w.per, w.total);
+    int at = 0;
     while (at + units_of(c.e) <= c.u) at += units_of(c.e++);
-    c.r = (int)(c.u - at);
     hstu::PagedSeg g;
+    c.load(v, w, &g);
+    c.loaded = true;
+    c.h = (c.u - at) / g.walk.nb;
+    c.i = c.u - at - c.h * g.walk.nb;
     while (c.next(v, w, &g)) {
       if (host_dst) {
         if (n >= capacity) return HSTU_ERR_INVALID_ARG;
@@ -859,15 +917,13 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   if (bad_rows(q, q_stride, (long long)heads * d) || hstu::bad_ptr(out, 16)) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_device(cache)) != HSTU_OK) return rc;
   hstu::PagedWork w{};
-  const bool tiled = p.max_q > 32;
+  const bool tiled = p.max_q > hstu::kStepRows;
   w.heads = heads;
-  w.tile_rows = tiled ? HSTU_BLOCK_M : p.max_q > 16 ? 32 : 16;
+  w.tile_rows = tiled ? HSTU_BLOCK_M : hstu::kStepRows;
   w.tiles = (p.max_q + w.tile_rows - 1) / w.tile_rows;
-  w.kb_shift = tiled ? 7 : hstu::kStepShift;
-  // a unit's index within an entry, and an entry's, are 32-bit
-  const long long blocks = (((long long)p.max_pages << cache->page_shift) >> w.kb_shift) + 3;
-  if (blocks * heads > 0x7fffffffLL || (long long)w.tiles * p.batch > 0x7fffffffLL)
-    return HSTU_ERR_INVALID_ARG;
+  w.kb_shift = tiled ? 7 : hstu::step_shift(d);
+  const long long most = units_bound(p, heads, w.tiles, w.kb_shift);
+  if (most > kMostUnits) return HSTU_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CUtensorMap tq;
   if (tiled) {
@@ -895,7 +951,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     hstu::PagedFwdArgs a{};
     a.p = p;
     a.w = w;
-    a.min_units = 4;
+    a.min_units = 1;
     a.out = static_cast<uint16_t*>(out);
     a.half_alpha = 0.5f * alpha;
     a.inv_n = inv_n;
@@ -903,14 +959,13 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     a.parts = parts;
     a.timeout_ns = hstu::host_wait_timeout_ns();
     a.debug_flags = hstu::host_debug_flags();
-    const long long most = (long long)w.tiles * p.batch * heads * blocks;
     const int grid = (int)std::min<long long>(cache->sms, (most + a.min_units - 1) / a.min_units);
     e = hstu::launch_fwd_paged(d, tq, cache->tk_tile, cache->tv_tile, a, grid, s);
   } else {
     hstu::StepArgs a{};
     a.p = p;
     a.w = w;
-    a.min_units = 4;
+    a.min_units = 1;
     a.red_rows = std::min(p.max_q, w.tile_rows);
     a.q = static_cast<const uint16_t*>(q);
     a.q_stride = q_stride;
@@ -921,8 +976,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     a.parts = parts;
     a.status = cache->status;
     a.timeout_ns = hstu::host_wait_timeout_ns();
-    e = w.tile_rows == 16 ? hstu::launch_step_d<1>(d, cache->tk, cache->tv, a, cache->sms, s)
-                          : hstu::launch_step_d<2>(d, cache->tk, cache->tv, a, cache->sms, s);
+    e = hstu::launch_step_d(d, cache->tk, cache->tv, most, a, cache->sms, s);
   }
   rc = hstu::status_of(e);
   if (own && cudaFreeAsync(own, s) != cudaSuccess && rc == HSTU_OK) rc = HSTU_ERR_CUDA;

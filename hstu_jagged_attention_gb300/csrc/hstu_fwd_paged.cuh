@@ -44,7 +44,16 @@ struct PagedItem {
 struct PagedWords {
   int4 step[kStepWords];
   PagedItem item[kItemWords];
+  // the items shared with earlier and with later CTAs (parts == 0: none), and
+  // which of them this CTA sums
+  PagedItem cut[2];
+  unsigned last;
 };
+// CTA `cta`'s part of the item that an earlier CTA starts (0) or that it starts (1).
+template <int D>
+__device__ __forceinline__ float4* paged_part(const PagedFwdArgs& a, int cta, int starts) {
+  return reinterpret_cast<float4*>(a.parts) + ((long long)cta * 2 + starts) * (kBM * D / 4);
+}
 __device__ __forceinline__ PagedStep read_step(const PagedWords* words, uint32_t tc) {
   PagedStep s;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -57,7 +66,7 @@ __device__ __forceinline__ PagedStep read_step(const PagedWords* words, uint32_t
 // One warp: the K stream with each item's Q tile, or the V stream.
 template <int D, bool KQ>
 __device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, const PagedFwdArgs& a,
-                               const PagedWork& w, const PagedCursor& from, PagedWords* words,
+                               const PagedWork& w, PagedCursor cur, PagedSeg g, PagedWords* words,
                                uint32_t base, const WaitCtx& wt) {
   using C = Cfg<D>;
   constexpr int FULL = KQ ? C::B_QKREADY : C::B_VFULL;
@@ -69,8 +78,6 @@ __device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, c
   const int box = ps < kBN ? ps : kBN;
   uint32_t c = 0, qc = 0;
   bool ok = true;
-  PagedCursor cur = from;
-  PagedSeg g;
   while (ok && cur.next(a.p, w, &g)) {
     if (KQ) {
       const int qs = (int)(qc % C::QS);
@@ -366,13 +373,11 @@ __device__ void paged_silu(const PagedFwdArgs& a, uint32_t steps, const PagedWor
 }
 
 // Epilogue: O x inv_n -> bf16 rows, or this CTA's part of a cut item, fp32 as
-// [D / 4][128 rows] float4 (consecutive lanes, consecutive 16 bytes).  Each
-// warp hands over its own 32 rows: the warp that arrives last among the CTAs'
-// sums their parts in the CTAs' order, so no warp waits for another and the
-// result does not depend on who is last.
+// [D / 4][128 rows] float4 (consecutive lanes, consecutive 16 bytes), with a
+// note of the item for paged_join.
 template <int D>
-__device__ void paged_epilogue(const PagedFwdArgs& a, uint32_t steps, const PagedWords* words,
-                               uint32_t base, uint32_t tmem, const WaitCtx& wt, int warp, int lane) {
+__device__ void paged_epilogue(const PagedFwdArgs& a, uint32_t steps, PagedWords* words, uint32_t base,
+                               uint32_t tmem, const WaitCtx& wt, int warp, int lane) {
   using C = Cfg<D>;
   const uint32_t bars = base + C::BAR_OFF;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
@@ -388,8 +393,6 @@ __device__ void paged_epilogue(const PagedFwdArgs& a, uint32_t steps, const Page
     done += (uint32_t)g.blocks;
     const uint32_t o_t = tmem + lane_off + C::O_COL + (uint32_t)(ob * D);
     const bool live = row < g.rows;
-    uint4* dst = reinterpret_cast<uint4*>(
-        a.out + ((size_t)(g.row0 + row) * (size_t)a.w.heads + (size_t)g.h) * D);
     if (g.parts == 1) {
       uint32_t packed[D / 2];
 #pragma unroll
@@ -405,15 +408,16 @@ __device__ void paged_epilogue(const PagedFwdArgs& a, uint32_t steps, const Page
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + ob));
       if (live) {
+        uint4* dst = reinterpret_cast<uint4*>(
+            a.out + ((size_t)(g.row0 + row) * (size_t)a.w.heads + (size_t)g.h) * D);
 #pragma unroll
         for (int u = 0; u < D / 8; ++u)
           dst[u] = make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
       }
       continue;
     }
-    constexpr long long PART = (long long)kBM * D / 4;  // float4s of a part
-    float4* parts = reinterpret_cast<float4*>(a.parts);
-    float4* mine = parts + ((long long)blockIdx.x * 2 + (g.c0 == (int)blockIdx.x ? 1 : 0)) * PART + row;
+    const int starts = g.c0 == (int)blockIdx.x ? 1 : 0;
+    float4* mine = paged_part<D>(a, blockIdx.x, starts) + row;
 #pragma unroll 1
     for (int cc = 0; cc < D / 32; ++cc) {
       uint32_t o[32];
@@ -427,30 +431,60 @@ __device__ void paged_epilogue(const PagedFwdArgs& a, uint32_t steps, const Page
       }
     }
     tc_fence_before();
-    __threadfence();
     __syncwarp();
-    int last = 0;
-    if (lane == 0) {
-      mbar_arrive(bar(C::B_OEMPTY + ob));
-      unsigned* counter = a.counters + 4 * g.c0 + quarter;
-      last = atomicAdd(counter, 1u) == (unsigned)(g.parts - 1);
-      if (last) *counter = 0;  // ready for the next launch
-    }
-    if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+    if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + ob));
+    if (threadIdx.x == 0) words->cut[starts] = g;
+  }
+}
+
+// Once all roles are done: the last CTA to arrive at a cut item (the one that
+// an earlier CTA starts, the one that this CTA starts) sums its parts in the
+// CTAs' order, with all its threads, so that the result does not depend on
+// who is last.  One fence a CTA, after the barrier and so for all the warps'
+// stores.
+template <int D>
+__device__ void paged_join(const PagedFwdArgs& a, PagedWords* words, bool dead) {
+  if (words->cut[0].parts == 0 && words->cut[1].parts == 0) return;
+  if (threadIdx.x == 0) {
     __threadfence();
-    if (live) {
+    unsigned last = 0;
+    for (int k = 0; k < 2; ++k) {
+      const PagedItem& g = words->cut[k];
+      if (!g.parts || dead || atomicAdd(a.counters + g.c0, 1u) != (unsigned)(g.parts - 1)) continue;
+      last |= 1u << k;
+      a.counters[g.c0] = 0;  // ready for the next launch
+    }
+    words->last = last;
+  }
+  __syncthreads();
+  const unsigned last = words->last;
+  if (last) __threadfence();
 #pragma unroll 1
-      for (int u = 0; u < D / 8; ++u) {
-        float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
-        for (int i = 0; i < g.parts; ++i) {
-          const float4* src = parts + ((long long)(g.c0 + i) * 2 + (i == 0 ? 1 : 0)) * PART + row;
-          const float4 y = __ldcg(src + 2 * u * kBM), z = __ldcg(src + (2 * u + 1) * kBM);
-          p.x += y.x; p.y += y.y; p.z += y.z; p.w += y.w;
-          q.x += z.x; q.y += z.y; q.z += z.z; q.w += z.w;
+  for (int k = 0; k < 2; ++k) {
+    if (!(last >> k & 1u)) continue;
+    const PagedItem g = words->cut[k];
+    for (int x = threadIdx.x; x < g.rows * (D / 4); x += blockDim.x) {
+      const int c4 = x / g.rows, row = x - c4 * g.rows;
+      const int at = c4 * kBM + row;
+      float4 v = __ldcg(paged_part<D>(a, g.c0, 1) + at);
+#pragma unroll 1
+      for (int i = 1; i < g.parts; i += 8) {  // eight loads in flight
+        float4 y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          y[j] = i + j < g.parts ? __ldcg(paged_part<D>(a, g.c0 + i + j, 0) + at)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v.x += y[j].x;
+          v.y += y[j].y;
+          v.z += y[j].z;
+          v.w += y[j].w;
         }
-        dst[u] = make_uint4(pack_bf16x2(p.x * a.inv_n, p.y * a.inv_n), pack_bf16x2(p.z * a.inv_n, p.w * a.inv_n),
-                            pack_bf16x2(q.x * a.inv_n, q.y * a.inv_n), pack_bf16x2(q.z * a.inv_n, q.w * a.inv_n));
       }
+      *reinterpret_cast<uint2*>(a.out + ((size_t)(g.row0 + row) * (size_t)a.w.heads + (size_t)g.h) * D +
+                                4 * c4) =
+          make_uint2(pack_bf16x2(v.x * a.inv_n, v.y * a.inv_n), pack_bf16x2(v.z * a.inv_n, v.w * a.inv_n));
     }
   }
 }
@@ -475,13 +509,15 @@ __global__ void __launch_bounds__(kFwdThreadsOf<D, 0>, 1)
     for (int i = 0; i < C::NBARS; ++i) mbar_init(bars + 8u * i, C::arrivals(i, kWideSilu<D, 0>));
     for (int j = 0; j < C::P; ++j) mbar_arrive(bars + 8u * (C::B_QKREADY + j));
     *abort_flag = 0;
+    words.cut[0].parts = words.cut[1].parts = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   PagedWork w = a.w;
   PagedCursor from;
+  PagedSeg first;
   // a CTA without work leaves before it allocates TMEM
-  if (!paged_locate(a.p, &w, a.min_units, &start, &g_dev_words[0], &from)) return;
+  if (!paged_locate(a.p, &w, a.min_units, &start, &g_dev_words[0], &from, &first)) return;
   if (warp == kMmaWarpQK) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
@@ -496,9 +532,9 @@ __global__ void __launch_bounds__(kFwdThreadsOf<D, 0>, 1)
   const WaitCtx wt{a.timeout_ns, abort_flag};
   const uint32_t steps = (uint32_t)(from.u1 - from.u);
   if (warp == kTmaWarpK) {
-    paged_producer<D, true>(&tm_k, &tm_q, a, w, from, &words, base, wt);
+    paged_producer<D, true>(&tm_k, &tm_q, a, w, from, first, &words, base, wt);
   } else if (warp == kTmaWarpV) {
-    paged_producer<D, false>(&tm_v, &tm_q, a, w, from, &words, base, wt);
+    paged_producer<D, false>(&tm_v, &tm_q, a, w, from, first, &words, base, wt);
   } else if (warp == kMmaWarpQK) {
     if (lane == 0) paged_mma_qk<D>(a, steps, &words, base, tmem, wt);
     __syncwarp();
@@ -518,6 +554,7 @@ __global__ void __launch_bounds__(kFwdThreadsOf<D, 0>, 1)
                  "r"(kTmemCols)
                  : "memory");
   }
+  paged_join<D>(a, &words, *abort_flag != 0);
 }
 
 template <int D>

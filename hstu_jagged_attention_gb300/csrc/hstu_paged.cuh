@@ -20,64 +20,96 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 
 template <int WARPS>
 struct PagedStart {
-  long long sums[WARPS];
-  int e, r;
+  int sums[WARPS];
+  int e, h, i;  // entry, head and block
+  int b, qt;
+  PagedSeq seq;
 };
 
+// Units of entries e .. e + 3 (0 past e1), their loads in flight together.
+__device__ __forceinline__ void paged_units4(const PagedView& p, const PagedWork& w, int e, int e1,
+                                             int (&units)[4], bool* bad) {
+  PagedRaw raw[4];
+  int qt[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int x = e + i < e1 ? e + i : e;
+    qt[i] = w.tiles == 1 ? 0 : x / p.batch;
+    raw[i] = paged_raw(p, x - qt[i] * p.batch);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    PagedSeq s;
+    if (!paged_check(p, raw[i], &s)) *bad = true;
+    units[i] = e + i < e1 ? w.heads * paged_walk(s, qt[i], w.tile_rows, w.kb_shift).nb : 0;
+  }
+}
+
 // Totals the work over all WARPS warps of the CTA and finds where its share
-// starts; false (for all of them) when it has none.  Synchronises the CTA.
+// starts, and its first entry's lengths (in *g); false (for all of them) when
+// it has none.  Synchronises the CTA.
 template <int WARPS>
 __device__ bool paged_locate(const PagedView& p, PagedWork* w, int min_units, PagedStart<WARPS>* m,
-                             unsigned* status, PagedCursor* c) {
+                             unsigned* status, PagedCursor* c, PagedSeg* g) {
   const int n = w->tiles * p.batch;
   const int each = (n + 32 * WARPS - 1) / (32 * WARPS);
   const int e0 = threadIdx.x * each, e1 = e0 + each < n ? e0 + each : n;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long sum = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int qt = e / p.batch, b = e - qt * p.batch;
-    PagedSeq s;
-    if (!paged_seq(p, b, &s) && blockIdx.x == 0) atomicOr(status, kStatusBadPaged);
-    sum += (long long)w->heads * paged_walk(s, qt, w->tile_rows, w->kb_shift).nb;
+  int sum = 0, units[4] = {0, 0, 0, 0};
+  bool bad = false;
+  for (int e = e0; e < e1; e += 4) {
+    paged_units4(p, *w, e, e1, units, &bad);
+    sum += units[0] + units[1] + units[2] + units[3];
   }
-  long long incl = sum;
+  if (bad && blockIdx.x == 0) atomicOr(status, kStatusBadPaged);
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
   if (lane == 31) m->sums[warp] = incl;
   __syncthreads();
-  long long before = 0, total = 0;
+  int before = 0, total = 0;
 #pragma unroll
   for (int i = 0; i < WARPS; ++i) {
     if (i < warp) before += m->sums[i];
     total += m->sums[i];
   }
   w->total = total;
-  w->per = paged_share(total, gridDim.x, min_units);
-  c->at = -1;
-  c->u = (long long)blockIdx.x * w->per;
+  w->per = paged_share(*w, p.batch, gridDim.x, min_units);
+  c->cta = blockIdx.x;
+  c->u = c->u0 = (int)blockIdx.x * w->per;
   if (c->u >= total) return false;
-  c->u1 = c->u + w->per < total ? c->u + w->per : total;
-  long long at = before + incl - sum;  // the thread's first unit
+  c->u1 = total - c->u > w->per ? c->u + w->per : total;
+  int at = before + incl - sum;  // the thread's first unit
   if (at <= c->u && c->u < at + sum) {
-    for (int e = e0; e < e1; ++e) {
-      const int qt = e / p.batch, b = e - qt * p.batch;
-      PagedSeq s;
-      paged_seq(p, b, &s);
-      const long long units = (long long)w->heads * paged_walk(s, qt, w->tile_rows, w->kb_shift).nb;
-      if (c->u < at + units) {
-        m->e = e;
-        m->r = (int)(c->u - at);
-        break;
-      }
-      at += units;
+    for (int e = e0; e < e1; e += 4) {
+      if (each > 4) paged_units4(p, *w, e, e1, units, &bad);  // else they are at hand
+      int i = 0;
+#pragma unroll 1
+      for (; i < 4 && c->u >= at + units[i]; ++i) at += units[i];
+      if (i == 4) continue;
+      c->e = e + i;
+      c->load(p, *w, g);
+      m->e = c->e;
+      m->h = (c->u - at) / g->walk.nb;
+      m->i = c->u - at - m->h * g->walk.nb;
+      m->b = g->b;
+      m->qt = g->qt;
+      m->seq = g->seq;
+      break;
     }
   }
   __syncthreads();
   c->e = m->e;
-  c->r = m->r;
+  c->h = m->h;
+  c->i = m->i;
+  c->loaded = true;
+  g->b = m->b;
+  g->qt = m->qt;
+  g->seq = m->seq;
+  g->walk = paged_walk(g->seq, g->qt, w->tile_rows, w->kb_shift);
   return true;
 }
 

@@ -31,23 +31,29 @@ struct PagedSeq {
   int hist;    // tokens that every candidate sees
 };
 
-// Sequence b; qn = 0 and false when its lengths contradict one another or
-// the arrays' bounds: nothing of such a sequence is read or written.
-HSTU_HD bool paged_seq(const PagedView& p, int b, PagedSeq* s) {
-  const int o0 = p.q_offsets[b], o1 = p.q_offsets[b + 1], kv = p.kv_lens[b];
-  const int nt = p.num_targets ? p.num_targets[b] : 0;
-  s->q0 = o0;
-  s->kv = kv;
-  s->hist = kv - nt;
+// Sequence b's four words, and what they say: qn = 0 and false when they
+// contradict one another or the arrays' bounds (nothing of such a sequence is
+// read or written).  Apart, so that several sequences' loads can be in flight.
+struct PagedRaw {
+  int o0, o1, kv, nt;
+};
+HSTU_HD PagedRaw paged_raw(const PagedView& p, int b) {
+  return PagedRaw{p.q_offsets[b], p.q_offsets[b + 1], p.kv_lens[b], p.num_targets ? p.num_targets[b] : 0};
+}
+HSTU_HD bool paged_check(const PagedView& p, const PagedRaw& r, PagedSeq* s) {
+  s->q0 = r.o0;
+  s->kv = r.kv;
+  s->hist = r.kv - r.nt;
   s->qn = 0;
   // with 0 <= o0 <= o1 the difference cannot overflow
-  if (o0 < 0 || o1 < o0 || o1 > p.rows) return false;
-  const int n = o1 - o0;
-  if (n > p.max_q || kv < n || nt < 0 || nt > n) return false;
-  if (kv > 0 && ((kv - 1) >> p.page_shift) >= p.max_pages) return false;
+  if (r.o0 < 0 || r.o1 < r.o0 || r.o1 > p.rows) return false;
+  const int n = r.o1 - r.o0;
+  if (n > p.max_q || r.kv < n || r.nt < 0 || r.nt > n) return false;
+  if (r.kv > 0 && ((r.kv - 1) >> p.page_shift) >= p.max_pages) return false;
   s->qn = n;
   return true;
 }
+HSTU_HD bool paged_seq(const PagedView& p, int b, PagedSeq* s) { return paged_check(p, paged_raw(p, b), s); }
 
 // The pool's row of token `pos` of sequence b; -1 when its page is out of range.
 HSTU_HD long long paged_slot(const PagedView& p, int b, int pos) {
@@ -110,12 +116,20 @@ HSTU_HD PagedWalk paged_walk(const PagedSeq& s, int qt, int tile_rows, int kb_sh
 // is summed from the CTAs' parts, in their order.
 struct PagedWork {
   int heads, tiles, tile_rows, kb_shift;
-  long long total, per;
+  int total, per;  // units (at most 2^30: the host checks) and units a CTA
 };
 
-HSTU_HD long long paged_share(long long total, int grid, int min_units) {
-  const long long per = (total + grid - 1) / grid;
-  return per > min_units ? per : min_units;
+// Units a CTA: an equal share, but no item cut into more than kMostParts parts
+// on average, which the last of its CTAs would sum alone.
+constexpr int kMostParts = 16;
+HSTU_HD int paged_share(const PagedWork& w, int batch, int grid, int min_units) {
+  const unsigned total = (unsigned)w.total, items = (unsigned)w.tiles * (unsigned)batch * (unsigned)w.heads;
+  unsigned per = (total + (unsigned)grid - 1u) / (unsigned)grid;
+  if (items < (unsigned)grid / kMostParts) {
+    const unsigned least = (total + kMostParts * items - 1u) / (kMostParts * items);
+    if (per < least) per = least;
+  }
+  return per > (unsigned)min_units ? (int)per : min_units;
 }
 
 struct PagedSeg {
@@ -126,39 +140,48 @@ struct PagedSeg {
   int c0, parts;        // the first CTA with a part of this item, and their number
 };
 
-// The segments of one CTA, from unit u (unit r of entry e) to u1.  The
-// entry's lengths are read once for all its heads: `at` is the entry that the
-// segment handed to next() holds (-1 before the first).
+// The segments of one CTA, units u0 .. u1 - 1: from block i of head h of entry
+// e on.  The entry's lengths are read once for all its heads; the segment
+// handed to next() keeps them (`loaded`: it already holds entry e's).
 struct PagedCursor {
-  long long u, u1;
-  int e, r, at;
+  int cta, u, u0, u1;
+  int e, h, i;
+  bool loaded;
+  HSTU_HD void load(const PagedView& p, const PagedWork& w, PagedSeg* g) const {
+    g->qt = w.tiles == 1 ? 0 : e / p.batch;
+    g->b = e - g->qt * p.batch;
+    paged_seq(p, g->b, &g->seq);
+    g->walk = paged_walk(g->seq, g->qt, w.tile_rows, w.kb_shift);
+  }
   HSTU_HD bool next(const PagedView& p, const PagedWork& w, PagedSeg* g) {
-    while (u < u1 && e < w.tiles * p.batch) {
-      if (at != e) {
-        at = e;
-        g->qt = e / p.batch;
-        g->b = e - g->qt * p.batch;
-        paged_seq(p, g->b, &g->seq);
-        g->walk = paged_walk(g->seq, g->qt, w.tile_rows, w.kb_shift);
-      }
-      const int nb = g->walk.nb;
-      if (r >= w.heads * nb) {
-        ++e;
-        r = 0;
-        continue;
-      }
-      g->h = r / nb;
-      g->i0 = r - g->h * nb;
-      g->n = nb - g->i0;
-      if (g->n > u1 - u) g->n = (int)(u1 - u);
-      const long long s = u - g->i0;  // the item's first unit
-      g->c0 = (int)(s / w.per);
-      g->parts = (int)((s + nb - 1) / w.per) - g->c0 + 1;
-      u += g->n;
-      r += g->n;
-      return true;
+    if (u >= u1) return false;
+    if (h == w.heads) {
+      h = 0;
+      ++e;
+      loaded = false;
     }
-    return false;
+    if (!loaded) {
+      for (;; ++e) {
+        if (e >= w.tiles * p.batch) return false;
+        load(p, w, g);
+        if (g->walk.nb) break;
+      }
+      loaded = true;
+    }
+    const int nb = g->walk.nb, s = u - i;  // the item's blocks and first unit
+    g->h = h;
+    g->i0 = i;
+    g->n = nb - i < u1 - u ? nb - i : u1 - u;
+    g->c0 = cta;
+    g->parts = 1;
+    if (s < u0 || s + nb > u1) {
+      g->c0 = s / w.per;
+      g->parts = (s + nb - 1) / w.per - g->c0 + 1;
+    }
+    u += g->n;
+    i = 0;
+    ++h;
+    return true;
   }
 };
 

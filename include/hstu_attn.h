@@ -625,7 +625,9 @@ int hstu_cache_destroy(hstu_cache* cache);
  *     num_targets[b] outside [0, n_b]: none of its rows is written;
  *   - a page number outside [0, num_pages): an append there is dropped, and
  *     the attention reads the page as zeros (its keys add nothing).
- * max_pages * page_size is at most 2^30.
+ * max_pages * page_size is at most 2^30, and so are the attention's units:
+ * the tiles of 16 or 128 rows in max_q, times batch, heads and blocks of 64 or
+ * 128 keys in max_pages (HSTU_ERR_INVALID_ARG).
  */
 typedef struct hstu_paged_batch {
   const int32_t* q_offsets;
@@ -659,7 +661,8 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
  * sequences, heads and the blocks a tile walks: those with a key before
  * hist that its last row may see, then its own keys' other blocks.  CTA c of
  * `grid` takes units [c per, (c + 1) per), per = max(ceil(units / grid),
- * min_units).  Segment i of host_dst is eight numbers: (CTA, sequence, head,
+ * min_units) or, with fewer than grid / 16 items = tiles * batch * heads, at
+ * least ceil(units / (16 items)): no item is cut into many more than 16.  Segment i of host_dst is eight numbers: (CTA, sequence, head,
  * tile, index of its first block in the walk, blocks, first CTA of the item,
  * CTAs that share the item).  tile_rows >= 1, block_keys a power of two.
  *   capacity    segments host_dst holds; NULL host_dst: count only.

@@ -136,7 +136,10 @@ def test_the_shares_cover_every_block_once(seed):
         assert v == list(range(expect[k]))
         assert sorted(c for c, _, _ in ctas[k]) == list(range(min(ctas[k])[1], min(ctas[k])[1] + min(ctas[k])[2]))
     total = sum(expect.values())
+    items = -(-batch.max_q // tile) * n * heads
     per = max(-(-total // grid), min_units)
+    if items < grid // 16:
+        per = max(per, -(-total // (16 * items)))
     assert all(u == per for c, u in units.items() if c != max(units)) and sum(units.values()) == total
     # a CTA starts at most one shared item that it does not end: its counter is free
     for c in units:
