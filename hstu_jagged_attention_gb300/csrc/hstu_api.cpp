@@ -523,7 +523,16 @@ long long schedule_items(const int32_t* cost, int n, int grid, int32_t* order, i
   return span;
 }
 
-int host_device_check(int* sm_count) { return device_check(sm_count); }
+// The answer is kept per device: it does not change.
+int host_device_check(int* sm_count) {
+  static std::atomic<int> known[64];  // SMs of an sm_103, 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (dev < 64 && (*sm_count = known[dev].load(std::memory_order_relaxed)) > 0) return HSTU_OK;
+  const int rc = device_check(sm_count);
+  if (rc == HSTU_OK && dev < 64) known[dev].store(*sm_count, std::memory_order_relaxed);
+  return rc;
+}
 unsigned long long host_wait_timeout_ns() { return wait_timeout_ns(); }
 unsigned host_debug_flags() {
   std::lock_guard<std::mutex> lk(g_mu);

@@ -621,8 +621,11 @@ cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, long long 
   const int bytes = a.stages * C::STAGEB + extra;
   const int grid = (int)std::min<long long>((long long)kPerSm * sms,
                                             (most + a.min_units - 1) / a.min_units);
-  const cudaError_t e = cudaFuncSetAttribute(step_kernel<D>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static DeviceOnce once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                64 * 1024 + step_red_bytes(kStepRows, D) + kStepTailBytes + 1024);
+  });
   if (e != cudaSuccess) return e;
   step_kernel<D><<<grid, kStepThreads, bytes, stream>>>(tk, tv, a);
   return cudaGetLastError();

@@ -561,8 +561,11 @@ template <int D>
 cudaError_t launch_paged_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PagedFwdArgs& a, int grid, cudaStream_t stream) {
   using C = Cfg<D>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      hstu_fwd_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_LAUNCH);
+  static DeviceOnce once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(hstu_fwd_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::SMEM_LAUNCH);
+  });
   if (e != cudaSuccess) return e;
   hstu_fwd_paged_kernel<D><<<grid, kFwdThreadsOf<D, 0>, C::SMEM_LAUNCH, stream>>>(tq, tk, tv, a);
   return cudaGetLastError();

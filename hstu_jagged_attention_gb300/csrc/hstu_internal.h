@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "hstu_paged.h"
 
 namespace hstu {
@@ -206,6 +208,25 @@ constexpr unsigned kStatusBadPaged = 2u;
 cudaError_t device_status_words(unsigned** words);
 // Wait sites of the cache's attention kernels (see device_status_words).
 constexpr int kSiteStepFull = 32, kSiteStepEmpty = 33;
+
+// Runs f, which returns a cudaError_t, on the first call of each device (and
+// again where it failed): a kernel's attributes are set once a device.
+class DeviceOnce {
+ public:
+  template <class F>
+  cudaError_t run(F f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done_.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    if ((e = f()) == cudaSuccess && dev < 64) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<unsigned long long> done_{0};
+};
 
 // Host helpers defined in hstu_api.cpp, shared with the other translation
 // units: argument checks, the launch, and (the current device's SMs) the
