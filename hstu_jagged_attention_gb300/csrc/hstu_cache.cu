@@ -158,19 +158,22 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 
 // ------------------------------------------------ attention of a few tokens
 // A tile is up to 16 new tokens of one (sequence, head); it walks blocks of 128
-// keys (64 at d = 128).  Warp 4 copies each block's K and V rows, page by page,
-// into a ring of shared-memory stages (bulk-tensor copies, swizzled rows).
-// Warps 0-3 take a quarter of the keys each: S = Q K^T, p = silu(alpha S),
-// O += p V on mma.sync m16n8k16, with p split into two bf16 terms as in the
-// forward, so that P V keeps 16 bits of p.  With so few rows the cache is read
+// keys.  The last warp copies each block's K and V rows, page by page, into a
+// ring of shared-memory stages (bulk-tensor copies, swizzled rows).  The other
+// four (eight at d = 128) take a part of the keys each: S = Q K^T,
+// p = silu(alpha S), O += p V on mma.sync m16n8k16, with p split into two bf16
+// terms as in the forward, so that P V keeps 16 bits of p.  With so few rows the cache is read
 // once for them all and the copies, not the products, set the time: a 128-row
 // tcgen05 tile would do the same reads with 8 times the products.
 constexpr int kStepRows = 16;
-constexpr int kStepWarps = 4;  // warps that compute
-constexpr int kStepThreads = 32 * (kStepWarps + 1);
-// Keys of a block: 32 a warp, two k16 steps whose chains of products overlap;
-// at d = 128 one step has as many products.
-constexpr int step_shift(int d) { return d == 128 ? 6 : 7; }
+constexpr int kStepKeys = 128, kStepShift = 7;
+// Warps that compute: 32 keys each, two k16 steps whose chains of products
+// overlap, or at d = 128 (where one step has as many products) 16.  One warp
+// more than a multiple of four puts two on one of the SM's four schedulers, so
+// two CTAs of five warps fit at 128 registers a thread, and at d = 128, with
+// 168, one CTA of nine.
+__host__ __device__ constexpr int step_warps(int d) { return d == 128 ? 8 : 4; }
+__host__ __device__ constexpr int step_per_sm(int d) { return d == 128 ? 1 : 2; }
 
 struct StepArgs {
   PagedView p;
@@ -238,9 +241,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 template <int D>
 struct StepCfg {
-  static constexpr int SHIFT = step_shift(D);
-  static constexpr int KEYS = 1 << SHIFT;
-  static constexpr int KW = KEYS / kStepWarps;  // keys of a warp: 16 or 32
+  static constexpr int WARPS = step_warps(D);
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int KEYS = kStepKeys;
+  static constexpr int KW = KEYS / WARPS;       // keys of a warp: 16 or 32
   static constexpr int CH = D < 64 ? D : 64;    // channels of a swizzled row
   static constexpr int NCH = D / CH;
   static constexpr int ROWB = CH * 2;
@@ -267,16 +271,17 @@ struct StepCfg {
 // 8 floats between rows, so that eight rows' 8-byte stores meet all banks
 __host__ __device__ constexpr int step_red_stride(int d) { return d + 8; }
 __host__ __device__ constexpr int step_red_bytes(int rows, int d) {
-  return kStepWarps * rows * step_red_stride(d) * (int)sizeof(float);
+  return step_warps(d) * rows * step_red_stride(d) * (int)sizeof(float);
 }
 constexpr int kStepTailBytes = 2 * 16 * 8 + 64 + 16 * 8;
 
+template <int WARPS>
 struct StepMisc {
   int abort_flag;
   unsigned last;  // bits: this CTA arrived last at the items it shares
-  PagedStart<kStepWarps + 1> start;
+  PagedStart<WARPS + 1> start;
 };
-static_assert(sizeof(StepMisc) <= 64 + 16 * 8, "misc");
+static_assert(sizeof(StepMisc<8>) <= 64 + 16 * 8, "misc");
 
 template <int D>
 __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const StepArgs& a,
@@ -294,7 +299,7 @@ __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const
     const int pages = (end + ps - 1) >> shift;  // of the sequence, as far as the tile sees
     PageIds ids;
     for (int i = 0; i < g.n; ++i) {
-      const int tok0 = g.walk.block(g.i0 + i) << C::SHIFT;
+      const int tok0 = g.walk.block(g.i0 + i) << kStepShift;
       const int p0 = tok0 >> shift;
       const int valid = end - tok0 < C::KEYS ? end - tok0 : C::KEYS;
       const int npg = ps >= C::KEYS ? 1 : (valid + ps - 1) >> shift;
@@ -339,8 +344,9 @@ drain:
   __syncwarp();
 }
 
+template <int WARPS>
 __device__ __forceinline__ void step_barrier() {  // the computing warps
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
 }
 
 // An item whose blocks several CTAs share.
@@ -368,7 +374,7 @@ __device__ __forceinline__ void step_store(uint16_t* out, int heads, int x, cons
 
 template <int D>
 __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor c, PagedSeg g, uint32_t base,
-                             uint32_t full, uint32_t empty, float* red, StepMisc* m,
+                             uint32_t full, uint32_t empty, float* red, StepMisc<step_warps(D)>* m,
                              const StepWait& wt) {
   using C = StepCfg<D>;
   constexpr int KS = C::KW / 16;  // k16 steps of the P V product
@@ -407,7 +413,7 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
       for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
 
     for (int i = 0; i < g.n; ++i) {
-      const int kb = g.walk.block(g.i0 + i) << C::SHIFT;
+      const int kb = g.walk.block(g.i0 + i) << kStepShift;
       if (!dead) dead = !__all_sync(0xffffffffu, step_wait(full + 8u * st, ph, wt, kSiteStepFull));
       const uint32_t ks = base + st * C::STAGEB + k_at, vs = base + st * C::STAGEB + v_at;
       float s[2 * KS][4];
@@ -495,7 +501,7 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
       }
     }
 
-    // the four warps' sums over their keys, then out or this CTA's part
+    // the warps' sums over their keys, then out or this CTA's part
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = 8 * r + g8;
@@ -506,15 +512,15 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
           *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
       }
     }
-    step_barrier();
+    step_barrier<C::WARPS>();
     dead = *static_cast<volatile int*>(&m->abort_flag) != 0;
     uint16_t* out = a.out + ((long long)g.seq.q0 * w.heads + g.h) * D;
     const bool before = g.c0 != (int)blockIdx.x;
     float* part = step_part<D>(a, blockIdx.x, !before);
-    for (int x = 4 * threadIdx.x; x < rows * D; x += 4 * 32 * kStepWarps) {
+    for (int x = 4 * threadIdx.x; x < rows * D; x += 4 * 32 * C::WARPS) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kStepWarps; ++i)
+      for (int i = 0; i < C::WARPS; ++i)
         add4(v, *reinterpret_cast<const float4*>(red + (i * a.red_rows + x / D) * RS + x % D));
       if (dead) continue;
       if (g.parts == 1)
@@ -529,7 +535,7 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
       else
         cut1 = cut;
     }
-    step_barrier();  // red is free for the next item
+    step_barrier<C::WARPS>();  // red is free for the next item
   }
   if (cut0.parts == 0 && cut1.parts == 0) return;
   // The last CTA to arrive at a cut item sums its parts in the CTAs' order, so
@@ -545,14 +551,14 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
     if (last & 2u) a.counters[cut1.c0] = 0;
     m->last = last;
   }
-  step_barrier();
+  step_barrier<C::WARPS>();
   const unsigned last = m->last;
   if (last) __threadfence();
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     if (!(last >> k & 1u)) continue;
     const StepCut cut = k ? cut1 : cut0;
-    for (int x = 4 * threadIdx.x; x < cut.rows * D; x += 4 * 32 * kStepWarps) {
+    for (int x = 4 * threadIdx.x; x < cut.rows * D; x += 4 * 32 * C::WARPS) {
       float4 v = __ldcg(reinterpret_cast<const float4*>(step_part<D>(a, cut.c0, true) + x));
 #pragma unroll 1
       for (int i = 1; i < cut.parts; i += 8) {  // eight loads in flight
@@ -571,7 +577,7 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kStepThreads)
+__global__ void __launch_bounds__(StepCfg<D>::THREADS)
     step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                 const StepArgs a) {
   using C = StepCfg<D>;
@@ -582,16 +588,16 @@ __global__ void __launch_bounds__(kStepThreads)
   float* red = reinterpret_cast<float*>(tail);
   uint8_t* after = tail + step_red_bytes(a.red_rows, D);
   const uint32_t full = smem_u32(after), empty = full + 8u * C::MAX_STAGES;
-  StepMisc* m = reinterpret_cast<StepMisc*>(after + 2 * C::MAX_STAGES * 8);
+  auto* m = reinterpret_cast<StepMisc<C::WARPS>*>(after + 2 * C::MAX_STAGES * 8);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x < a.stages) {
     mbar_init(full + 8u * threadIdx.x, 1);
-    mbar_init(empty + 8u * threadIdx.x, kStepWarps);
+    mbar_init(empty + 8u * threadIdx.x, C::WARPS);
     if (threadIdx.x == 0) m->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (threadIdx.x == 32 * kStepWarps) {
+  if (threadIdx.x == 32 * C::WARPS) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tk)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tv)) : "memory");
   }
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(kStepThreads)
   PagedSeg g;
   if (!paged_locate(a.p, &w, a.min_units, &m->start, a.status, &c, &g)) return;
   const StepWait wt{a.timeout_ns, &m->abort_flag, a.status};
-  if (warp == kStepWarps)
+  if (warp == C::WARPS)
     step_produce<D>(&tk, &tv, a, w, c, g, base, full, empty, wt);
   else
     step_compute<D>(a, w, c, g, base, full, empty, red, m, wt);
@@ -610,24 +616,24 @@ template <int D>
 cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, long long most, StepArgs a,
                         int sms, cudaStream_t stream) {
   using C = StepCfg<D>;
-  // Two CTAs an SM, 64 KB of copies in flight each.  More stages make every
-  // CTA's first block wait for the others' queued copies and leave more
-  // blocks to compute once the last bytes have landed: 512 sequences of
-  // log-normal lengths took 42.2 us with 2 stages of 32 KB, 44.2 with 3.
-  constexpr int kPerSm = 2;
-  a.stages = (64 * 1024) / C::STAGEB;
-  static_assert((64 * 1024) / C::STAGEB >= 2 && (64 * 1024) / C::STAGEB <= C::MAX_STAGES, "stages");
+  // 128 KB of copies in flight an SM.  More make every CTA's first block wait
+  // for the others' queued copies and leave more blocks to compute once the
+  // last bytes have landed: 512 sequences of log-normal lengths took 42.2 us
+  // with 2 stages of 32 KB a CTA, 44.2 with 3.
+  constexpr int PER_SM = step_per_sm(D), RING = 128 * 1024 / PER_SM;
+  a.stages = RING / C::STAGEB;
+  static_assert(RING / C::STAGEB >= 2 && RING / C::STAGEB <= C::MAX_STAGES, "stages");
   const int extra = step_red_bytes(a.red_rows, D) + kStepTailBytes + 1024;
   const int bytes = a.stages * C::STAGEB + extra;
-  const int grid = (int)std::min<long long>((long long)kPerSm * sms,
+  const int grid = (int)std::min<long long>((long long)PER_SM * sms,
                                             (most + a.min_units - 1) / a.min_units);
   static DeviceOnce once;
   const cudaError_t e = once.run([] {
     return cudaFuncSetAttribute(step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                64 * 1024 + step_red_bytes(kStepRows, D) + kStepTailBytes + 1024);
+                                RING + step_red_bytes(kStepRows, D) + kStepTailBytes + 1024);
   });
   if (e != cudaSuccess) return e;
-  step_kernel<D><<<grid, kStepThreads, bytes, stream>>>(tk, tv, a);
+  step_kernel<D><<<grid, C::THREADS, bytes, stream>>>(tk, tv, a);
   return cudaGetLastError();
 }
 
@@ -651,14 +657,14 @@ bool bad_ptr(const void* p, unsigned align) {
 }
 
 // The pool as (d, heads, page_size, num_pages) with box (min(d, 64), 1,
-// min(page_size, rows), 1) and the swizzle of a box row.
+// min(page_size, 128), 1) and the swizzle of a box row.
 int make_pool_map(CUtensorMap* m, void* ptr, int num_pages, int page_size, int heads, int d,
-                  long long page_stride, int rows) {
+                  long long page_stride) {
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)page_size,
                               (cuuint64_t)num_pages};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 2u, (cuuint64_t)heads * (cuuint64_t)d * 2u,
                                  (cuuint64_t)page_stride * 2u};
-  const cuuint32_t box[4] = {(cuuint32_t)std::min(d, 64), 1u, (cuuint32_t)std::min(page_size, rows), 1u};
+  const cuuint32_t box[4] = {(cuuint32_t)std::min(d, 64), 1u, (cuuint32_t)std::min(page_size, kStepKeys), 1u};
   return host_encode_map(m, ptr, 4, dims, strides, box, d >= 64);
 }
 
@@ -672,8 +678,7 @@ struct hstu_cache {
   long long page_stride;
   int device, sms;
   unsigned* status;
-  // boxes of 128 keys, and of a block of a few new tokens' kernel
-  CUtensorMap tk_tile, tv_tile, tk, tv;
+  CUtensorMap tk, tv;  // boxes of up to 128 keys, both kernels' blocks
 };
 
 namespace {
@@ -759,17 +764,9 @@ int hstu_cache_create(void* k_pages, void* v_pages, int num_pages, int page_size
   if (rc == HSTU_OK && cudaGetDevice(&c->device) != cudaSuccess) rc = HSTU_ERR_CUDA;
   if (rc == HSTU_OK && hstu::device_status_words(&c->status) != cudaSuccess) rc = HSTU_ERR_CUDA;
   if (rc == HSTU_OK)
-    rc = hstu::make_pool_map(&c->tk, k_pages, num_pages, page_size, heads, d, page_stride,
-                             1 << hstu::step_shift(d));
+    rc = hstu::make_pool_map(&c->tk, k_pages, num_pages, page_size, heads, d, page_stride);
   if (rc == HSTU_OK)
-    rc = hstu::make_pool_map(&c->tv, v_pages, num_pages, page_size, heads, d, page_stride,
-                             1 << hstu::step_shift(d));
-  if (rc == HSTU_OK)
-    rc = hstu::make_pool_map(&c->tk_tile, k_pages, num_pages, page_size, heads, d, page_stride,
-                             HSTU_BLOCK_N);
-  if (rc == HSTU_OK)
-    rc = hstu::make_pool_map(&c->tv_tile, v_pages, num_pages, page_size, heads, d, page_stride,
-                             HSTU_BLOCK_N);
+    rc = hstu::make_pool_map(&c->tv, v_pages, num_pages, page_size, heads, d, page_stride);
   if (rc != HSTU_OK) {
     delete c;
     return rc;
@@ -924,7 +921,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   w.heads = heads;
   w.tile_rows = tiled ? HSTU_BLOCK_M : hstu::kStepRows;
   w.tiles = (p.max_q + w.tile_rows - 1) / w.tile_rows;
-  w.kb_shift = tiled ? 7 : hstu::step_shift(d);
+  w.kb_shift = hstu::kStepShift;  // both kernels' blocks have 128 keys
   const long long most = units_bound(p, heads, w.tiles, w.kb_shift);
   if (most > kMostUnits) return HSTU_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -963,7 +960,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     a.timeout_ns = hstu::host_wait_timeout_ns();
     a.debug_flags = hstu::host_debug_flags();
     const int grid = (int)std::min<long long>(cache->sms, (most + a.min_units - 1) / a.min_units);
-    e = hstu::launch_fwd_paged(d, tq, cache->tk_tile, cache->tv_tile, a, grid, s);
+    e = hstu::launch_fwd_paged(d, tq, cache->tk, cache->tv, a, grid, s);
   } else {
     hstu::StepArgs a{};
     a.p = p;

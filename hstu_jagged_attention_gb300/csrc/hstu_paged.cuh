@@ -26,24 +26,27 @@ struct PagedStart {
   PagedSeq seq;
 };
 
-// Units of entries e .. e + 3 (0 past e1), their loads in flight together.
-__device__ __forceinline__ void paged_units4(const PagedView& p, const PagedWork& w, int e, int e1,
-                                             int (&units)[4], bool* bad) {
-  PagedRaw raw[4];
-  int qt[4];
+// Lengths and units (0 past e1) of entries e .. e + 3, their loads in flight
+// together.
+struct PagedFour {
+  PagedSeq seq[4];
+  int units[4];
+  __device__ __forceinline__ void load(const PagedView& p, const PagedWork& w, int e, int e1, bool* bad) {
+    PagedRaw raw[4];
+    int qt[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int x = e + i < e1 ? e + i : e;
-    qt[i] = w.tiles == 1 ? 0 : x / p.batch;
-    raw[i] = paged_raw(p, x - qt[i] * p.batch);
-  }
+    for (int i = 0; i < 4; ++i) {
+      const int x = e + i < e1 ? e + i : e;
+      qt[i] = w.tiles == 1 ? 0 : x / p.batch;
+      raw[i] = paged_raw(p, x - qt[i] * p.batch);
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    PagedSeq s;
-    if (!paged_check(p, raw[i], &s)) *bad = true;
-    units[i] = e + i < e1 ? w.heads * paged_walk(s, qt[i], w.tile_rows, w.kb_shift).nb : 0;
+    for (int i = 0; i < 4; ++i) {
+      if (!paged_check(p, raw[i], &seq[i])) *bad = true;
+      units[i] = e + i < e1 ? w.heads * paged_walk(seq[i], qt[i], w.tile_rows, w.kb_shift).nb : 0;
+    }
   }
-}
+};
 
 // Totals the work over all WARPS warps of the CTA and finds where its share
 // starts, and its first entry's lengths (in *g); false (for all of them) when
@@ -55,11 +58,12 @@ __device__ bool paged_locate(const PagedView& p, PagedWork* w, int min_units, Pa
   const int each = (n + 32 * WARPS - 1) / (32 * WARPS);
   const int e0 = threadIdx.x * each, e1 = e0 + each < n ? e0 + each : n;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int sum = 0, units[4] = {0, 0, 0, 0};
+  int sum = 0;
   bool bad = false;
+  PagedFour four;
   for (int e = e0; e < e1; e += 4) {
-    paged_units4(p, *w, e, e1, units, &bad);
-    sum += units[0] + units[1] + units[2] + units[3];
+    four.load(p, *w, e, e1, &bad);
+    sum += four.units[0] + four.units[1] + four.units[2] + four.units[3];
   }
   if (bad && blockIdx.x == 0) atomicOr(status, kStatusBadPaged);
   int incl = sum;
@@ -85,19 +89,30 @@ __device__ bool paged_locate(const PagedView& p, PagedWork* w, int min_units, Pa
   int at = before + incl - sum;  // the thread's first unit
   if (at <= c->u && c->u < at + sum) {
     for (int e = e0; e < e1; e += 4) {
-      if (each > 4) paged_units4(p, *w, e, e1, units, &bad);  // else they are at hand
-      int i = 0;
-#pragma unroll 1
-      for (; i < 4 && c->u >= at + units[i]; ++i) at += units[i];
-      if (i == 4) continue;
-      c->e = e + i;
-      c->load(p, *w, g);
+      if (each > 4) four.load(p, *w, e, e1, &bad);  // else they are at hand
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!found && c->u < at + four.units[i]) {
+          found = true;
+          c->e = e + i;
+          g->seq = four.seq[i];
+        }
+        if (!found) at += four.units[i];
+      }
+      if (!found) continue;
+      g->qt = w->tiles == 1 ? 0 : c->e / p.batch;
+      g->b = c->e - g->qt * p.batch;
+      g->walk = paged_walk(g->seq, g->qt, w->tile_rows, w->kb_shift);
       m->e = c->e;
       m->h = (c->u - at) / g->walk.nb;
       m->i = c->u - at - m->h * g->walk.nb;
       m->b = g->b;
       m->qt = g->qt;
       m->seq = g->seq;
+      // the producers read these next
+      const int page = (g->walk.block(m->i) << w->kb_shift) >> p.page_shift;
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.page_table + (long long)g->b * p.max_pages + page));
       break;
     }
   }

@@ -626,8 +626,8 @@ int hstu_cache_destroy(hstu_cache* cache);
  *   - a page number outside [0, num_pages): an append there is dropped, and
  *     the attention reads the page as zeros (its keys add nothing).
  * max_pages * page_size is at most 2^30, and so are the attention's units:
- * the tiles of 16 or 128 rows in max_q, times batch, heads and blocks of 64 or
- * 128 keys in max_pages (HSTU_ERR_INVALID_ARG).
+ * the tiles of 16 or 128 rows in max_q, times batch, heads and blocks of 128
+ * keys in max_pages (HSTU_ERR_INVALID_ARG).
  */
 typedef struct hstu_paged_batch {
   const int32_t* q_offsets;
