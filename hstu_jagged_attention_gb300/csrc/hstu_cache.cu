@@ -90,6 +90,7 @@ constexpr int kAppendThreads = 256;
 // once, with 16-byte accesses.  Bound by memory; a step of a few tokens by
 // the chain offsets -> lengths -> page -> store.
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  after_previous_kernel();
   const int per_head = a.d / 16, per_token = a.heads * per_head;
   const long long unit = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
   const long long tl = unit / per_token;
@@ -601,6 +602,7 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tk)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tv)) : "memory");
   }
+  after_previous_kernel();
   PagedWork w = a.w;
   PagedCursor c;
   PagedSeg g;
@@ -633,8 +635,7 @@ cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, long long 
                                 RING + step_red_bytes(kStepRows, D) + kStepTailBytes + 1024);
   });
   if (e != cudaSuccess) return e;
-  step_kernel<D><<<grid, C::THREADS, bytes, stream>>>(tk, tv, a);
-  return cudaGetLastError();
+  return launch_after(step_kernel<D>, grid, C::THREADS, bytes, stream, tk, tv, a);
 }
 
 cudaError_t launch_step_d(int d, const CUtensorMap& tk, const CUtensorMap& tv, long long most,
@@ -900,8 +901,8 @@ int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, co
   const long long units = (long long)a.p.rows * (width / 16);
   const long long grid = (units + hstu::kAppendThreads - 1) / hstu::kAppendThreads;
   if (grid > 0x7fffffffLL) return HSTU_ERR_INVALID_ARG;
-  hstu::append_kernel<<<(unsigned)grid, hstu::kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return hstu::status_of(cudaGetLastError());
+  return hstu::status_of(hstu::launch_after(hstu::append_kernel, (int)grid, hstu::kAppendThreads, 0,
+                                            reinterpret_cast<cudaStream_t>(stream), a));
 }
 
 int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, const void* q,

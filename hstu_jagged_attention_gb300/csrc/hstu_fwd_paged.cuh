@@ -513,6 +513,7 @@ __global__ void __launch_bounds__(kFwdThreadsOf<D, 0>, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  after_previous_kernel();
   PagedWork w = a.w;
   PagedCursor from;
   PagedSeg first;
@@ -567,6 +568,6 @@ cudaError_t launch_paged_d(const CUtensorMap& tq, const CUtensorMap& tk, const C
                                 C::SMEM_LAUNCH);
   });
   if (e != cudaSuccess) return e;
-  hstu_fwd_paged_kernel<D><<<grid, kFwdThreadsOf<D, 0>, C::SMEM_LAUNCH, stream>>>(tq, tk, tv, a);
-  return cudaGetLastError();
+  return launch_after(hstu_fwd_paged_kernel<D>, grid, kFwdThreadsOf<D, 0>, C::SMEM_LAUNCH, stream, tq, tk,
+                      tv, a);
 }

@@ -20,6 +20,7 @@
 
 #include "hstu_attn.h"
 #include "hstu_internal.h"
+#include "hstu_ptx.cuh"
 
 namespace {
 
@@ -113,6 +114,7 @@ constexpr int kFwdThreads = 256;
 
 template <int LANES, int NV, bool GATE, bool RES>
 __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(const NormFwdArgs a) {
+  hstu::after_previous_kernel();
   __shared__ float red[2 * kFwdThreads / 32];
   int turn = 0;
   const int lane = threadIdx.x % LANES;
@@ -249,8 +251,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_kernel(const NormBwdA
   const int group = threadIdx.x / LANES;
   constexpr int GROUPS = kBwdThreads / LANES;
   const float inv_w = 1.f / (float)a.width;
-  // the sums' kernel may be scheduled as this one's CTAs end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  hstu::after_previous_kernel();
   V8 gm[NV], bt[NV], dg[NV], db[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float* part
   __shared__ float acc[W][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = 32 * blockIdx.x + lane;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  hstu::after_previous_kernel();
   float s = 0.f;
   if (col < 2 * width) {
 #pragma unroll 5
@@ -430,14 +431,12 @@ template <int LANES, int NV>
 cudaError_t fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
   const int grid = norm_grid(a.rows, kFwdThreads / LANES, kFwdPerSm, sms);
   if (a.u && a.residual)
-    norm_fwd_kernel<LANES, NV, true, true><<<grid, kFwdThreads, 0, s>>>(a);
-  else if (a.u)
-    norm_fwd_kernel<LANES, NV, true, false><<<grid, kFwdThreads, 0, s>>>(a);
-  else if (a.residual)
-    norm_fwd_kernel<LANES, NV, false, true><<<grid, kFwdThreads, 0, s>>>(a);
-  else
-    norm_fwd_kernel<LANES, NV, false, false><<<grid, kFwdThreads, 0, s>>>(a);
-  return cudaGetLastError();
+    return hstu::launch_after(norm_fwd_kernel<LANES, NV, true, true>, grid, kFwdThreads, 0, s, a);
+  if (a.u)
+    return hstu::launch_after(norm_fwd_kernel<LANES, NV, true, false>, grid, kFwdThreads, 0, s, a);
+  if (a.residual)
+    return hstu::launch_after(norm_fwd_kernel<LANES, NV, false, true>, grid, kFwdThreads, 0, s, a);
+  return hstu::launch_after(norm_fwd_kernel<LANES, NV, false, false>, grid, kFwdThreads, 0, s, a);
 }
 
 template <int LANES, int NV, bool GATE, bool RES>
@@ -450,8 +449,7 @@ cudaError_t bwd_one(const NormBwdArgs& a, int grid, cudaStream_t s) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
   });
   if (e != cudaSuccess) return e;
-  norm_bwd_kernel<LANES, NV, GATE, RES><<<grid, kBwdThreads, BYTES, s>>>(a);
-  return cudaGetLastError();
+  return hstu::launch_after(norm_bwd_kernel<LANES, NV, GATE, RES>, grid, kBwdThreads, BYTES, s, a);
 }
 
 template <int LANES, int NV>
@@ -462,16 +460,8 @@ cudaError_t bwd(const NormBwdArgs& a, bool res, float* dgamma, float* dbeta, int
                         : res      ? bwd_one<LANES, NV, false, true>(a, grid, s)
                                    : bwd_one<LANES, NV, false, false>(a, grid, s);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((2 * a.width + 31) / 32));
-  cfg.blockDim = dim3(kSumThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_sum_kernel, (const float*)a.parts, grid, a.width, dgamma, dbeta);
+  return hstu::launch_after(norm_sum_kernel, (2 * a.width + 31) / 32, kSumThreads, 0, s, (const float*)a.parts,
+                            grid, a.width, dgamma, dbeta);
 }
 
 // The lanes and vectors a lane for a row of 8 nvec channels.  Forward: a warp

@@ -17,6 +17,31 @@ __host__ __device__ constexpr uint32_t make_idesc(int M, int N, int b_mn_major) 
 }
 
 // ----------------------------------------------------------------- PTX helpers
+// Kernels launched by launch_after (below) start while the stream's previous
+// kernel ends.  Every thread calls this before it touches global memory: it
+// returns when that kernel is done and its writes are visible.  What comes
+// before it (barriers, tensor maps) overlaps the previous kernel's end.
+__device__ __forceinline__ void after_previous_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t stream,
+                         const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
