@@ -21,6 +21,7 @@
 // item is at most 6 steps ahead of the PV issuer, and that at most two items
 // ahead of the epilogue: 16 item words are enough.
 constexpr int kStepWords = 8, kItemWords = 16;
+constexpr int kPagedThreads = 768;  // four SiLU warpgroups, the wide P layout, at every d
 struct PagedStep {
   int lim;    // position of the tile's first row, less the block's first key
   int hist;   // history end, less the block's first key
@@ -210,10 +211,8 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int kk = 4 * H + i;
-      const int hi_col = kWideSilu<D, 0> ? 16 * kk : 32 * (kk >> 1) + 8 * (kk & 1);
-      constexpr int lo_off = kWideSilu<D, 0> ? 8 : 16;
-      pa[2 * i] = pin32(tmem + (uint32_t)(J * 128 + hi_col));
-      pa[2 * i + 1] = pin32(tmem + (uint32_t)(J * 128 + hi_col + lo_off));
+      pa[2 * i] = pin32(tmem + (uint32_t)(J * 128 + 16 * kk));  // P_hi, then P_lo
+      pa[2 * i + 1] = pin32(tmem + (uint32_t)(J * 128 + 16 * kk + 8));
       vb[i] = pin64(v_desc0 + (uint64_t)((J * C::TILEB + kk * 2 * C::ATOMB) >> 4));
     }
     if (cols == kBN && (H == 1 || !start)) {
@@ -281,9 +280,9 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
   }
 }
 
-// SiLU warpgroups: as role_silu.  A masked block keeps key k for the row at
-// lim iff k <= lim and (k < lim_hist or k == lim); 16- or 32-key steps none
-// of whose keys a warp's rows keep are zeros without a load.
+// SiLU warpgroups: as role_silu's wide form.  A masked block keeps key k for
+// the row at lim iff k <= lim and (k < lim_hist or k == lim); 16-key steps
+// none of whose keys a warp's rows keep are zeros without a load.
 template <int D>
 __device__ void paged_silu(const PagedFwdArgs& a, uint32_t steps, const PagedWords* words, uint32_t base,
                            uint32_t tmem, const WaitCtx& wt, int warp, int lane) {
@@ -291,11 +290,8 @@ __device__ void paged_silu(const PagedFwdArgs& a, uint32_t steps, const PagedWor
   constexpr int P = C::P;
   const uint32_t bars = base + C::BAR_OFF;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
-  constexpr bool WIDE = kWideSilu<D, 0>;
-  constexpr int W = WIDE ? 16 : 32;  // keys of a step
   const int wg = (warp - kEwWarp0) >> 2;
-  const int e = WIDE ? wg >> 1 : wg;
-  const int half = WIDE ? wg & 1 : 0;
+  const int e = wg >> 1, half = wg & 1;  // every other step, half of its keys
   const int quarter = warp & 3;
   const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
   const float2 ha2 = make_float2(a.half_alpha, a.half_alpha);
@@ -310,58 +306,36 @@ __device__ void paged_silu(const PagedFwdArgs& a, uint32_t steps, const PagedWor
     const uint32_t t_s = lane_base + (uint32_t)(j * 128);
     if (quarter * 32 < st.rows) {
       if (st.plain()) {
-        if constexpr (WIDE) {
-          uint32_t w0[16], w1[16];
-          const uint32_t t_h = t_s + 64u * (uint32_t)half;
-          tmem_ld16_async(t_h, w0);
-          tmem_wait_ld16(w0);
+        uint32_t w0[16], w1[16];
+        const uint32_t t_h = t_s + 64u * (uint32_t)half;
+        tmem_ld16_async(t_h, w0);
+        tmem_wait_ld16(w0);
 #pragma unroll 1
-          for (int u = 0; u < 4; u += 2) {
-            tmem_ld16_async(t_h + 16u * (u + 1), w1);
-            silu_store16<0>(w0, ha2, 0, 0, t_h + 16u * u);
-            tmem_wait_ld16(w1);
-            if (u + 2 < 4) tmem_ld16_async(t_h + 16u * (u + 2), w0);
-            silu_store16<0>(w1, ha2, 0, 0, t_h + 16u * (u + 1));
-            if (u + 2 < 4) tmem_wait_ld16(w0);
-          }
-        } else {
-          uint32_t s0[32], s1[32];
-          tmem_ld32_async(t_s, s0);
-          tmem_wait_ld(s0);
-#pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            tmem_ld32_async(t_s + 32u * (c + 1), s1);
-            silu_store32<0>(s0, ha2, 0, 0, t_s + 32u * c);
-            tmem_wait_ld(s1);
-            if (c + 2 < 4) tmem_ld32_async(t_s + 32u * (c + 2), s0);
-            silu_store32<0>(s1, ha2, 0, 0, t_s + 32u * (c + 1));
-            if (c + 2 < 4) tmem_wait_ld(s0);
-          }
+        for (int u = 0; u < 4; u += 2) {
+          tmem_ld16_async(t_h + 16u * (u + 1), w1);
+          silu_store16<0>(w0, ha2, 0, 0, t_h + 16u * u);
+          tmem_wait_ld16(w1);
+          if (u + 2 < 4) tmem_ld16_async(t_h + 16u * (u + 2), w0);
+          silu_store16<0>(w1, ha2, 0, 0, t_h + 16u * (u + 1));
+          if (u + 2 < 4) tmem_wait_ld16(w0);
         }
       } else {
         const int cols = st.cols();
         // the warp's rows stand at lim0 .. lim0 + 31, this lane's at lim0 + lane
         const int lim0 = st.lim + 32 * quarter;
         const int hist0 = st.hist;
-        const int k0 = WIDE ? 64 * half : 0, k1 = WIDE ? 64 * half + 64 : kBN;
 #pragma unroll 1
-        for (int k = k0; k < k1 && k < cols; k += W) {
+        for (int k = 64 * half; k < 64 * half + 64 && k < cols; k += 16) {
           const uint32_t t_k = t_s + (uint32_t)k;
-          if (k > lim0 + 31 || (k >= hist0 && k + W <= lim0)) {
-            uint32_t z[16];
+          uint32_t s[16];
+          if (k > lim0 + 31 || (k >= hist0 && k + 16 <= lim0)) {
 #pragma unroll
-            for (int m = 0; m < 16; ++m) z[m] = 0u;
-            tmem_st16(t_k, z);
-            if constexpr (!WIDE) tmem_st16(t_k + 16u, z);
-          } else if constexpr (WIDE) {
-            uint32_t s[16];
+            for (int m = 0; m < 16; ++m) s[m] = 0u;
+            tmem_st16(t_k, s);
+          } else {
             tmem_ld16_async(t_k, s);
             tmem_wait_ld16(s);
             silu_store16<2>(s, ha2, lim0 + lane - k, hist0 - k, t_k);
-          } else {
-            uint32_t s[32];
-            tmem_ld32(t_k, s);
-            silu_store32<2>(s, ha2, lim0 + lane - k, hist0 - k, t_k);
           }
         }
       }
@@ -394,25 +368,34 @@ __device__ void paged_epilogue(const PagedFwdArgs& a, uint32_t steps, PagedWords
     const uint32_t o_t = tmem + lane_off + C::O_COL + (uint32_t)(ob * D);
     const bool live = row < g.rows;
     if (g.parts == 1) {
-      uint32_t packed[D / 2];
+      uint4* dst = reinterpret_cast<uint4*>(
+          a.out + ((size_t)(g.row0 + row) * (size_t)a.w.heads + (size_t)g.h) * D);
+      // 64 columns at a time (the registers of 768 threads); the O buffer is
+      // released before the last ones are stored
+      constexpr int PIECE = D < 64 ? D : 64;
 #pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t o[32];
-        tmem_ld32(o_t + 32u * cc, o);
+      for (int c0 = 0; c0 < D; c0 += PIECE) {
+        uint32_t packed[PIECE / 2];
 #pragma unroll
-        for (int m = 0; m < 16; ++m)
-          packed[16 * cc + m] =
-              pack_bf16x2(__uint_as_float(o[2 * m]) * a.inv_n, __uint_as_float(o[2 * m + 1]) * a.inv_n);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + ob));
-      if (live) {
-        uint4* dst = reinterpret_cast<uint4*>(
-            a.out + ((size_t)(g.row0 + row) * (size_t)a.w.heads + (size_t)g.h) * D);
+        for (int cc = 0; cc < PIECE / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(o_t + (uint32_t)c0 + 32u * cc, o);
 #pragma unroll
-        for (int u = 0; u < D / 8; ++u)
-          dst[u] = make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
+          for (int m = 0; m < 16; ++m)
+            packed[16 * cc + m] =
+                pack_bf16x2(__uint_as_float(o[2 * m]) * a.inv_n, __uint_as_float(o[2 * m + 1]) * a.inv_n);
+        }
+        if (c0 + PIECE == D) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + ob));
+        }
+        if (live) {
+#pragma unroll
+          for (int u = 0; u < PIECE / 8; ++u)
+            dst[c0 / 8 + u] =
+                make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
+        }
       }
       continue;
     }
@@ -490,11 +473,11 @@ __device__ void paged_join(const PagedFwdArgs& a, PagedWords* words, bool dead) 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kFwdThreadsOf<D, 0>, 1)
+__global__ void __launch_bounds__(kPagedThreads, 1)
     hstu_fwd_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const PagedFwdArgs a) {
   using C = Cfg<D>;
-  constexpr int WARPS = kFwdThreadsOf<D, 0> / 32;
+  constexpr int WARPS = kPagedThreads / 32;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PagedStart<WARPS> start;
   __shared__ PagedWords words;
@@ -506,7 +489,7 @@ __global__ void __launch_bounds__(kFwdThreadsOf<D, 0>, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bars = base + C::BAR_OFF;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NBARS; ++i) mbar_init(bars + 8u * i, C::arrivals(i, kWideSilu<D, 0>));
+    for (int i = 0; i < C::NBARS; ++i) mbar_init(bars + 8u * i, C::arrivals(i, true));
     for (int j = 0; j < C::P; ++j) mbar_arrive(bars + 8u * (C::B_QKREADY + j));
     *abort_flag = 0;
     words.cut[0].parts = words.cut[1].parts = 0;
@@ -568,6 +551,6 @@ cudaError_t launch_paged_d(const CUtensorMap& tq, const CUtensorMap& tk, const C
                                 C::SMEM_LAUNCH);
   });
   if (e != cudaSuccess) return e;
-  return launch_after(hstu_fwd_paged_kernel<D>, grid, kFwdThreadsOf<D, 0>, C::SMEM_LAUNCH, stream, tq, tk,
+  return launch_after(hstu_fwd_paged_kernel<D>, grid, kPagedThreads, C::SMEM_LAUNCH, stream, tq, tk,
                       tv, a);
 }
