@@ -703,11 +703,20 @@ def _refuse(t, dtype, shape, device, what: str):
 
 
 def _row_stride(t, shape, device, what: str) -> int:
-    """Elements between rows of a bf16 device tensor of ``shape`` whose rows
-    are packed (a slice of a wider projection has a larger row stride)."""
+    """Elements between rows of a bf16 device tensor of ``shape`` (rows, width)
+    or (rows, heads, d), whose rows are packed (a slice of a wider projection
+    has a larger row stride)."""
     if t.dtype is not _bf16 or t.device != device or t.shape != shape:
         _refuse(t, _bf16, shape, device, what)
-    step, width = t.stride(), 1
+    step = t.stride()
+    if step[-1] != 1 or (len(step) > 2 and step[-2] != shape[-1]) or shape[0] <= 1:
+        return _odd_row_stride(step, shape, what)
+    return step[0]
+
+
+def _odd_row_stride(step, shape, what: str) -> int:
+    """As _row_stride, where a dimension of one entry may have any stride."""
+    width = 1
     for i in range(len(shape) - 1, 0, -1):
         if step[i] != width and shape[i] != 1:
             raise ValueError(f"{what}: the values of a row must be packed")
@@ -808,8 +817,10 @@ def hstu_cache_create(k_pages, v_pages) -> Cache:
     shape = k_pages.shape
     if len(shape) != 4 or not k_pages.is_cuda:
         raise ValueError("k_pages must be a device tensor (num_pages, page_size, heads, d)")
-    stride = _row_stride(k_pages, shape, k_pages.device, "k_pages")
-    if _row_stride(v_pages, shape, k_pages.device, "v_pages") != stride:
+    _refuse(k_pages, _bf16, shape, k_pages.device, "k_pages")
+    _refuse(v_pages, _bf16, shape, k_pages.device, "v_pages")
+    stride = _odd_row_stride(k_pages.stride(), shape, "k_pages")
+    if _odd_row_stride(v_pages.stride(), shape, "v_pages") != stride:
         raise ValueError("k_pages and v_pages must have the same page stride")
     h = _VP()
     _check(lib().hstu_cache_create(k_pages.data_ptr(), v_pages.data_ptr(), *shape, stride,
@@ -958,6 +969,17 @@ def hstu_norm_bwd_workspace_bytes(width: int) -> int:
     return n.value
 
 
+_norm_workspace = {}  # (device, width) -> bytes
+
+
+def _norm_workspace_bytes(device, width: int) -> int:
+    n = _norm_workspace.get((device.index, width))
+    if n is None:
+        with _torch.cuda.device(device):
+            n = _norm_workspace[device.index, width] = hstu_norm_bwd_workspace_bytes(width)
+    return n
+
+
 def hstu_norm_bwd(dy, z, gamma, beta, eps: float, dz, dgamma, dbeta, u=None, du=None, dz_in=None,
                   dx=None, scale: float = 1.0, workspace=None, stream=None) -> None:
     """Gradients of hstu_norm_fwd for ``dy``: ``dz`` of the norm's input ``z``
@@ -978,7 +1000,7 @@ def hstu_norm_bwd(dy, z, gamma, beta, eps: float, dz, dgamma, dbeta, u=None, du=
     if dx is not None:
         dxa = _packed(dx, shape, dev, "dx")
     if workspace is not None:
-        ws = _space(workspace, dev, hstu_norm_bwd_workspace_bytes(width), "workspace")
+        ws = _space(workspace, dev, _norm_workspace_bytes(dev, width), "workspace")
     code = lib().hstu_norm_bwd(dy.data_ptr(), dys, z.data_ptr(), zs, ua, us,
                                _vector(gamma, width, dev, "gamma"), _vector(beta, width, dev, "beta"), eps,
                                da, ds, scale, rows, width, _packed(dz, shape, dev, "dz"), dxa, dua, dus,

@@ -397,7 +397,8 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
     uint32_t qf[D / 16][4];
     {
       const int r0 = g8, r1 = r0 + 8;
-      const uint16_t* x0 = a.q + (long long)(g.seq.q0 + r0) * a.q_stride + (long long)g.h * D + 2 * t4;
+      const uint16_t* x0 =
+          a.q + (long long)(g.seq.q0 + kStepRows * g.qt + r0) * a.q_stride + (long long)g.h * D + 2 * t4;
       const uint16_t* x1 = x0 + 8 * a.q_stride;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -515,7 +516,7 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
     }
     step_barrier<C::WARPS>();
     dead = *static_cast<volatile int*>(&m->abort_flag) != 0;
-    uint16_t* out = a.out + ((long long)g.seq.q0 * w.heads + g.h) * D;
+    uint16_t* out = a.out + ((long long)(g.seq.q0 + kStepRows * g.qt) * w.heads + g.h) * D;
     const bool before = g.c0 != (int)blockIdx.x;
     float* part = step_part<D>(a, blockIdx.x, !before);
     for (int x = 4 * threadIdx.x; x < rows * D; x += 4 * 32 * C::WARPS) {
@@ -714,6 +715,19 @@ long long units_bound(const PagedView& v, int heads, int tiles, int kb_shift) {
   const long long blocks = (((long long)v.max_pages << v.page_shift) >> kb_shift) + 2;
   const long long entries = (long long)tiles * v.batch;
   return entries > INT32_MAX || entries * heads > INT32_MAX ? LLONG_MAX : entries * heads * blocks;
+}
+
+// Whether more than one tile of 16 rows goes to the 128-row tcgen05 tiles
+// instead.  Those take about 4 us more to fill their pipeline and less per
+// block: 32 rows, 4 heads, d = 64 took 6.9 us as 16-row tiles and 10.5 as one
+// tile on 600 keys, 10.5 and 13.3 on 8 x 2000, 24.2 and 24.4 on 16 x 4096, 70
+// and 61 on 64 x 4096; 64 rows 15.3 and 16.5 on 8 x 2000, 36.7 and 26.0 on
+// 16 x 4096.  At d = 128 the blocks cost more: 32 rows 11.0 and 13.5 on
+// 4 x 2000, 19.0 and 16.7 on 8 x 2000.  `units`: blocks of the 16-row tiles, at
+// most.
+bool use_tiles(const PagedView& v, int d, int sms, long long units) {
+  if (v.max_q <= hstu::kStepRows) return false;
+  return v.max_q > 64 || units > (d == 128 ? 5LL : 20LL) * sms;
 }
 
 int check_geometry(int num_pages, int page_size, int* shift) {
@@ -918,11 +932,15 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   if (bad_rows(q, q_stride, (long long)heads * d) || hstu::bad_ptr(out, 16)) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_device(cache)) != HSTU_OK) return rc;
   hstu::PagedWork w{};
-  const bool tiled = p.max_q > hstu::kStepRows;
   w.heads = heads;
-  w.tile_rows = tiled ? HSTU_BLOCK_M : hstu::kStepRows;
+  w.tile_rows = hstu::kStepRows;
   w.tiles = (p.max_q + w.tile_rows - 1) / w.tile_rows;
   w.kb_shift = hstu::kStepShift;  // both kernels' blocks have 128 keys
+  const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift));
+  if (tiled) {
+    w.tile_rows = HSTU_BLOCK_M;
+    w.tiles = (p.max_q + w.tile_rows - 1) / w.tile_rows;
+  }
   const long long most = units_bound(p, heads, w.tiles, w.kb_shift);
   if (most > kMostUnits) return HSTU_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

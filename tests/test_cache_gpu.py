@@ -120,6 +120,23 @@ def test_attention_parity(name, d, heads, page):
     s.check(out)
 
 
+@pytest.mark.parametrize("d,heads,page", [(32, 2, 32), (64, 3, 16), (128, 1, 128)])
+@pytest.mark.parametrize("name", ["one token", "few tokens, some without", "candidates",
+                                  "17 to 32 tokens"])
+def test_few_rows_on_large_tiles(name, d, heads, page):
+    # a bound on the new tokens that asks for 128-row tiles, with few rows in them
+    hist, new, nt = SHAPES[name]
+    s = Setup(hist, new, page, heads, d, nt, seed=20 + d, pad=1, max_q=130)
+    s.check(s.attend())
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("new,targets", [(33, 0), (47, 47), (64, 20)])
+def test_several_small_tiles(d, new, targets):
+    s = Setup([0, 140, 300], [new, 1, 17], 64, 2, d, [targets, 0, 17], seed=30 + d)
+    s.check(s.attend())
+
+
 @pytest.mark.parametrize("max_q", [1, 4, 16, 32, 33, 500])
 def test_max_q_changes_the_tiling_not_the_result(max_q):
     s = Setup([90, 300, 5], [1, 1, 1], 32, 2, 64, seed=1, max_q=max_q)
