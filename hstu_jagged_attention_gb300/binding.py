@@ -134,7 +134,8 @@ _SIGNATURES = {
     "hstu_cache_destroy": (_INT, [_VP]),
     "hstu_cache_workspace": (_INT, [_VP, ctypes.POINTER(ctypes.c_size_t)]),
     "hstu_cache_slots": (_INT, [_PBP, _INT, _INT, ctypes.POINTER(_I64), _I32P]),
-    "hstu_cache_worklist": (_INT, [_PBP, _INT, _INT, _INT, _INT, _INT, _INT, _INT, _I32P, _INT, _IP]),
+    "hstu_cache_worklist": (_INT, [_PBP, _INT, _INT, _INT, _INT, _INT, _INT, _INT, _INT, _I32P, _INT,
+                                   _IP]),
     "hstu_cache_append": (_INT, [_VP, _PBP, _VP, _I64, _VP, _I64, _VP, _I64, _ROTP, _VP, _VP]),
     "hstu_attn_fwd_cache": (_INT, [_VP, _PBP, _VP, _I64, _F32, _F32, _VP, _VP, _VP]),
     "hstu_norm_fwd": (_INT, [_VP, _I64, _VP, _I64, _F32, _VP, _I64, _VP, _VP, _F32, _I64, _INT, _VP, _VP,
@@ -906,14 +907,15 @@ def hstu_cache_slots(batch: PagedBatch, num_pages: int, page_size: int, rows: in
 
 
 def hstu_cache_worklist(batch: PagedBatch, num_pages: int, page_size: int, rows: int, heads: int,
-                        tile_rows: int, block_keys: int, grid: int, min_units: int = 1) -> np.ndarray:
+                        tile_rows: int, block_keys: int, grid: int, min_units: int = 1,
+                        extra: int = 1) -> np.ndarray:
     """Host-only (no CUDA call; a batch of numpy arrays): the shares of
     hstu_attn_fwd_cache's CTAs, int32 (n, 8): CTA, sequence, head, tile, first
     block, blocks, first CTA of the item, CTAs that share it."""
     if not batch.host:
         raise ValueError("hstu_cache_worklist takes a batch of numpy arrays")
     args = (batch.struct(rows), int(num_pages), int(page_size), int(heads), int(tile_rows),
-            int(block_keys), int(grid), int(min_units))
+            int(block_keys), int(extra), int(grid), int(min_units))
     n = ctypes.c_int()
     _check(lib().hstu_cache_worklist(*args, None, 0, ctypes.byref(n)), "hstu_cache_worklist")
     buf = np.zeros((max(n.value, 1), 8), dtype=np.int32)

@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS)
   PagedWork w = a.w;
   PagedCursor c;
   PagedSeg g;
-  if (!paged_locate(a.p, &w, a.min_units, &m->start, a.status, &c, &g)) return;
+  if (!paged_locate<C::WARPS + 1, false>(a.p, &w, a.min_units, &m->start, a.status, &c, &g)) return;
   const StepWait wt{a.timeout_ns, &m->abort_flag, a.status};
   if (warp == C::WARPS)
     step_produce<D>(&tk, &tv, a, w, c, g, base, full, empty, wt);
@@ -710,9 +710,17 @@ int check_batch(const hstu_paged_batch* b, PagedView* v, int num_pages, int page
 }
 
 constexpr long long kMostUnits = 1 << 30;
+
+// Units for what an item costs besides its blocks (its queries' load, the
+// pipeline's filling, its rows' way out).  With 0, 1, 2 and 3 of them, 16 x
+// 4096 tokens from an empty cache (items of 1 to 32 blocks) took 300, 242, 249
+// and 252 us at d = 64, and 16 ragged chunks 76.8, 73.1, 69.9 and 70.8 us at
+// d = 128; 512 single tokens 43.1, 42.2, 43.1 and 44.7.
+constexpr int item_units(int d) { return d == 128 ? 2 : 1; }
+
 // Units of a launch, at most: a tile walks every block of its sequence once.
-long long units_bound(const PagedView& v, int heads, int tiles, int kb_shift) {
-  const long long blocks = (((long long)v.max_pages << v.page_shift) >> kb_shift) + 2;
+long long units_bound(const PagedView& v, int heads, int tiles, int kb_shift, int extra) {
+  const long long blocks = (((long long)v.max_pages << v.page_shift) >> kb_shift) + 2 + extra;
   const long long entries = (long long)tiles * v.batch;
   return entries > INT32_MAX || entries * heads > INT32_MAX ? LLONG_MAX : entries * heads * blocks;
 }
@@ -829,26 +837,27 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
 }
 
 int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int page_size, int heads,
-                        int tile_rows, int block_keys, int grid, int min_units, int32_t* host_dst,
+                        int tile_rows, int block_keys, int extra, int grid, int min_units, int32_t* host_dst,
                         int capacity, int* n_segments) {
   int shift = 0;
   if (check_geometry(num_pages, page_size, &shift) != HSTU_OK) return HSTU_ERR_INVALID_ARG;
   if (!n_segments || heads < 1 || tile_rows < 1 || block_keys < 1 || (block_keys & (block_keys - 1)) ||
-      grid < 1 || min_units < 1 || capacity < 0)
+      extra < 0 || extra > 64 || grid < 1 || min_units < 1 || capacity < 0)
     return HSTU_ERR_INVALID_ARG;
   PagedView v;
   const int rc = check_batch(host_batch, &v, num_pages, shift);
   if (rc != HSTU_OK) return rc;
   hstu::PagedWork w{};
   w.heads = heads;
+  w.extra = extra;
   w.tile_rows = tile_rows;
   w.tiles = v.rows > 0 && v.batch > 0 ? (v.max_q + tile_rows - 1) / tile_rows : 0;
   while ((1 << w.kb_shift) < block_keys) ++w.kb_shift;
-  if (units_bound(v, heads, w.tiles, w.kb_shift) > kMostUnits) return HSTU_ERR_INVALID_ARG;
+  if (units_bound(v, heads, w.tiles, w.kb_shift, extra) > kMostUnits) return HSTU_ERR_INVALID_ARG;
   auto units_of = [&](int e) {
     hstu::PagedSeq s;
     hstu::paged_seq(v, e % v.batch, &s);
-    return heads * hstu::paged_walk(s, e / v.batch, tile_rows, w.kb_shift).nb;
+    return hstu::paged_units(w, hstu::paged_walk(s, e / v.batch, tile_rows, w.kb_shift).nb);
   };
   for (int e = 0; e < w.tiles * v.batch; ++e) w.total += units_of(e);
   w.per = hstu::paged_share(w, v.batch, grid, min_units);
@@ -863,8 +872,8 @@ int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int p
     hstu::PagedSeg g;
     c.load(v, w, &g);
     c.loaded = true;
-    c.h = (c.u - at) / g.walk.nb;
-    c.i = c.u - at - c.h * g.walk.nb;
+    c.h = (c.u - at) / (g.walk.nb + extra);
+    c.i = c.u - at - c.h * (g.walk.nb + extra);
     while (c.next(v, w, &g)) {
       if (host_dst) {
         if (n >= capacity) return HSTU_ERR_INVALID_ARG;
@@ -936,12 +945,13 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   w.tile_rows = hstu::kStepRows;
   w.tiles = (p.max_q + w.tile_rows - 1) / w.tile_rows;
   w.kb_shift = hstu::kStepShift;  // both kernels' blocks have 128 keys
-  const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift));
+  w.extra = item_units(d);
+  const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra));
   if (tiled) {
     w.tile_rows = HSTU_BLOCK_M;
     w.tiles = (p.max_q + w.tile_rows - 1) / w.tile_rows;
   }
-  const long long most = units_bound(p, heads, w.tiles, w.kb_shift);
+  const long long most = units_bound(p, heads, w.tiles, w.kb_shift, w.extra);
   if (most > kMostUnits) return HSTU_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CUtensorMap tq;

@@ -500,8 +500,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   PagedWork w = a.w;
   PagedCursor from;
   PagedSeg first;
+  int n_steps;
   // a CTA without work leaves before it allocates TMEM
-  if (!paged_locate(a.p, &w, a.min_units, &start, &g_dev_words[0], &from, &first)) return;
+  if (!paged_locate<WARPS, true>(a.p, &w, a.min_units, &start, &g_dev_words[0], &from, &first, &n_steps)) return;
   if (warp == kMmaWarpQK) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wt{a.timeout_ns, abort_flag};
-  const uint32_t steps = (uint32_t)(from.u1 - from.u);
+  const uint32_t steps = (uint32_t)n_steps;
   if (warp == kTmaWarpK) {
     paged_producer<D, true>(&tm_k, &tm_q, a, w, from, first, &words, base, wt);
   } else if (warp == kTmaWarpV) {

@@ -20,9 +20,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 
 template <int WARPS>
 struct PagedStart {
-  int sums[WARPS];
-  int e, h, i;  // entry, head and block
-  int b, qt;
+  int2 sums[WARPS];  // units and blocks
+  int r0, r1;        // blocks before the share and before its end
+  int e, h, i;       // entry, head and unit
   PagedSeq seq;
 };
 
@@ -30,7 +30,7 @@ struct PagedStart {
 // together.
 struct PagedFour {
   PagedSeq seq[4];
-  int units[4];
+  int units[4], nb[4];
   __device__ __forceinline__ void load(const PagedView& p, const PagedWork& w, int e, int e1, bool* bad) {
     PagedRaw raw[4];
     int qt[4];
@@ -43,86 +43,98 @@ struct PagedFour {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (!paged_check(p, raw[i], &seq[i])) *bad = true;
-      units[i] = e + i < e1 ? w.heads * paged_walk(seq[i], qt[i], w.tile_rows, w.kb_shift).nb : 0;
+      nb[i] = e + i < e1 ? paged_walk(seq[i], qt[i], w.tile_rows, w.kb_shift).nb : 0;
+      units[i] = paged_units(w, nb[i]);
     }
   }
 };
 
 // Totals the work over all WARPS warps of the CTA and finds where its share
 // starts, and its first entry's lengths (in *g); false (for all of them) when
-// it has none.  Synchronises the CTA.
-template <int WARPS>
+// it has none.  COUNT: also its blocks, in *steps (a share without blocks is
+// none).  Synchronises the CTA.
+template <int WARPS, bool COUNT>
 __device__ bool paged_locate(const PagedView& p, PagedWork* w, int min_units, PagedStart<WARPS>* m,
-                             unsigned* status, PagedCursor* c, PagedSeg* g) {
+                             unsigned* status, PagedCursor* c, PagedSeg* g, int* steps = nullptr) {
   const int n = w->tiles * p.batch;
   const int each = (n + 32 * WARPS - 1) / (32 * WARPS);
   const int e0 = threadIdx.x * each, e1 = e0 + each < n ? e0 + each : n;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int sum = 0;
+  int sum = 0, blocks = 0;
   bool bad = false;
   PagedFour four;
   for (int e = e0; e < e1; e += 4) {
     four.load(p, *w, e, e1, &bad);
-    sum += four.units[0] + four.units[1] + four.units[2] + four.units[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum += four.units[i];
+      if (COUNT) blocks += w->heads * four.nb[i];
+    }
   }
   if (bad && blockIdx.x == 0) atomicOr(status, kStatusBadPaged);
-  int incl = sum;
+  int incl = sum, bincl = blocks;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
+    if (COUNT) {
+      const int y = __shfl_up_sync(0xffffffffu, bincl, o);
+      if (lane >= o) bincl += y;
+    }
   }
-  if (lane == 31) m->sums[warp] = incl;
+  if (lane == 31) m->sums[warp] = make_int2(incl, bincl);
   __syncthreads();
-  int before = 0, total = 0;
+  int2 before = make_int2(0, 0), total = before;
 #pragma unroll
   for (int i = 0; i < WARPS; ++i) {
-    if (i < warp) before += m->sums[i];
-    total += m->sums[i];
+    const int2 x = m->sums[i];
+    if (i < warp) {
+      before.x += x.x;
+      before.y += x.y;
+    }
+    total.x += x.x;
+    total.y += x.y;
   }
-  w->total = total;
+  w->total = total.x;
   w->per = paged_share(*w, p.batch, gridDim.x, min_units);
   c->cta = blockIdx.x;
   c->u = c->u0 = (int)blockIdx.x * w->per;
-  if (c->u >= total) return false;
-  c->u1 = total - c->u > w->per ? c->u + w->per : total;
-  int at = before + incl - sum;  // the thread's first unit
-  if (at <= c->u && c->u < at + sum) {
+  if (c->u >= total.x) return false;
+  c->u1 = total.x - c->u > w->per ? c->u + w->per : total.x;
+  if (COUNT && threadIdx.x == 0 && c->u1 == total.x) m->r1 = total.y;
+  int at = before.x + incl - sum, done = before.y + bincl - blocks;  // before the thread's entries
+  if ((at <= c->u && c->u < at + sum) || (COUNT && at <= c->u1 && c->u1 < at + sum)) {
     for (int e = e0; e < e1; e += 4) {
       if (each > 4) four.load(p, *w, e, e1, &bad);  // else they are at hand
-      bool found = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (!found && c->u < at + four.units[i]) {
-          found = true;
-          c->e = e + i;
-          g->seq = four.seq[i];
+        const int units = four.units[i], nb = four.nb[i];
+        if (COUNT && at <= c->u1 && c->u1 < at + units) m->r1 = done + paged_blocks(*w, nb, c->u1 - at);
+        if (at <= c->u && c->u < at + units) {
+          const int r = c->u - at;
+          const int h = r / (nb + w->extra);
+          m->e = e + i;
+          m->h = h;
+          m->i = r - h * (nb + w->extra);
+          if (COUNT) m->r0 = done + paged_blocks(*w, nb, r);
+          m->seq = four.seq[i];
         }
-        if (!found) at += four.units[i];
+        at += units;
+        done += w->heads * nb;
       }
-      if (!found) continue;
-      g->qt = w->tiles == 1 ? 0 : c->e / p.batch;
-      g->b = c->e - g->qt * p.batch;
-      g->walk = paged_walk(g->seq, g->qt, w->tile_rows, w->kb_shift);
-      m->e = c->e;
-      m->h = (c->u - at) / g->walk.nb;
-      m->i = c->u - at - m->h * g->walk.nb;
-      m->b = g->b;
-      m->qt = g->qt;
-      m->seq = g->seq;
-      // the producers read these next
-      const int page = (g->walk.block(m->i) << w->kb_shift) >> p.page_shift;
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.page_table + (long long)g->b * p.max_pages + page));
-      break;
     }
   }
   __syncthreads();
+  if (COUNT) {
+    *steps = m->r1 - m->r0;
+    if (*steps == 0) return false;
+  }
   c->e = m->e;
   c->h = m->h;
   c->i = m->i;
   c->loaded = true;
-  g->b = m->b;
-  g->qt = m->qt;
+  g->qt = w->tiles == 1 ? 0 : c->e / p.batch;
+  g->b = c->e - g->qt * p.batch;
   g->seq = m->seq;
   g->walk = paged_walk(g->seq, g->qt, w->tile_rows, w->kb_shift);
   return true;

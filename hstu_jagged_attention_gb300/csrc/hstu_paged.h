@@ -111,11 +111,12 @@ HSTU_HD PagedWalk paged_walk(const PagedSeq& s, int qt, int tile_rows, int kb_sh
 // The work of a launch: entries (query tile qt, sequence b), qt outermost, so
 // that CTAs that run at the same time on different tiles of a sequence read
 // the same keys; within an entry the heads, within a head the key blocks.
-// Each block is one unit, and CTA c takes units [c per, (c + 1) per): equal
-// shares, whatever the lengths.  A (tile, sequence, head) cut by a share's end
-// is summed from the CTAs' parts, in their order.
+// Each block is one unit, then come `extra` units without work, for what an
+// item costs besides its blocks; CTA c takes units [c per, (c + 1) per): equal
+// shares, whatever the lengths.  A (tile, sequence, head) whose blocks a
+// share's end cuts is summed from the CTAs' parts, in their order.
 struct PagedWork {
-  int heads, tiles, tile_rows, kb_shift;
+  int heads, tiles, tile_rows, kb_shift, extra;
   int total, per;  // units (at most 2^30: the host checks) and units a CTA
 };
 
@@ -132,6 +133,14 @@ HSTU_HD int paged_share(const PagedWork& w, int batch, int grid, int min_units) 
   return per > (unsigned)min_units ? (int)per : min_units;
 }
 
+// Units of an entry whose tile walks nb blocks, and the blocks among its
+// first r units.
+HSTU_HD int paged_units(const PagedWork& w, int nb) { return nb ? w.heads * (nb + w.extra) : 0; }
+HSTU_HD int paged_blocks(const PagedWork& w, int nb, int r) {
+  const int h = r / (nb + w.extra), i = r - h * (nb + w.extra);
+  return h * nb + (i < nb ? i : nb);
+}
+
 struct PagedSeg {
   PagedSeq seq;
   PagedWalk walk;
@@ -140,7 +149,7 @@ struct PagedSeg {
   int c0, parts;        // the first CTA with a part of this item, and their number
 };
 
-// The segments of one CTA, units u0 .. u1 - 1: from block i of head h of entry
+// The segments of one CTA, units u0 .. u1 - 1: from unit i of head h of entry
 // e on.  The entry's lengths are read once for all its heads; the segment
 // handed to next() keeps them (`loaded`: it already holds entry e's).
 struct PagedCursor {
@@ -154,19 +163,25 @@ struct PagedCursor {
     g->walk = paged_walk(g->seq, g->qt, w.tile_rows, w.kb_shift);
   }
   HSTU_HD bool next(const PagedView& p, const PagedWork& w, PagedSeg* g) {
-    if (u >= u1) return false;
-    if (h == w.heads) {
-      h = 0;
-      ++e;
-      loaded = false;
-    }
-    if (!loaded) {
-      for (;; ++e) {
-        if (e >= w.tiles * p.batch) return false;
-        load(p, w, g);
-        if (g->walk.nb) break;
+    for (;;) {
+      if (u >= u1) return false;
+      if (h == w.heads) {
+        h = 0;
+        ++e;
+        loaded = false;
       }
-      loaded = true;
+      if (!loaded) {
+        for (;; ++e) {
+          if (e >= w.tiles * p.batch) return false;
+          load(p, w, g);
+          if (g->walk.nb) break;
+        }
+        loaded = true;
+      }
+      if (i < g->walk.nb) break;
+      u += g->walk.nb + w.extra - i;  // the share starts behind the item's blocks
+      i = 0;
+      ++h;
     }
     const int nb = g->walk.nb, s = u - i;  // the item's blocks and first unit
     g->h = h;
@@ -178,7 +193,7 @@ struct PagedCursor {
       g->c0 = s / w.per;
       g->parts = (s + nb - 1) / w.per - g->c0 + 1;
     }
-    u += g->n;
+    u = s + nb + w.extra;  // a cut item ends the share
     i = 0;
     ++h;
     return true;

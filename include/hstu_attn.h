@@ -626,8 +626,8 @@ int hstu_cache_destroy(hstu_cache* cache);
  *   - a page number outside [0, num_pages): an append there is dropped, and
  *     the attention reads the page as zeros (its keys add nothing).
  * max_pages * page_size is at most 2^30, and so are the attention's units:
- * the tiles of 16 or 128 rows in max_q, times batch, heads and blocks of 128
- * keys in max_pages (HSTU_ERR_INVALID_ARG).
+ * the tiles of 16 or 128 rows in max_q, times batch, heads and (a few more
+ * than) the blocks of 128 keys in max_pages (HSTU_ERR_INVALID_ARG).
  */
 typedef struct hstu_paged_batch {
   const int32_t* q_offsets;
@@ -659,8 +659,9 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
  * A unit is one block of block_keys keys of one (tile of tile_rows new
  * tokens, sequence, head); units are numbered with tiles outermost, then
  * sequences, heads and the blocks a tile walks: those with a key before
- * hist that its last row may see, then its own keys' other blocks.  CTA c of
- * `grid` takes units [c per, (c + 1) per), per = max(ceil(units / grid),
+ * hist that its last row may see, then its own keys' other blocks.  After an
+ * item's blocks come `extra` (0 .. 64) units without work, for what an item
+ * costs besides them.  CTA c of `grid` takes units [c per, (c + 1) per), per = max(ceil(units / grid),
  * min_units) or, with fewer than grid / 16 items = tiles * batch * heads, at
  * least ceil(units / (16 items)): no item is cut into many more than 16.  Segment i of host_dst is eight numbers: (CTA, sequence, head,
  * tile, index of its first block in the walk, blocks, first CTA of the item,
@@ -670,7 +671,7 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
  * Errors: HSTU_ERR_INVALID_ARG for bad arguments or a short capacity.
  */
 int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int page_size, int heads,
-                        int tile_rows, int block_keys, int grid, int min_units, int32_t* host_dst,
+                        int tile_rows, int block_keys, int extra, int grid, int min_units, int32_t* host_dst,
                         int capacity, int* n_segments);
 
 /*

@@ -112,8 +112,10 @@ def test_the_shares_cover_every_block_once(seed):
     tile, keys = [(16, 64), (32, 64), (128, 128)][seed % 3]
     heads, grid = int(rng.integers(1, 5)), int(rng.integers(1, 60))
     min_units = int(rng.integers(1, 6))
+    extra = int(rng.integers(0, 4))
     batch, num_pages, rows = make_batch(hist, new, 32, nt, seed)
-    segs = binding.hstu_cache_worklist(batch, num_pages, 32, rows, heads, tile, keys, grid, min_units)
+    segs = binding.hstu_cache_worklist(batch, num_pages, 32, rows, heads, tile, keys, grid, min_units,
+                                       extra)
     # every key that a row may see lies in exactly one unit of its (tile, head)
     expect = {}
     for b in range(n):
@@ -135,12 +137,21 @@ def test_the_shares_cover_every_block_once(seed):
     for k, v in got.items():
         assert v == list(range(expect[k]))
         assert sorted(c for c, _, _ in ctas[k]) == list(range(min(ctas[k])[1], min(ctas[k])[1] + min(ctas[k])[2]))
-    total = sum(expect.values())
+    # equal shares of blocks and `extra` units an item, in that order
+    total = sum(m + extra for m in expect.values() if m)
     items = -(-batch.max_q // tile) * n * heads
     per = max(-(-total // grid), min_units)
     if items < grid // 16:
         per = max(per, -(-total // (16 * items)))
-    assert all(u == per for c, u in units.items() if c != max(units)) and sum(units.values()) == total
+    want, at = {}, 0
+    for qt in range(-(-batch.max_q // tile)):
+        for b in range(n):
+            for h in range(heads):
+                m = expect.get((b, h, qt), 0)
+                for i in range(m):
+                    want[(at + i) // per] = want.get((at + i) // per, 0) + 1
+                at += m + extra if m else 0
+    assert units == want
     # a CTA starts at most one shared item that it does not end: its counter is free
     for c in units:
         assert sum(1 for x in segs.tolist() if x[0] == c and x[6] == c and x[7] > 1) <= 1
