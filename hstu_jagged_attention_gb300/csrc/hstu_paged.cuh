@@ -104,25 +104,36 @@ __device__ bool paged_locate(const PagedView& p, PagedWork* w, int min_units, Pa
   if (COUNT && threadIdx.x == 0 && c->u1 == total.x) m->r1 = total.y;
   int at = before.x + incl - sum, done = before.y + bincl - blocks;  // before the thread's entries
   if ((at <= c->u && c->u < at + sum) || (COUNT && at <= c->u1 && c->u1 < at + sum)) {
+    // the entries that hold the share's first unit and the one behind its last
+    int nb0 = 0, r0 = 0, done0 = 0, nb1 = 0, r1 = 0, done1 = 0;
     for (int e = e0; e < e1; e += 4) {
       if (each > 4) four.load(p, *w, e, e1, &bad);  // else they are at hand
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int units = four.units[i], nb = four.nb[i];
-        if (COUNT && at <= c->u1 && c->u1 < at + units) m->r1 = done + paged_blocks(*w, nb, c->u1 - at);
+        const int units = four.units[i];
         if (at <= c->u && c->u < at + units) {
-          const int r = c->u - at;
-          const int h = r / (nb + w->extra);
+          nb0 = four.nb[i];
+          r0 = c->u - at;
+          done0 = done;
           m->e = e + i;
-          m->h = h;
-          m->i = r - h * (nb + w->extra);
-          if (COUNT) m->r0 = done + paged_blocks(*w, nb, r);
           m->seq = four.seq[i];
         }
+        if (COUNT && at <= c->u1 && c->u1 < at + units) {
+          nb1 = four.nb[i];
+          r1 = c->u1 - at;
+          done1 = done;
+        }
         at += units;
-        done += w->heads * nb;
+        if (COUNT) done += w->heads * four.nb[i];
       }
     }
+    if (nb0) {
+      const int h = r0 / (nb0 + w->extra), i = r0 - h * (nb0 + w->extra);
+      m->h = h;
+      m->i = i;
+      if (COUNT) m->r0 = done0 + h * nb0 + (i < nb0 ? i : nb0);
+    }
+    if (COUNT && nb1) m->r1 = done1 + paged_blocks(*w, nb1, r1);
   }
   __syncthreads();
   if (COUNT) {

@@ -125,7 +125,10 @@ struct PagedWork {
 constexpr int kMostParts = 16;
 HSTU_HD int paged_share(const PagedWork& w, int batch, int grid, int min_units) {
   const unsigned total = (unsigned)w.total, items = (unsigned)w.tiles * (unsigned)batch * (unsigned)w.heads;
-  unsigned per = (total + (unsigned)grid - 1u) / (unsigned)grid;
+  // ceil(total / grid), from the fp32 quotient (a few off for the largest totals)
+  unsigned per = (unsigned)((float)total / (float)grid);
+  while (per * (unsigned)grid < total) ++per;
+  while (per > 0 && (per - 1u) * (unsigned)grid >= total) --per;
   if (items < (unsigned)grid / kMostParts) {
     const unsigned least = (total + kMostParts * items - 1u) / (kMostParts * items);
     if (per < least) per = least;
