@@ -886,8 +886,8 @@ def hstu_attn_fwd_cache(cache: Cache, batch: PagedBatch, q, alpha: float, inv_n:
     qs = _row_stride(q, shape, dev, "q")
     o = _packed(out, shape, dev, "out")
     ws = _space(workspace, dev, cache.workspace_bytes, "workspace")
-    code = lib().hstu_attn_fwd_cache(cache.handle, batch.struct(rows), q.data_ptr(), qs, alpha, inv_n, o,
-                                     ws, _cuda_stream(stream, dev))
+    code = lib().hstu_attn_fwd_cache(cache.handle, batch.struct(rows), q.data_ptr(), qs, float(alpha),
+                                     float(inv_n), o, ws, _cuda_stream(stream, dev))
     if code:
         _check(code, "hstu_attn_fwd_cache")
 
@@ -938,7 +938,10 @@ def _rows_of(t, what: str):
         _load_torch()
     if t.ndim != 2 or not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor (rows, width)")
-    return t.shape, t.device
+    device = t.device
+    if device.index != _torch._C._cuda_getDevice():
+        raise ValueError(f"{what} is on {device}, which is not the current device")
+    return t.shape, device
 
 
 def hstu_norm_fwd(x, gamma, beta, eps: float, y, u=None, residual=None, scale: float = 1.0, z=None,
@@ -957,8 +960,9 @@ def hstu_norm_fwd(x, gamma, beta, eps: float, y, u=None, residual=None, scale: f
         ua, us = u.data_ptr(), _row_stride(u, shape, dev, "u")
     if z is not None:
         za = _packed(z, shape, dev, "z")
-    code = lib().hstu_norm_fwd(x.data_ptr(), xs, ra, rs, scale, ua, us, _vector(gamma, width, dev, "gamma"),
-                               _vector(beta, width, dev, "beta"), eps, rows, width,
+    code = lib().hstu_norm_fwd(x.data_ptr(), xs, ra, rs, float(scale), ua, us,
+                               _vector(gamma, width, dev, "gamma"), _vector(beta, width, dev, "beta"),
+                               float(eps), rows, width,
                                _packed(y, shape, dev, "y"), za, _cuda_stream(stream, dev))
     if code:
         _check(code, "hstu_norm_fwd")
@@ -1004,8 +1008,8 @@ def hstu_norm_bwd(dy, z, gamma, beta, eps: float, dz, dgamma, dbeta, u=None, du=
     if workspace is not None:
         ws = _space(workspace, dev, _norm_workspace_bytes(dev, width), "workspace")
     code = lib().hstu_norm_bwd(dy.data_ptr(), dys, z.data_ptr(), zs, ua, us,
-                               _vector(gamma, width, dev, "gamma"), _vector(beta, width, dev, "beta"), eps,
-                               da, ds, scale, rows, width, _packed(dz, shape, dev, "dz"), dxa, dua, dus,
+                               _vector(gamma, width, dev, "gamma"), _vector(beta, width, dev, "beta"),
+                               float(eps), da, ds, float(scale), rows, width, _packed(dz, shape, dev, "dz"), dxa, dua, dus,
                                _vector(dgamma, width, dev, "dgamma"), _vector(dbeta, width, dev, "dbeta"),
                                ws, _cuda_stream(stream, dev))
     if code:

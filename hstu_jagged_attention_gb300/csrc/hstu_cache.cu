@@ -190,6 +190,7 @@ struct StepArgs {
   float* parts;
   unsigned* status;
   unsigned long long timeout_ns;
+  unsigned debug_flags;
 };
 
 struct StepWait {
@@ -392,6 +393,9 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
   uint32_t ph = 0;
   bool dead = false;  // the CTA gave up: run on without waits, store nothing
   StepCut cut0{}, cut1{};  // items shared with earlier, and with later, CTAs
+  // test hook: the barrier behind the stages' is never arrived on
+  if (a.debug_flags & kDebugUnsignalledWait)
+    dead = !__all_sync(0xffffffffu, step_wait(full + 8u * C::MAX_STAGES - 8u, 0, wt, kSiteUnsignalledStep));
   while (c.next(a.p, w, &g)) {
     const int rows = g.walk.rows;
     uint32_t qf[D / 16][4];
@@ -595,7 +599,10 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS)
   if (threadIdx.x < a.stages) {
     mbar_init(full + 8u * threadIdx.x, 1);
     mbar_init(empty + 8u * threadIdx.x, C::WARPS);
-    if (threadIdx.x == 0) m->abort_flag = 0;
+    if (threadIdx.x == 0) {
+      m->abort_flag = 0;
+      mbar_init(full + 8u * C::MAX_STAGES - 8u, 1);  // for the test hook alone: a.stages < MAX_STAGES
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -625,7 +632,7 @@ cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, long long 
   // with 2 stages of 32 KB a CTA, 44.2 with 3.
   constexpr int PER_SM = step_per_sm(D), RING = 128 * 1024 / PER_SM;
   a.stages = RING / C::STAGEB;
-  static_assert(RING / C::STAGEB >= 2 && RING / C::STAGEB <= C::MAX_STAGES, "stages");
+  static_assert(RING / C::STAGEB >= 2 && RING / C::STAGEB < C::MAX_STAGES, "stages");
   const int extra = step_red_bytes(a.red_rows, D) + kStepTailBytes + 1024;
   const int bytes = a.stages * C::STAGEB + extra;
   const int grid = (int)std::min<long long>((long long)PER_SM * sms,
@@ -1005,6 +1012,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     a.parts = parts;
     a.status = cache->status;
     a.timeout_ns = hstu::host_wait_timeout_ns();
+    a.debug_flags = hstu::host_debug_flags();
     e = hstu::launch_step_d(d, cache->tk, cache->tv, most, a, cache->sms, s);
   }
   rc = hstu::status_of(e);

@@ -207,7 +207,7 @@ constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusBadPaged = 2u;
 cudaError_t device_status_words(unsigned** words);
 // Wait sites of the cache's attention kernels (see device_status_words).
-constexpr int kSiteStepFull = 32, kSiteStepEmpty = 33;
+constexpr int kSiteStepFull = 32, kSiteStepEmpty = 33, kSiteUnsignalledStep = 34;
 
 // Runs f, which returns a cudaError_t, on the first call of each device (and
 // again where it failed): a kernel's attributes are set once a device.

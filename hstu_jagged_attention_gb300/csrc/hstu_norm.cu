@@ -403,8 +403,17 @@ __global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float* part
   hstu::after_previous_kernel();
   float s = 0.f;
   if (col < 2 * width) {
-#pragma unroll 5
-    for (int i = warp; i < n; i += W) s += __ldcg(parts + (long long)i * 2 * width + col);
+    // ten loads in flight: all of a warp's share of 152 CTAs
+    for (int i0 = warp; i0 < n; i0 += 10 * W) {
+      float x[10];
+#pragma unroll
+      for (int k = 0; k < 10; ++k) {
+        const int i = i0 + k * W;
+        x[k] = i < n ? __ldcg(parts + (long long)i * 2 * width + col) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 10; ++k) s += x[k];
+    }
   }
   acc[warp][lane] = s;
   __syncthreads();

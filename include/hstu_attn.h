@@ -764,6 +764,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
  *              given exactly when residual is; may be residual or x if packed.
  *   width      a multiple of 8, 8 .. HSTU_NORM_MAX_WIDTH.
  *   scale      finite; used with residual.
+ * Device memory is the current device's throughout.
  *
  * hstu_norm_bwd  for dy, with z the norm's input (x without residual), as
  * stored, and g = dy (.) u, xhat the normalised row:
@@ -843,8 +844,8 @@ int hstu_set_wait_timeout_ns(uint64_t ns);
  *   HSTU_DEBUG_BWD_ROWS  run the backward in its row form (query rows on
  *       the TMEM lanes) where it would run in its transposed form (key rows
  *       on the lanes: d <= 64 without the bias), for comparing the two.
- * The unsignalled wait applies to the forward and to the backward's
- * transposed form.
+ * The unsignalled wait applies to the forward, to the backward's transposed
+ * form and to the attention over a cache.
  * Errors: HSTU_ERR_INVALID_ARG for unknown bits.
  */
 #define HSTU_DEBUG_UNSIGNALLED_WAIT 1u

@@ -419,6 +419,27 @@ def test_growing_by_steps_is_the_forward_over_the_whole():
         assert np.all(np.abs(layer.f64(x) - ref64) <= 2.0 ** -8 * np.abs(ref64) + bound)
 
 
+@pytest.mark.parametrize("new", [1, 70])
+def test_a_wait_that_runs_out_is_reported(new):
+    # both kernels give up at a barrier nothing signals, write nothing, and
+    # leave a device (and, zeroed again, a workspace) that works
+    s = Setup([900, 40], [new, 1], 32, 2, 64, seed=40 + new)
+    good, ws = s.attend(), s.workspace()
+    torch.cuda.synchronize()
+    binding.hstu_set_wait_timeout_ns(20_000_000)
+    binding.hstu_set_debug_flags(binding.HSTU_DEBUG_UNSIGNALLED_WAIT)
+    try:
+        out = s.attend(workspace=ws)
+        status, site = binding.hstu_last_status()
+    finally:
+        binding.hstu_set_debug_flags(0)
+        binding.hstu_set_wait_timeout_ns(0)
+    assert status == binding.HSTU_ERR_TIMEOUT and site != 0
+    assert (out == 7.0).all()
+    ws.zero_()
+    assert torch.equal(s.attend(workspace=ws), good)
+
+
 def test_refusals():
     s = Setup([10], [2], 16, 2, 64, seed=13)
     q, out = s.q.cuda(), torch.empty(2, 2, 64, device="cuda", dtype=torch.bfloat16)
