@@ -26,20 +26,31 @@ __device__ __forceinline__ void after_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// cluster: CTAs of a thread-block cluster (0: no clusters).
 template <class... Params, class... Args>
-cudaError_t launch_after(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t stream,
-                         const Args&... args) {
+cudaError_t launch_after_in_clusters(int cluster, void (*kernel)(Params...), int grid, int threads, int smem,
+                                     cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t stream,
+                         const Args&... args) {
+  return launch_after_in_clusters(0, kernel, grid, threads, smem, stream, args...);
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

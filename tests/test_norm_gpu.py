@@ -132,6 +132,17 @@ def test_many_rows_and_repeats():
     assert all(torch.equal(o[n], p[n]) for n in o)
 
 
+@pytest.mark.parametrize("width,rows", [(64, 1024), (64, 1025), (256, 255), (256, 256), (256, 257),
+                                        (520, 64), (520, 65), (8192, 16), (8192, 17)])
+def test_one_cluster_and_many_ctas(width, rows):
+    # on both sides of where one cluster takes the whole gradient
+    a, dy, dz_in = make(rows, width, True, True, seed=rows)
+    dev = to_gpu(a)
+    _, z = run_fwd(dev, EPS, 0.5)
+    o = run_bwd(dy.cuda(), z, dev, EPS, dz_in.cuda(), True, 0.5)
+    check_bwd(o, dy, z, a, EPS, dz_in, 0.5)
+
+
 def test_rows_with_a_large_mean_and_with_no_spread():
     a, dy, _ = make(50, 256, True, False, seed=2, offset=30.0)
     a["x"][7] = 3.0   # no spread at all: xhat = 0
