@@ -7,14 +7,20 @@
 //   - equal shares of (tile, sequence, head, key block) units per CTA, so an
 //     item may be cut between CTAs; its parts are summed in their order by
 //     the CTA that arrives last.
+// Bound by the same stages as the forward (SiLU on the MUFU and the issue
+// slots, the split P's products; ncu: MUFU 47%, issue 55%, tensor pipe 37%
+// busy): 1024 candidates of 32 users against 2048 to 8192 tokens, 4 heads of
+// 64, take 289 us (167 GFLOP, 578 TF/s), 1.03 us a 128 x 128 block; at d = 128
+// 1.6 to 1.8 us a block (chunks of 100 to 700 tokens: 70 us, 578 TF/s).
 // Included by hstu_fwd.cu.
 
 // What the K producer, which runs ahead of every other role, leaves in shared
 // memory for them: a word per step (key block) and one per item.  Each role
 // then follows the CTA's steps 0 .. n - 1 with no schedule of its own: with
 // the cursor inlined in every role, the kernel missed the instruction cache
-// (73.7% hits, 88% of the cache's fill bandwidth) and 1024 candidates of 32
-// users took 494 us.
+// (73.7% hits, 88% of the cache's fill bandwidth) and the candidates took 494
+// us; with these words 357, and with the product issuers' loops not unrolled
+// over the three buffers 318 (now 96.6% hits).
 // A word is written before its step's K copy is armed, so a role that has
 // waited for the step's barrier finds it.  When the word of step c is
 // written, QK(c - 3) and so PV(c - 6) are done: 8 step words are enough.  An

@@ -725,7 +725,7 @@ int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, co
  *   q          bf16 device (rows, heads, d), rows q_stride elements apart
  *              (16-byte aligned, a multiple of 8).
  *   out        bf16 device (rows, heads, d) packed; written for the rows of
- *              the sequences only.
+ *              the sequences only.  Must not overlap q.
  *   workspace  device memory of hstu_cache_workspace bytes, 16-byte aligned,
  *              zeroed once before its first use: calls leave it ready for the
  *              next.  One call at a time may use it: give each stream, and

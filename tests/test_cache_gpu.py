@@ -137,7 +137,7 @@ def test_several_small_tiles(d, new, targets):
     s.check(s.attend())
 
 
-@pytest.mark.parametrize("max_q", [1, 4, 16, 32, 33, 500])
+@pytest.mark.parametrize("max_q", [1, 4, 16, 32, 33, 500, 2 ** 31 - 1])
 def test_max_q_changes_the_tiling_not_the_result(max_q):
     s = Setup([90, 300, 5], [1, 1, 1], 32, 2, 64, seed=1, max_q=max_q)
     s.check(s.attend())
