@@ -381,7 +381,9 @@ __device__ __forceinline__ void step_store(uint16_t* out, int heads, int x, cons
       make_uint2(pack_bf16x2(v.x * inv_n, v.y * inv_n), pack_bf16x2(v.z * inv_n, v.w * inv_n));
 }
 
-template <int D>
+// CLUSTER: the item's other parts are in the cluster's other CTAs; this CTA's
+// sums stay in `red`, in the first warp's place, for step_cluster_join.
+template <int D, bool CLUSTER>
 __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor c, PagedSeg g, uint32_t base,
                              uint32_t full, uint32_t empty, float* red, StepMisc<step_warps(D)>* m,
                              const StepWait& wt) {
@@ -526,6 +528,17 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
       }
     }
     step_barrier<C::WARPS>();
+    if constexpr (CLUSTER) {
+      for (int x = 4 * threadIdx.x; x < rows * D; x += 4 * 32 * C::WARPS) {
+        float* at = red + (x / D) * RS + x % D;
+        float4 v = *reinterpret_cast<const float4*>(at);
+#pragma unroll
+        for (int i = 1; i < C::WARPS; ++i)
+          add4(v, *reinterpret_cast<const float4*>(at + i * a.red_rows * RS));
+        *reinterpret_cast<float4*>(at) = v;
+      }
+      return;  // one segment a CTA
+    }
     dead = *static_cast<volatile int*>(&m->abort_flag) != 0;
     uint16_t* out = a.out + ((long long)(g.seq.q0 + kStepRows * g.qt) * w.heads + g.h) * D;
     const bool before = g.c0 != (int)blockIdx.x;
@@ -589,7 +602,44 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
   }
 }
 
+// Few items of few blocks: a cluster of kStepCluster CTAs an item, each with
+// an equal part of its blocks.  No CTA looks for its share, and the parts meet
+// in shared memory instead of behind a fence and a counter.
+constexpr int kStepCluster = 8;
+
+// The cluster's sums, a share of the values each CTA, in the CTAs' order.
 template <int D>
+__device__ void step_cluster_join(const StepArgs& a, const PagedSeg& g, int rank, const float* red,
+                                  const int* abort_flag) {
+  using C = StepCfg<D>;
+  constexpr int RS = step_red_stride(D);
+  cluster_barrier();
+  const uint32_t mine = smem_u32(red), flag = smem_u32(abort_flag);
+  int stop = 0;
+#pragma unroll
+  for (int r = 0; r < kStepCluster; ++r) {
+    int f;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(f) : "r"(cluster_addr(flag, r)) : "memory");
+    stop |= f;
+  }
+  uint16_t* out = a.out + ((long long)(g.seq.q0 + kStepRows * g.qt) * a.w.heads + g.h) * D;
+  for (int x = 4 * (rank * C::THREADS + (int)threadIdx.x); x < g.walk.rows * D;
+       x += 4 * kStepCluster * C::THREADS) {
+    float4 y[kStepCluster];
+#pragma unroll
+    for (int r = 0; r < kStepCluster; ++r)
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(y[r].x), "=f"(y[r].y), "=f"(y[r].z), "=f"(y[r].w)
+                   : "r"(cluster_addr(mine + 4u * (uint32_t)((x / D) * RS + x % D), r))
+                   : "memory");
+#pragma unroll
+    for (int r = 1; r < kStepCluster; ++r) add4(y[0], y[r]);
+    if (!stop) step_store<D>(out, a.w.heads, x, y[0], a.inv_n);
+  }
+  cluster_barrier();  // no CTA leaves while another reads its sums
+}
+
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(StepCfg<D>::THREADS)
     step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                 const StepArgs a) {
@@ -621,17 +671,86 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS)
   PagedWork w = a.w;
   PagedCursor c;
   PagedSeg g;
-  if (!paged_locate<C::WARPS + 1, false>(a.p, &w, a.min_units, &m->start, a.status, &c, &g)) return;
+  int rank = 0;
+  if constexpr (CLUSTER) {
+    rank = (int)blockIdx.x % kStepCluster;
+    const int item = (int)blockIdx.x / kStepCluster;
+    c.e = item / w.heads;
+    c.h = item - c.e * w.heads;
+    g.qt = c.e / a.p.batch;
+    g.b = c.e - g.qt * a.p.batch;
+    if (!paged_seq(a.p, g.b, &g.seq) && item == g.b * w.heads && rank == 0 && threadIdx.x == 0)
+      atomicOr(a.status, kStatusBadPaged);
+    g.walk = paged_walk(g.seq, g.qt, w.tile_rows, w.kb_shift);
+    if (g.walk.nb == 0) return;  // the same for the whole cluster
+    const int from = rank * g.walk.nb / kStepCluster, to = (rank + 1) * g.walk.nb / kStepCluster;
+    w.per = 1;
+    c.cta = (int)blockIdx.x;
+    c.u = c.u0 = 0;
+    c.u1 = to - from;
+    c.i = from;
+    c.loaded = true;
+    g.h = c.h;
+    if (to == from)  // no block of its own: its sums are zero
+      for (int x = threadIdx.x; x < a.red_rows * step_red_stride(D); x += C::THREADS) red[x] = 0.f;
+    __syncthreads();
+  } else {
+    if (!paged_locate<C::WARPS + 1, false>(a.p, &w, a.min_units, &m->start, a.status, &c, &g)) return;
+  }
   const StepWait wt{a.timeout_ns, &m->abort_flag, a.status};
   if (warp == C::WARPS)
     step_produce<D>(&tk, &tv, a, w, c, g, base, full, empty, wt);
   else
-    step_compute<D>(a, w, c, g, base, full, empty, red, m, wt);
+    step_compute<D, CLUSTER>(a, w, c, g, base, full, empty, red, m, wt);
+  if constexpr (CLUSTER) step_cluster_join<D>(a, g, rank, red, &m->abort_flag);
+}
+
+constexpr int step_ring_bytes(int d) { return 128 * 1024 / step_per_sm(d); }
+template <int D>
+constexpr int kStepBytesMost = step_ring_bytes(D) + step_red_bytes(kStepRows, D) + kStepTailBytes + 1024;
+
+// The kernels' shared memory, once a device.
+template <int D>
+cudaError_t step_prepare() {
+  static DeviceOnce once;
+  return once.run([] {
+    const cudaError_t e = cudaFuncSetAttribute(
+        step_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStepBytesMost<D>);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(step_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kStepBytesMost<D>);
+  });
+}
+
+// Clusters that run at once, with the most shared memory a call may ask for.
+template <int D>
+cudaError_t step_clusters(int* n) {
+  const cudaError_t e = step_prepare<D>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kStepCluster);
+  cfg.blockDim = dim3(StepCfg<D>::THREADS);
+  cfg.dynamicSmemBytes = kStepBytesMost<D>;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kStepCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(n, step_kernel<D, true>, &cfg);
+}
+cudaError_t step_clusters_d(int d, int* n) {
+  switch (d) {
+    case 32: return step_clusters<32>(n);
+    case 64: return step_clusters<64>(n);
+    default: return step_clusters<128>(n);
+  }
 }
 
 template <int D>
-cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, long long most, StepArgs a,
-                        int sms, cudaStream_t stream) {
+cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, long long most, bool clusters,
+                        StepArgs a, int sms, cudaStream_t stream) {
   using C = StepCfg<D>;
   // 128 KB of copies in flight an SM.  More make every CTA's first block wait
   // for the others' queued copies and leave more blocks to compute once the
@@ -642,23 +761,24 @@ cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, long long 
   static_assert(RING / C::STAGEB >= 2 && RING / C::STAGEB < C::MAX_STAGES, "stages");
   const int extra = step_red_bytes(a.red_rows, D) + kStepTailBytes + 1024;
   const int bytes = a.stages * C::STAGEB + extra;
+  static_assert(RING == step_ring_bytes(D), "ring");
+  const cudaError_t e = step_prepare<D>();
+  if (e != cudaSuccess) return e;
+  if (clusters)
+    return launch_after_in_clusters(kStepCluster, step_kernel<D, true>,
+                                    kStepCluster * a.w.tiles * a.p.batch * a.w.heads, C::THREADS, bytes,
+                                    stream, tk, tv, a);
   const int grid = (int)std::min<long long>((long long)PER_SM * sms,
                                             (most + a.min_units - 1) / a.min_units);
-  static DeviceOnce once;
-  const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                RING + step_red_bytes(kStepRows, D) + kStepTailBytes + 1024);
-  });
-  if (e != cudaSuccess) return e;
-  return launch_after(step_kernel<D>, grid, C::THREADS, bytes, stream, tk, tv, a);
+  return launch_after(step_kernel<D, false>, grid, C::THREADS, bytes, stream, tk, tv, a);
 }
 
-cudaError_t launch_step_d(int d, const CUtensorMap& tk, const CUtensorMap& tv, long long most,
+cudaError_t launch_step_d(int d, const CUtensorMap& tk, const CUtensorMap& tv, long long most, bool clusters,
                           const StepArgs& a, int sms, cudaStream_t s) {
   switch (d) {
-    case 32: return launch_step<32>(tk, tv, most, a, sms, s);
-    case 64: return launch_step<64>(tk, tv, most, a, sms, s);
-    default: return launch_step<128>(tk, tv, most, a, sms, s);
+    case 32: return launch_step<32>(tk, tv, most, clusters, a, sms, s);
+    case 64: return launch_step<64>(tk, tv, most, clusters, a, sms, s);
+    default: return launch_step<128>(tk, tv, most, clusters, a, sms, s);
   }
 }
 
@@ -694,6 +814,7 @@ struct hstu_cache {
   long long page_stride;
   int device, sms;
   unsigned* status;
+  int clusters;        // clusters of the few-token kernel that run at once
   CUtensorMap tk, tv;  // boxes of up to 128 keys, both kernels' blocks
 };
 
@@ -753,6 +874,17 @@ bool use_tiles(const PagedView& v, int d, int sms, long long units) {
   return v.max_q > 64 || units > (d == 128 ? 5LL : 20LL) * sms;
 }
 
+// Whether 16-row tiles get a cluster of CTAs an item: where all clusters run
+// at once (`clusters_at_once`) and no CTA has more than 8 blocks.  One token,
+// 4 heads of 64, against equal shares: 4.1 us and 6.0 on 513 keys, 6.4 and 7.6
+// on 4096, 9.2 and 9.2 on 8192, 15.1 and 12.6 on 16384; 9 sequences 16.9 and
+// 18.5 on 8192.
+bool use_clusters(const PagedView& v, int heads, int tiles, int clusters_at_once) {
+  const long long items = (long long)tiles * v.batch * heads;
+  const long long blocks = (((long long)v.max_pages << v.page_shift) + hstu::kStepKeys - 1) >> hstu::kStepShift;
+  return items <= clusters_at_once && blocks <= 8LL * hstu::kStepCluster;
+}
+
 int check_geometry(int num_pages, int page_size, int* shift) {
   if (num_pages < 1 || page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)))
     return HSTU_ERR_INVALID_ARG;
@@ -801,6 +933,7 @@ int hstu_cache_create(void* k_pages, void* v_pages, int num_pages, int page_size
   int rc = hstu::host_device_check(&c->sms);
   if (rc == HSTU_OK && cudaGetDevice(&c->device) != cudaSuccess) rc = HSTU_ERR_CUDA;
   if (rc == HSTU_OK && hstu::device_status_words(&c->status) != cudaSuccess) rc = HSTU_ERR_CUDA;
+  if (rc == HSTU_OK) rc = hstu::status_of(hstu::step_clusters_d(d, &c->clusters));
   if (rc == HSTU_OK)
     rc = hstu::make_pool_map(&c->tk, k_pages, num_pages, page_size, heads, d, page_stride);
   if (rc == HSTU_OK)
@@ -968,6 +1101,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   }
   const long long most = units_bound(p, heads, w.tiles, w.kb_shift, w.extra);
   if (most > kMostUnits) return HSTU_ERR_INVALID_ARG;
+  const bool clusters = !tiled && use_clusters(p, heads, w.tiles, cache->clusters);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CUtensorMap tq;
   if (tiled) {
@@ -979,7 +1113,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
       return rc;
   }
   char* own = nullptr;
-  if (!workspace) {
+  if (!workspace && !clusters) {
     cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&own), workspace_bytes(cache), s);
     if (e != cudaSuccess) return e == cudaErrorMemoryAllocation ? HSTU_ERR_NO_MEMORY : HSTU_ERR_CUDA;
     if (cudaMemsetAsync(own, 0, (size_t)kCounterBytes, s) != cudaSuccess) {
@@ -1021,7 +1155,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     a.status = cache->status;
     a.timeout_ns = hstu::host_wait_timeout_ns();
     a.debug_flags = hstu::host_debug_flags();
-    e = hstu::launch_step_d(d, cache->tk, cache->tv, most, a, cache->sms, s);
+    e = hstu::launch_step_d(d, cache->tk, cache->tv, most, clusters, a, cache->sms, s);
   }
   rc = hstu::status_of(e);
   if (own && cudaFreeAsync(own, s) != cudaSuccess && rc == HSTU_OK) rc = HSTU_ERR_CUDA;

@@ -243,11 +243,6 @@ struct RowRing {
   __device__ __forceinline__ void step() { get = get + 1 == STAGES ? 0 : get + 1; }
 };
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // One CTA an SM, so that few CTAs hand over sums of dgamma and dbeta.
 constexpr int kBwdThreads = 512;
 
@@ -401,15 +396,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_kernel(const NormBwdA
     }
   if (!a.dgamma) return;
   // each CTA sums a share of the columns over the cluster's CTAs, in order
-  cluster_barrier();
+  hstu::cluster_barrier();
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(kept);
   for (int x = blockIdx.x * kBwdThreads + threadIdx.x; x < 2 * a.width; x += gridDim.x * kBwdThreads) {
     float t = 0.f;
     for (int r = 0; r < (int)gridDim.x; ++r) {
-      uint32_t at;
       float v;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine + 4u * x), "r"(r));
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(hstu::cluster_addr(mine + 4u * x, r)) : "memory");
       t += v;
     }
     if (x < a.width)
@@ -417,7 +410,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_kernel(const NormBwdA
     else
       a.dbeta[x - a.width] = t;
   }
-  cluster_barrier();  // no CTA leaves while another reads its sums
+  hstu::cluster_barrier();  // no CTA leaves while another reads its sums
 }
 
 // dgamma and dbeta: the CTAs' sums in a fixed order.  A block takes 32 of the

@@ -26,6 +26,20 @@ __device__ __forceinline__ void after_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Every thread of the cluster's CTAs meets; what they wrote to shared memory
+// before is visible to all behind it.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address in the cluster's CTA `rank` of this CTA's shared address.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, int rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
+  return at;
+}
+
 // cluster: CTAs of a thread-block cluster (0: no clusters).
 template <class... Params, class... Args>
 cudaError_t launch_after_in_clusters(int cluster, void (*kernel)(Params...), int grid, int threads, int smem,

@@ -16,14 +16,15 @@ def _built():
     build.build()
 
 
-def make_batch(hist, new, page, targets=None, seed=0, max_q=None, spare=2):
-    """A batch of numpy arrays with shuffled pages: (PagedBatch, num_pages, rows)."""
+def make_batch(hist, new, page, targets=None, seed=0, max_q=None, spare=2, width=1):
+    """A batch of numpy arrays with shuffled pages (a table of at least ``width``
+    pages a row): (PagedBatch, num_pages, rows)."""
     rng = np.random.default_rng(seed)
     hist, new = np.asarray(hist), np.asarray(new)
     kv = hist + new
     pages = -(-kv // page)
     order = rng.permutation(int(pages.sum()) + spare)
-    table = np.full((len(kv), max(int(pages.max(initial=0)), 1)), -7, dtype=np.int32)
+    table = np.full((len(kv), max(int(pages.max(initial=0)), width)), -7, dtype=np.int32)
     at = 0
     for b, n in enumerate(pages):
         table[b, :n] = order[at:at + n]

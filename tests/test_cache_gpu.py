@@ -46,8 +46,10 @@ def rotary_table(positions, dim):
 class Setup:
     """A host batch with its pools, and the same on the device."""
 
-    def __init__(self, hist, new, page, heads, d, targets=None, seed=0, pad=0, max_q=None, nan_tail=True):
-        self.host, self.num_pages, self.total = make_batch(hist, new, page, targets, seed, max_q)
+    def __init__(self, hist, new, page, heads, d, targets=None, seed=0, pad=0, max_q=None, nan_tail=True,
+                 width=1):
+        self.host, self.num_pages, self.total = make_batch(hist, new, page, targets, seed, max_q,
+                                                           width=width)
         self.rows, self.heads, self.d, self.page = self.total + pad, heads, d, page
         gen = torch.Generator().manual_seed(seed)
         sigma = 1.0 if d < 128 else 0.5
@@ -113,11 +115,22 @@ SHAPES = {
 @pytest.mark.parametrize("d,heads,page", [(32, 3, 16), (64, 2, 64), (128, 1, 32), (64, 1, 256),
                                           (32, 2, 128), (128, 2, 16)])
 @pytest.mark.parametrize("name", SHAPES)
-def test_attention_parity(name, d, heads, page):
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_parity(wide, name, d, heads, page):
+    # wide: a table for 10,000 tokens, so that few items share the GPU evenly
+    # instead of taking a cluster each
     hist, new, nt = SHAPES[name]
-    s = Setup(hist, new, page, heads, d, nt, seed=len(name) + d, pad=3)
+    s = Setup(hist, new, page, heads, d, nt, seed=len(name) + d, pad=3, width=10000 // page if wide else 1)
     out = s.attend()
     s.check(out)
+
+
+def test_many_items():
+    # more items than clusters run at once, of one to seven blocks
+    rng = np.random.default_rng(50)
+    hist, new = rng.integers(0, 850, size=60), rng.integers(0, 4, size=60)
+    s = Setup(hist, new, 32, 2, 64, rng.integers(0, new + 1), seed=50)
+    s.check(s.attend())
 
 
 @pytest.mark.parametrize("d,heads,page", [(32, 2, 32), (64, 3, 16), (128, 1, 128)])
@@ -143,10 +156,11 @@ def test_max_q_changes_the_tiling_not_the_result(max_q):
     s.check(s.attend())
 
 
+@pytest.mark.parametrize("width", [1, 200])
 @pytest.mark.parametrize("new", [1, 5, 40, 130])
-def test_long_cache_few_rows(new):
-    # one sequence and one head over the whole GPU: many parts a row
-    s = Setup([6000], [new], 64, 1, 64, [new], seed=2)
+def test_long_cache_few_rows(new, width):
+    # one sequence and one head over a cluster or the whole GPU: many parts a row
+    s = Setup([6000], [new], 64, 1, 64, [new], seed=2, width=width)
     ws = s.workspace()
     a = s.attend(workspace=ws)
     assert not ws[:8192].any(), "the workspace is ready for the next call"
@@ -205,8 +219,9 @@ def test_a_shared_prefix_is_read_from_shared_pages():
     s.check(s.attend())
 
 
-def test_bad_lengths_and_pages_are_skipped_and_reported():
-    s = Setup([100, 40, 70], [2, 2, 1], 16, 1, 64, seed=7, nan_tail=False)
+@pytest.mark.parametrize("width", [1, 600])
+def test_bad_lengths_and_pages_are_skipped_and_reported(width):
+    s = Setup([100, 40, 70], [2, 2, 1], 16, 1, 64, seed=7, nan_tail=False, width=width)
     good = s.attend()
 
     def run(name, at, value):
@@ -419,11 +434,11 @@ def test_growing_by_steps_is_the_forward_over_the_whole():
         assert np.all(np.abs(layer.f64(x) - ref64) <= 2.0 ** -8 * np.abs(ref64) + bound)
 
 
-@pytest.mark.parametrize("new", [1, 70])
-def test_a_wait_that_runs_out_is_reported(new):
-    # both kernels give up at a barrier nothing signals, write nothing, and
+@pytest.mark.parametrize("new,width", [(1, 1), (1, 400), (70, 1)])
+def test_a_wait_that_runs_out_is_reported(new, width):
+    # the kernels give up at a barrier nothing signals, write nothing, and
     # leave a device (and, zeroed again, a workspace) that works
-    s = Setup([900, 40], [new, 1], 32, 2, 64, seed=40 + new)
+    s = Setup([900, 40], [new, 1], 32, 2, 64, seed=40 + new, width=width)
     good, ws = s.attend(), s.workspace()
     torch.cuda.synchronize()
     binding.hstu_set_wait_timeout_ns(20_000_000)
