@@ -27,8 +27,10 @@ __device__ __forceinline__ void after_previous_kernel() {
 }
 
 // Every thread of the cluster's CTAs meets; what they wrote to shared memory
-// before is visible to all behind it.
+// before is visible to all behind it.  A warp's lanes meet first: the aligned
+// form wants them together.
 __device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

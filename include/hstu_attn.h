@@ -732,6 +732,8 @@ int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, co
  *              each captured graph that may run beside another, its own, and
  *              zero it again after a call ended in HSTU_ERR_TIMEOUT.  NULL: a
  *              stream-ordered allocation.
+ * Calls of few new tokens, heads and pages (by rows, batch, max_q and
+ * max_pages, not by the lengths) run without the workspace.
  * The keys are split evenly over the GPU's SMs; a row's parts are summed in
  * a fixed order, so results repeat bit for bit.
  * Errors: HSTU_ERR_INVALID_ARG (also for a cache of another device than the
