@@ -876,14 +876,14 @@ bool use_tiles(const PagedView& v, int d, int sms, long long units) {
 }
 
 // Whether 16-row tiles get a cluster of CTAs an item: where all clusters run
-// at once (`clusters_at_once`) and no CTA has more than 8 blocks.  One token,
-// 4 heads of 64, against equal shares: 4.1 us and 6.0 on 513 keys, 6.4 and 7.6
-// on 4096, 9.2 and 9.2 on 8192, 15.1 and 12.6 on 16384; 9 sequences 16.9 and
-// 18.5 on 8192.
+// at once (`clusters_at_once`), there is more than one block to share, and no
+// CTA has more than 8.  One token, 4 heads of 64, against equal shares: 4.2 us
+// and 3.9 on 64 keys, 4.1 and 6.0 on 513, 6.4 and 7.6 on 4096, 9.2 and 9.2 on
+// 8192, 15.1 and 12.6 on 16384; 9 sequences 16.9 and 18.5 on 8192.
 bool use_clusters(const PagedView& v, int heads, int tiles, int clusters_at_once) {
   const long long items = (long long)tiles * v.batch * heads;
   const long long blocks = (((long long)v.max_pages << v.page_shift) + hstu::kStepKeys - 1) >> hstu::kStepShift;
-  return items <= clusters_at_once && blocks <= 8LL * hstu::kStepCluster;
+  return items <= clusters_at_once && blocks > 1 && blocks <= 8LL * hstu::kStepCluster;
 }
 
 int check_geometry(int num_pages, int page_size, int* shift) {
