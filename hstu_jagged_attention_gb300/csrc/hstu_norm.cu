@@ -365,6 +365,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_kernel(const NormBwdA
   float* kept = acc + (GROUPS > 1 ? 8 * kBwdThreads : 0);
   float* out = a.dgamma ? kept : a.parts + (long long)blockIdx.x * 2 * a.width;
   asm volatile("cp.async.wait_all;" ::: "memory");
+  // `kept` lies over the other threads' vectors too, where their copies of the
+  // rows past the end (zeros) may still land; with several groups the barrier
+  // in the loop stands before the first store
+  if constexpr (GROUPS == 1) __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll

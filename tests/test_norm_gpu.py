@@ -269,3 +269,19 @@ def test_matches_the_fused_output_stage():
     ref = ref.reshape(w.total, -1)
     tol = 2.0 ** -8 * (spread * gu + np.abs(ref)) + 1e-3 * rms
     assert np.all(np.abs(layer.f64(y).reshape(w.total, -1) - ref) <= tol)
+
+
+@pytest.mark.parametrize("width", [2056, 4096, 4104, 8192])
+@pytest.mark.parametrize("rows", [9, 12, 16])
+def test_sums_of_one_cluster_with_a_row_a_cta(rows, width):
+    # a CTA holds one row at a time and sums dgamma and dbeta where its copies of
+    # the rows past the end (zeros) land: no column may be lost, ever
+    a, dy, dz_in = make(rows, width, True, True, seed=rows + width)
+    dev = to_gpu(a)
+    _, z = run_fwd(dev, EPS, 0.5)
+    dy_d, in_d = dy.cuda(), dz_in.cuda()
+    first = run_bwd(dy_d, z, dev, EPS, in_d, True, 0.5)
+    check_bwd(first, dy, z, a, EPS, dz_in, 0.5)
+    for _ in range(100):
+        o = run_bwd(dy_d, z, dev, EPS, in_d, True, 0.5)
+        assert torch.equal(o["dgamma"], first["dgamma"]) and torch.equal(o["dbeta"], first["dbeta"])
