@@ -539,7 +539,9 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
       }
       return;  // one segment a CTA
     }
-    dead = *static_cast<volatile int*>(&m->abort_flag) != 0;
+    // one answer for the warp, whose lanes meet again in the next item's waits:
+    // the copying warp may give up between two lanes' reads
+    dead = __any_sync(0xffffffffu, *static_cast<volatile int*>(&m->abort_flag) != 0);
     uint16_t* out = a.out + ((long long)(g.seq.q0 + kStepRows * g.qt) * w.heads + g.h) * D;
     const bool before = g.c0 != (int)blockIdx.x;
     float* part = step_part<D>(a, blockIdx.x, !before);
