@@ -302,7 +302,8 @@ __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const
   const int box = ps < C::KEYS ? ps : C::KEYS;
   int st = 0;
   uint32_t ph = 1, count = 0;
-  while (c.next(a.p, w, &g)) {
+  bool ok = true;
+  while (ok && c.next(a.p, w, &g)) {
     const int32_t* row = a.p.page_table + (long long)g.b * a.p.max_pages;
     const int end = g.walk.end();
     const int pages = (end + ps - 1) >> shift;  // of the sequence, as far as the tile sees
@@ -317,7 +318,7 @@ __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const
       const int pg = lane / (2 * C::NCH), ch = (lane >> 1) % C::NCH;
       int page = ids.get(p0 + pg);
       const uint32_t bar = full + 8u * st;
-      if (!__all_sync(0xffffffffu, step_wait(empty + 8u * st, ph, wt, kSiteStepEmpty))) goto drain;
+      if (!(ok = __all_sync(0xffffffffu, step_wait(empty + 8u * st, ph, wt, kSiteStepEmpty)))) break;
       if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(npg * box * C::ROWB * C::NCH * 2));
       __syncwarp();
       if (pg < npg) {
@@ -338,15 +339,16 @@ __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const
       }
     }
   }
-  return;
-drain:
-  // every copy lands before the CTA ends
+  // Every copy lands before the CTA ends, also where the warps that would wait
+  // for it have given up.  A stage is armed again only once all of them have
+  // seen its last phase complete, so each stage's last phase is the one to wait
+  // for.
   if (lane == 0) {
     for (int s = 0; s < a.stages; ++s)
       if (count > (uint32_t)s) {
-        const uint32_t uses = (count - 1u - s) / a.stages + 1u;
+        const uint32_t parity = ((count - 1u - s) / a.stages) & 1u;
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(full + 8u * s, (uses - 1u) & 1u))
+        while (!mbar_try_wait(full + 8u * s, parity))
           if (globaltimer() - t0 > 2000000000ull) break;
       }
   }
@@ -400,7 +402,9 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
   const float2 ha2 = make_float2(a.half_alpha, a.half_alpha);
   int st = 0;
   uint32_t ph = 0;
-  bool dead = false;  // the CTA gave up: run on without waits, store nothing
+  // The CTA gave up: go through the items' barriers, but touch no stage (one
+  // that was not waited for is not released either) and store nothing.
+  bool dead = false;
   StepCut cut0{}, cut1{};  // items shared with earlier, and with later, CTAs
   // test hook: the barrier behind the stages' is never arrived on
   if (a.debug_flags & kDebugUnsignalledWait)
@@ -427,9 +431,9 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
 
-    for (int i = 0; i < g.n; ++i) {
+    for (int i = 0; i < g.n && !dead; ++i) {
       const int kb = g.walk.block(g.i0 + i) << kStepShift;
-      if (!dead) dead = !__all_sync(0xffffffffu, step_wait(full + 8u * st, ph, wt, kSiteStepFull));
+      if ((dead = !__all_sync(0xffffffffu, step_wait(full + 8u * st, ph, wt, kSiteStepFull)))) break;
       const uint32_t ks = base + st * C::STAGEB + k_at, vs = base + st * C::STAGEB + v_at;
       float s[2 * KS][4];
 #pragma unroll

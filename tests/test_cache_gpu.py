@@ -502,3 +502,25 @@ def test_empty_calls():
     binding.hstu_attn_fwd_cache(s.cache, batch, none, 1.0, 1.0, none)
     binding.hstu_attn_fwd_cache(s.cache, batch, s.q.cuda(), 1.0, 1.0, s.q.cuda())
     parity.assert_device_ok()
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("new,width", [(1, 1), (5, 1), (1, 700), (16, 700)])
+def test_giving_up_at_once_leaves_nothing_behind(new, width, d):
+    # a limit that runs out while the first copies are on their way: they land
+    # before the kernel ends, and the calls behind it are right
+    s = Setup([5000, 40, 1300], [new, 1, 3], 32, 2, d, seed=60 + new, width=width)
+    good, ws, q = s.attend(), s.workspace(), s.q.cuda()
+    for _ in range(10):
+        binding.hstu_set_wait_timeout_ns(1)
+        try:
+            s.attend(q=q, workspace=ws)
+        finally:
+            binding.hstu_set_wait_timeout_ns(0)
+        after = s.attend(q=q)  # right behind it, with a workspace of its own
+        status, site = binding.hstu_last_status()
+        assert (status == binding.HSTU_ERR_TIMEOUT) == (site != 0)
+        assert status in (binding.HSTU_OK, binding.HSTU_ERR_TIMEOUT)
+        assert torch.equal(after, good)
+        ws.zero_()
+        assert torch.equal(s.attend(q=q, workspace=ws), good)
