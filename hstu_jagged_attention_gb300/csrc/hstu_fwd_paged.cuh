@@ -113,8 +113,12 @@ __device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, c
       const int pg = lane / C::NCHUNK, ch = lane % C::NCHUNK;  // npg NCHUNK <= 16 lanes copy
       int page = ids.get(p0 + pg);
       const int slot = (int)(c % C::P);
-      ok = KQ ? wait_warp(bar(C::B_SFULL + slot), ((c / C::P) & 1u) ^ 1u, wt, kSiteKEmpty)
-              : wait_warp(bar(C::B_QKREADY + slot), (c / C::P) & 1u, wt, kSiteVEmpty);
+      // no further K copies once the CTA has given up (see the PV issuer's end);
+      // one lane asks: all of them, with a vote, took 291.8 us on the candidates, 288 so
+      if (lane == 0)
+        ok = KQ ? wait_one(bar(C::B_SFULL + slot), ((c / C::P) & 1u) ^ 1u, wt, kSiteKEmpty) && !*wt.abort_flag
+                : wait_one(bar(C::B_QKREADY + slot), (c / C::P) & 1u, wt, kSiteVEmpty);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
       if (lane == 0) {
         if (KQ)
@@ -135,7 +139,9 @@ __device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, c
       ++c;
     }
   }
-  if (!ok && lane == 0) {
+  // every copy lands before the CTA ends, also where the roles that would wait
+  // for it have given up
+  if (lane == 0) {
     drain_copies(bar(FULL), C::P, c);
     if (KQ) drain_copies(bar(C::B_QFULL), C::QS, qc);
   }
@@ -188,10 +194,10 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, uint32_t steps, const PagedW
     ++tc;
     if (J == P - 1) ph ^= 1u;
   }
-  if (!ok) {
-    mma_commit(bar(C::B_DRAIN));
-    wait_drain(bar(C::B_DRAIN), 0);
-  }
+  // every product is done before TMEM is freed, also where the SiLU warps have
+  // given up
+  mma_commit(bar(C::B_DRAIN));
+  wait_drain(bar(C::B_DRAIN), 0);
 }
 
 // PV issuer: as role_mma_pv, with the block that holds the tile's last keys
@@ -280,9 +286,16 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
     ++tc;
     if (J == P - 1) ph ^= 1u;
   }
+  mma_commit(bar(C::B_DRAIN + 1));
+  wait_drain(bar(C::B_DRAIN + 1), 0);
   if (!ok) {
-    mma_commit(bar(C::B_DRAIN + 1));
-    wait_drain(bar(C::B_DRAIN + 1), 0);
+    // The K producer waits for its last copies' QK-ready, which also counts on
+    // PV(t), tc <= t < tc + P, where K(t) has landed and so K(t + P) may be on
+    // its way.  Those PVs do not come: arrive for them.  (PV(t - P) is done, so
+    // the barrier is in the phase of step t or the next one and the test is
+    // exact.)
+    for (uint32_t t = tc; t < tc + P; ++t)
+      if (mbar_test(bar(C::B_QKREADY + (int)(t % P)), (t / P) & 1u)) mbar_arrive(bar(C::B_QKREADY + (int)(t % P)));
   }
 }
 

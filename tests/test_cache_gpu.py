@@ -524,3 +524,25 @@ def test_giving_up_at_once_leaves_nothing_behind(new, width, d):
         assert torch.equal(after, good)
         ws.zero_()
         assert torch.equal(s.attend(q=q, workspace=ws), good)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_giving_up_at_once_on_large_tiles(d):
+    s = Setup([3000, 40, 1300], [200, 1, 130], 32, 2, d, seed=70)
+    good, ws, q = s.attend(), s.workspace(), s.q.cuda()
+    for flags in (0, binding.HSTU_DEBUG_UNSIGNALLED_WAIT):
+        for _ in range(5):
+            binding.hstu_set_wait_timeout_ns(1)
+            binding.hstu_set_debug_flags(flags)
+            try:
+                s.attend(q=q, workspace=ws)
+            finally:
+                binding.hstu_set_debug_flags(0)
+                binding.hstu_set_wait_timeout_ns(0)
+            after = s.attend(q=q)
+            status, site = binding.hstu_last_status()
+            assert (status == binding.HSTU_ERR_TIMEOUT) == (site != 0)
+            assert status == binding.HSTU_ERR_TIMEOUT or not flags
+            assert torch.equal(after, good)
+            ws.zero_()
+            assert torch.equal(s.attend(q=q, workspace=ws), good)
