@@ -619,10 +619,12 @@ int hstu_cache_destroy(hstu_cache* cache);
  *                written as tokens.
  *
  * What the device finds wrong is skipped and reported by hstu_last_status
- * as HSTU_ERR_INVALID_ARG:
+ * as HSTU_ERR_INVALID_ARG, by the append and by the attention (a call without
+ * rows launches nothing and reports nothing):
  *   - a sequence whose offsets decrease or leave [0, rows], with n_b > max_q,
  *     kv_lens[b] < n_b, more tokens than max_pages pages hold, or
- *     num_targets[b] outside [0, n_b]: none of its rows is written;
+ *     num_targets[b] outside [0, n_b]: none of its rows is written (whether
+ *     it has new tokens or not, it is reported);
  *   - a page number outside [0, num_pages): an append there is dropped, and
  *     the attention reads the page as zeros (its keys add nothing).
  * max_pages * page_size is at most 2^30, and so are the attention's units:

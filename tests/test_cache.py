@@ -89,6 +89,24 @@ def test_contradictions_are_found(name, at, value, skipped):
             assert slot[t] == good[t], t
 
 
+@pytest.mark.parametrize("new,name,at,value,skipped", [
+    ([3, 5, 2], "q_offsets", 3, 5, range(5, 10)),   # decreasing at the end: rows 5 .. 9 are behind it
+    ([3, 5, 2], "q_offsets", 3, -1, range(10)),
+    ([3, 0, 2], "kv_lens", 1, -1, ()),              # a sequence without new tokens
+    ([3, 0, 2], "kv_lens", 1, 10 ** 6, ()),
+    ([3, 5, 0], "num_targets", 2, 1, ()),
+    ([3, 5, 0], "q_offsets", 3, 99, ()),            # past the rows, behind the last of them
+])
+def test_contradictions_without_a_row_are_found(new, name, at, value, skipped):
+    batch, num_pages, rows = make_batch([100, 40, 7], new, 16, [0, 0, 0], max_q=5)
+    good, _, fine = binding.hstu_cache_slots(batch, num_pages, 16, rows)
+    assert fine
+    batch.keep[name][at] = value
+    slot, _, ok = binding.hstu_cache_slots(batch, num_pages, 16, rows)
+    assert not ok
+    assert [t for t in range(rows) if slot[t] != good[t]] == list(skipped)
+
+
 @pytest.mark.parametrize("value", [-1, 10 ** 6, 2 ** 31 - 1, -2 ** 31])
 def test_bad_pages_are_found(value):
     def change(arrays):

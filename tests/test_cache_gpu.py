@@ -546,3 +546,22 @@ def test_giving_up_at_once_on_large_tiles(d):
             assert torch.equal(after, good)
             ws.zero_()
             assert torch.equal(s.attend(q=q, workspace=ws), good)
+
+
+@pytest.mark.parametrize("name,at,value,kept", [("q_offsets", 3, 5, 5), ("kv_lens", 3, -1, 10),
+                                                ("kv_lens", 3, 10 ** 6, 10), ("q_offsets", 5, 99, 10)])
+def test_append_reports_contradictions_without_a_row(name, at, value, kept):
+    s = Setup([100, 40, 7, 9, 1], [3, 5, 2, 0, 0], 16, 2, 64, seed=80)
+    if name == "q_offsets" and at == 3:
+        s.dev[name][4:] = value
+    s.dev[name][at] = value
+    k, v = s.k.cuda(), s.v.cuda()
+    binding.hstu_cache_append(s.cache, s.batch, k, v)
+    assert binding.hstu_last_status()[0] == binding.HSTU_ERR_INVALID_ARG
+    a = s.host.keep
+    off, kv, table = a["q_offsets"], a["kv_lens"], a["page_table"]
+    for t in range(kept):  # the other sequences' rows are in their places
+        b = int(np.searchsorted(off, t, side="right")) - 1
+        p = kv[b] - (off[b + 1] - off[b]) + t - off[b]
+        assert torch.equal(s.kd[table[b, p // 16], p % 16], k[t])
+    assert binding.hstu_last_status() == (binding.HSTU_OK, 0)
