@@ -130,10 +130,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   }
   if (t >= total) return;  // a row behind the last sequence
   const int b = paged_find(a.p, t);
-  if (b < 0 || !paged_seq(a.p, b, &s)) {
-    atomicOr(a.status, kStatusBadPaged);
-    return;
-  }
+  if (b < 0 || !paged_seq(a.p, b, &s)) return;  // before the first sequence, or of one that is reported
   const int pos = s.kv - s.qn + (t - s.q0);
   const long long slot = paged_slot(a.p, b, pos);
   const int turned_at = pos < s.hist ? pos : s.hist;  // a candidate stands right behind the history
@@ -991,10 +988,7 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
     if (v.batch == 0 || t >= v.q_offsets[v.batch]) continue;
     const int b = hstu::paged_find(v, t);
     hstu::PagedSeq s;
-    if (b < 0 || !hstu::paged_seq(v, b, &s)) {
-      bad = 1;
-      continue;
-    }
+    if (b < 0 || !hstu::paged_seq(v, b, &s)) continue;
     const int pos = s.kv - s.qn + (t - s.q0);
     host_slot[t] = hstu::paged_slot(v, b, pos);
     host_pos[t] = pos < s.hist ? pos : s.hist;

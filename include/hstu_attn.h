@@ -614,9 +614,9 @@ int hstu_cache_destroy(hstu_cache* cache);
  *   page_table   int32[batch][max_pages]; entries past a sequence's last page
  *                are not read.
  *   max_q        upper bound on every n_b: it chooses the kernel's tiling.
- *   rows         rows that q, k, v and out have.  Rows at or past
- *                q_offsets[batch] (a padded batch) are neither read nor
- *                written as tokens.
+ *   rows         rows that q, k, v and out have.  Rows before q_offsets[0]
+ *                (a part of a larger batch) and at or past q_offsets[batch]
+ *                (a padded one) are neither read nor written as tokens.
  *
  * What the device finds wrong is skipped and reported by hstu_last_status
  * as HSTU_ERR_INVALID_ARG, by the append and by the attention (a call without
@@ -646,8 +646,8 @@ typedef struct hstu_paged_batch {
  * hstu_cache_slots -- where each row of a batch goes, on the host only (no
  * CUDA call; the batch's arrays are host memory): host_slot[t] = the pool row
  * (page * page_size + row in page) of token row t and host_pos[t] the
- * position its rotation uses, both -1 for a row behind the last sequence,
- * of a skipped sequence, or (the slot) with a page out of range.  The kernels use the same
+ * position its rotation uses, both -1 for a row of no sequence or of a
+ * skipped one, the slot also where its page is out of range.  The kernels use the same
  * arithmetic.  host_slot, host_pos: `rows` entries.  Returns
  * HSTU_ERR_INVALID_ARG, with the arrays written, when the device would
  * report the batch, and without them on an argument error.

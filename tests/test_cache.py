@@ -107,6 +107,17 @@ def test_contradictions_without_a_row_are_found(new, name, at, value, skipped):
     assert [t for t in range(rows) if slot[t] != good[t]] == list(skipped)
 
 
+def test_rows_before_the_first_sequence_are_nobodys():
+    batch, num_pages, rows = make_batch([100, 0, 40], [3, 2, 1], 16, [0, 2, 0])
+    slot, pos, ok = binding.hstu_cache_slots(batch, num_pages, 16, rows)
+    batch.keep["q_offsets"] += 4
+    slot4, pos4, ok4 = binding.hstu_cache_slots(batch, num_pages, 16, rows + 7)
+    assert ok and ok4
+    assert np.array_equal(slot4[4:-3], slot) and np.array_equal(pos4[4:-3], pos)
+    for x in (slot4, pos4):
+        assert np.all(x[:4] == -1) and np.all(x[-3:] == -1)
+
+
 @pytest.mark.parametrize("value", [-1, 10 ** 6, 2 ** 31 - 1, -2 ** 31])
 def test_bad_pages_are_found(value):
     def change(arrays):

@@ -565,3 +565,28 @@ def test_append_reports_contradictions_without_a_row(name, at, value, kept):
         p = kv[b] - (off[b + 1] - off[b]) + t - off[b]
         assert torch.equal(s.kd[table[b, p // 16], p % 16], k[t])
     assert binding.hstu_last_status() == (binding.HSTU_OK, 0)
+
+
+@pytest.mark.parametrize("new", [1, 40, 130])
+def test_rows_before_the_first_sequence_stay(new):
+    s = Setup([100, 0, 700], [3, new, 1], 16, 2, 64, seed=81)
+    s.dev["q_offsets"].add_(4)
+    lead = torch.full((4, 2, 64), float("nan"), device="cuda", dtype=torch.bfloat16)
+    pad = lambda x: torch.cat([lead, x.cuda(), lead[:1]])
+    q_out = torch.full((s.rows + 5, 2, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+    good = s.kp.clone(), s.vp.clone()
+    a = s.host.keep
+    for t in range(s.total):
+        b = int(np.searchsorted(a["q_offsets"], t, side="right")) - 1
+        p = a["kv_lens"][b] - a["q_offsets"][b + 1] + t
+        for x, y in zip(good, (s.k, s.v)):
+            x[a["page_table"][b, p // 16], p % 16] = y[t]
+    binding.hstu_cache_append(s.cache, s.batch, pad(s.k), pad(s.v), q=pad(s.q), q_out=q_out)
+    assert torch.equal(s.kd.cpu().nan_to_num(), good[0].nan_to_num())
+    assert torch.equal(s.vd.cpu().nan_to_num(), good[1].nan_to_num())
+    assert torch.equal(q_out[4:-1].cpu(), s.q) and (q_out[:4] == 7).all() and (q_out[-1] == 7).all()
+    out = torch.full_like(q_out, 7.0)
+    s.attend(q=pad(s.q), out=out)
+    assert (out[:4] == 7).all() and (out[-1] == 7).all()
+    s.kp, s.vp = good
+    s.check(out[4:-1])
