@@ -35,7 +35,7 @@ struct AppendArgs {
   const float* table;  // (positions, rot): rot / 2 cosines, then as many sines; null: no rotation
   int positions, rot, pairs;
   int heads, d;
-  unsigned row_ctas;
+  unsigned check_ctas;
   unsigned* status;
 };
 
@@ -95,17 +95,17 @@ constexpr int kAppendThreads = 256;
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
   after_previous_kernel();
   const int per_head = a.d / 16, per_token = a.heads * per_head;
-  const long long unit = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
-  const long long tl = unit / per_token;
   PagedSeq s;
-  if (blockIdx.x >= a.row_ctas) {
-    // The CTAs behind the rows' check a sequence a thread: one that contradicts
-    // itself may have no row.  (In the rows' CTAs the same check made 65,536
-    // tokens 37.3 us.)
-    const long long b = unit - (long long)a.row_ctas * kAppendThreads;
+  if (blockIdx.x < a.check_ctas) {
+    // The first CTAs check a sequence a thread: one that contradicts itself may
+    // have no row.  (In the rows' CTAs the same check made 65,536 tokens 37.3
+    // us, in CTAs behind them 34.1; so 33.6, as without it.)
+    const long long b = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
     if (b < a.p.batch && !paged_seq(a.p, (int)b, &s)) atomicOr(a.status, kStatusBadPaged);
     return;
   }
+  const long long unit = (long long)(blockIdx.x - a.check_ctas) * kAppendThreads + threadIdx.x;
+  const long long tl = unit / per_token;
   if (tl >= a.p.rows) return;
   const int t = (int)tl, w = (int)(unit - tl * per_token);
   const int h = w / per_head, c = w - h * per_head;
@@ -1083,10 +1083,9 @@ int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, co
   a.d = cache->d;
   a.status = cache->status;
   const long long units = (long long)a.p.rows * (width / 16);
-  const long long row_ctas = (units + hstu::kAppendThreads - 1) / hstu::kAppendThreads;
-  const long long grid = row_ctas + ((long long)a.p.batch + hstu::kAppendThreads - 1) / hstu::kAppendThreads;
+  a.check_ctas = ((unsigned)a.p.batch + hstu::kAppendThreads - 1) / hstu::kAppendThreads;
+  const long long grid = a.check_ctas + (units + hstu::kAppendThreads - 1) / hstu::kAppendThreads;
   if (grid > 0x7fffffffLL) return HSTU_ERR_INVALID_ARG;
-  a.row_ctas = (unsigned)row_ctas;
   return hstu::status_of(hstu::launch_after(hstu::append_kernel, (int)grid, hstu::kAppendThreads, 0,
                                             reinterpret_cast<cudaStream_t>(stream), a));
 }
