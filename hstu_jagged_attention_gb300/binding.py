@@ -818,6 +818,8 @@ def hstu_cache_create(k_pages, v_pages) -> Cache:
     shape = k_pages.shape
     if len(shape) != 4 or not k_pages.is_cuda:
         raise ValueError("k_pages must be a device tensor (num_pages, page_size, heads, d)")
+    if k_pages.device.index != _torch._C._cuda_getDevice():  # the cache is the current device's
+        raise ValueError(f"k_pages is on {k_pages.device}, which is not the current device")
     _refuse(k_pages, _bf16, shape, k_pages.device, "k_pages")
     _refuse(v_pages, _bf16, shape, k_pages.device, "v_pages")
     stride = _odd_row_stride(k_pages.stride(), shape, "k_pages")

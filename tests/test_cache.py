@@ -295,3 +295,17 @@ def test_norm_gradient_against_differences(gate, residual):
             down[at] -= step
             diff = (loss(**{name: up}) - loss(**{name: down})) / (2 * step)
             assert abs(diff - got[at]) <= 1e-6 * (1 + abs(diff)), (name, at)
+
+
+def test_a_cache_of_another_device_is_refused(monkeypatch):
+    torch = pytest.importorskip("torch")
+
+    class Pool:  # what the binding asks of a tensor on the second GPU
+        shape, is_cuda, dtype = torch.Size((4, 16, 2, 64)), True, torch.bfloat16
+        device = torch.device("cuda:1")
+        stride = staticmethod(lambda: (16 * 128, 128, 64, 1))
+        data_ptr = staticmethod(lambda: 1 << 20)
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    with pytest.raises(ValueError, match="current device"):
+        binding.hstu_cache_create(Pool, Pool)
