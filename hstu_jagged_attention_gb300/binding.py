@@ -796,7 +796,10 @@ class PagedBatch:
                     raise ValueError(f"{name} must be a device tensor (or a numpy array)")
                 if a.device != self.device:
                     raise ValueError(f"{name} is on {a.device}, not on {self.device}")
-        self.keep, self.batch, self.max_q = arrays, batch, int(max_q)
+        if max_q < 0:
+            raise ValueError(f"max_q must not be negative, not {max_q}")
+        # (the struct's field has 32 bits)
+        self.keep, self.batch, self.max_q = arrays, batch, min(int(max_q), 2 ** 31 - 1)
         at = {n: (a.ctypes.data if self.host else a.data_ptr()) for n, a in arrays.items()}
         self._fields = (at["q_offsets"], at["kv_lens"], at.get("num_targets"), at["page_table"], batch,
                         shapes["page_table"][1], self.max_q)
@@ -806,6 +809,8 @@ class PagedBatch:
         """A pointer to the C struct for tensors of ``rows`` rows."""
         s = self._structs.get(rows)
         if s is None:
+            if rows >= 2 ** 31:
+                raise ValueError(f"{rows} rows: a call takes at most 2^31 - 1")
             s = self._structs[rows] = ctypes.byref(_PagedBatch(*self._fields, int(rows)))
         return s
 

@@ -309,3 +309,22 @@ def test_a_cache_of_another_device_is_refused(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     with pytest.raises(ValueError, match="current device"):
         binding.hstu_cache_create(Pool, Pool)
+
+
+@pytest.mark.parametrize("max_q", [2 ** 31, 2 ** 32, 2 ** 32 + 1, 2 ** 63])
+def test_a_bound_past_32_bits_is_a_bound(max_q):
+    batch, num_pages, rows = make_batch([100, 40], [3, 5], 16)
+    good = binding.hstu_cache_slots(batch, num_pages, 16, rows)
+    large, _, _ = make_batch([100, 40], [3, 5], 16, max_q=max_q)
+    got = binding.hstu_cache_slots(large, num_pages, 16, rows)
+    assert good[2] and got[2] and np.array_equal(good[0], got[0])
+
+
+def test_sizes_that_do_not_fit_are_refused():
+    batch, num_pages, rows = make_batch([100, 40], [3, 5], 16)
+    for n in (2 ** 31, 2 ** 32 + rows):
+        with pytest.raises(ValueError):
+            batch.struct(n)
+    for max_q in (-1, -2 ** 32 + 5):
+        with pytest.raises(ValueError):
+            make_batch([100, 40], [3, 5], 16, max_q=max_q)
