@@ -722,7 +722,7 @@ def _odd_row_stride(step, shape, what: str) -> int:
         if step[i] != width and shape[i] != 1:
             raise ValueError(f"{what}: the values of a row must be packed")
         width *= shape[i]
-    return step[0] if shape[0] > 1 else max(step[0], width)
+    return step[0] if shape[0] > 1 else width
 
 
 def _packed(t, shape, device, what: str) -> int:

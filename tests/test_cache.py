@@ -328,3 +328,17 @@ def test_sizes_that_do_not_fit_are_refused():
     for max_q in (-1, -2 ** 32 + 5):
         with pytest.raises(ValueError):
             make_batch([100, 40], [3, 5], 16, max_q=max_q)
+
+
+def test_the_stride_of_a_single_row_does_not_matter():
+    torch = pytest.importorskip("torch")
+    binding._load_torch()
+    cpu = torch.device("cpu")
+    x = torch.zeros(600, dtype=torch.bfloat16)
+    for step in (0, 1, 13, 64, 300):
+        row = x.as_strided((1, 2, 32), (step, 32, 1))
+        assert binding._row_stride(row, row.shape, cpu, "x") == 64
+        flat = x.as_strided((1, 64), (step, 1))
+        assert binding._row_stride(flat, flat.shape, cpu, "x") == 64
+    rows = x.as_strided((2, 64), (72, 1))
+    assert binding._row_stride(rows, rows.shape, cpu, "x") == 72
