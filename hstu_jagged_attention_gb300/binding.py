@@ -811,6 +811,8 @@ class PagedBatch:
         if s is None:
             if rows >= 2 ** 31:
                 raise ValueError(f"{rows} rows: a call takes at most 2^31 - 1")
+            if len(self._structs) >= 8:  # a batch is called with a few row counts, if not one
+                self._structs.clear()
             s = self._structs[rows] = ctypes.byref(_PagedBatch(*self._fields, int(rows)))
         return s
 

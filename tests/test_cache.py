@@ -1,6 +1,7 @@
 """The paged cache without a GPU: slots, shares of work, refusals, and the
 64-bit forms against one another."""
 import ctypes
+import gc
 
 import numpy as np
 import pytest
@@ -342,3 +343,14 @@ def test_the_stride_of_a_single_row_does_not_matter():
         assert binding._row_stride(flat, flat.shape, cpu, "x") == 64
     rows = x.as_strided((2, 64), (72, 1))
     assert binding._row_stride(rows, rows.shape, cpu, "x") == 72
+
+
+def test_a_batch_keeps_few_structs():
+    batch, _, _ = make_batch([100], [1], 16)
+    count = lambda: sum(isinstance(x, binding._PagedBatch) for x in gc.get_objects())
+    gc.collect()
+    before = count()
+    for rows in range(1, 200):
+        assert batch.struct(rows) is batch.struct(rows)
+    gc.collect()
+    assert 0 < count() - before <= 8
