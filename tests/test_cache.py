@@ -347,7 +347,7 @@ def test_the_stride_of_a_single_row_does_not_matter():
 
 def test_a_batch_keeps_few_structs():
     batch, _, _ = make_batch([100], [1], 16)
-    count = lambda: sum(isinstance(x, binding._PagedBatch) for x in gc.get_objects())
+    count = lambda: sum(type(x) is binding._PagedBatch for x in gc.get_objects())
     gc.collect()
     before = count()
     for rows in range(1, 200):
