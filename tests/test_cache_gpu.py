@@ -590,3 +590,164 @@ def test_rows_before_the_first_sequence_stay(new):
     assert (out[:4] == 7).all() and (out[-1] == 7).all()
     s.kp, s.vp = good
     s.check(out[4:-1])
+
+
+# table widths (pages of 16) and new tokens that send a call to each of the
+# kernels: shares of 16-row tiles, 128-row tiles
+FORMS = [(600, [1, 1, 1]), (600, [5, 1, 16]), (40, [70, 3, 130])]
+
+
+class Growing:
+    """Sequences that grow by ``new`` tokens a step, with their device arrays."""
+
+    def __init__(self, hist, new, width, steps, heads, d, seed):
+        self.hist, self.new, self.steps = np.array(hist), np.array(new), steps
+        pages = -(-(self.hist + steps * self.new) // 16)
+        rng = np.random.default_rng(seed)
+        self.table = np.zeros((len(new), max(int(pages.max()), width)), dtype=np.int32)
+        order, at = rng.permutation(int(pages.sum())), 0
+        for b, n in enumerate(pages):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        gen = torch.Generator().manual_seed(seed)
+        self.kp, self.vp = (randn(gen, at, 16, heads, d, sigma=0.5).cuda() for _ in range(2))
+        self.off = np.concatenate([[0], np.cumsum(self.new)]).astype(np.int32)
+        rows = int(self.off[-1])
+        self.qkv = randn(gen, steps, 3, rows, heads, d, sigma=0.5).cuda()
+        self.q, self.k, self.v = (torch.zeros(rows, heads, d, device="cuda", dtype=torch.bfloat16)
+                                  for _ in range(3))
+        self.out = torch.zeros_like(self.q)
+        i32 = lambda x: torch.from_numpy(np.asarray(x, dtype=np.int32)).cuda()
+        self.kv, self.table_d = i32(self.hist + self.new), i32(self.table)
+        self.batch = binding.PagedBatch(i32(self.off), self.kv, self.table_d, int(self.new.max()))
+        self.cache = binding.hstu_cache_create(self.kp, self.vp)
+
+    def workspace(self):
+        return torch.zeros(binding.hstu_cache_workspace_bytes(self.cache), device="cuda", dtype=torch.uint8)
+
+    def call(self, workspace, stream=None):
+        binding.hstu_cache_append(self.cache, self.batch, self.k, self.v, stream=stream)
+        binding.hstu_attn_fwd_cache(self.cache, self.batch, self.q, 0.125, 1 / 600, self.out,
+                                    workspace=workspace, stream=stream)
+
+    def capture(self, workspace):
+        self.kv.copy_(torch.from_numpy((self.hist + self.new).astype(np.int32)))
+        keep = self.kp.clone(), self.vp.clone()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            self.call(workspace)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            self.call(workspace)
+        self.kp.copy_(keep[0]), self.vp.copy_(keep[1])
+        return graph
+
+    def step(self, i):
+        """Step i's inputs, in the arrays that the graph reads."""
+        self.kv.copy_(torch.from_numpy((self.hist + (i + 1) * self.new).astype(np.int32)))
+        for x, y in zip((self.q, self.k, self.v), self.qkv[i]):
+            x.copy_(y)
+        self.out.fill_(7.0)
+
+    def check(self, i):
+        kv = self.hist + (i + 1) * self.new
+        for b in range(len(self.new)):  # the new keys and values are in their places
+            p = np.arange(kv[b] - self.new[b], kv[b])
+            rows = slice(int(self.off[b]), int(self.off[b + 1]))
+            at = torch.from_numpy(self.table[b, p // 16].astype(np.int64)), torch.from_numpy(p % 16)
+            assert torch.equal(self.kp[at], self.k[rows]) and torch.equal(self.vp[at], self.v[rows])
+        ref, bound = layer.attention(self.kp, self.vp, self.q, self.off, kv, self.table, 0.125, 1 / 600)
+        assert np.all(np.abs(layer.f64(self.out) - ref) <= 2.0 ** -8 * np.abs(ref) + bound)
+
+
+@pytest.mark.parametrize("own_workspace", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("width,new", FORMS)
+def test_captured_steps_with_parts(width, new, d, own_workspace):
+    # as the captured step above, in the forms that sum parts of cut items
+    g = Growing([30, 500, 62], new, width, 4, 2, d, seed=90 + d)
+    ws = g.workspace() if own_workspace else None
+    graph = g.capture(ws)
+    for i in range(g.steps):
+        g.step(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        g.check(i)
+    if own_workspace:
+        assert ws[8192:].any(), "no item was cut: this is not the form that the test is for"
+        assert not ws[:8192].any(), "the workspace is ready for the next call"
+
+
+def test_graphs_that_take_turns_share_a_workspace():
+    gs = [Growing([30, 500, 62], new, width, 4, 2, 64, seed=95) for width, new in FORMS]
+    ws = gs[0].workspace()
+    graphs = [g.capture(ws) for g in gs]
+    for i in range(4):
+        for g in gs:
+            g.step(i)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for g in gs:
+            g.check(i)
+
+
+@pytest.mark.parametrize("first,second", [(0, 1), (0, 2), (2, 2)])
+def test_two_streams_with_parts(first, second):
+    a, b = (Growing([3000, 90, 700], FORMS[f][1], FORMS[f][0], 1, 2, 64, seed=97 + f) for f in (first, second))
+    a.step(0), b.step(0)
+    wa, wb = a.workspace(), b.workspace()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a.call(wa), b.call(wb)
+    torch.cuda.synchronize()
+    a.check(0), b.check(0)
+    ra, rb = a.out.clone(), b.out.clone()
+    assert wa[8192:].any() and wb[8192:].any()
+    for own in (True, False):
+        for _ in range(20):
+            a.out.fill_(7.0), b.out.fill_(7.0)
+            torch.cuda.synchronize()
+            for _ in range(3):
+                a.call(wa if own else None, stream=streams[0])
+                b.call(wb if own else None, stream=streams[1])
+            torch.cuda.synchronize()
+            assert torch.equal(a.out, ra) and torch.equal(b.out, rb)
+
+
+@pytest.mark.parametrize("page", [512, 1024, 4096])
+@pytest.mark.parametrize("d,heads", [(32, 16), (64, 5), (128, 12)])
+@pytest.mark.parametrize("name", ["one token", "candidates", "candidate chunks"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_large_pages_and_many_heads(wide, name, d, heads, page):
+    hist, new, nt = SHAPES[name]
+    s = Setup(hist, new, page, heads, d, nt, seed=page + d, pad=1, width=-(-10000 // page) if wide else 1)
+    s.check(s.attend())
+    k, v = s.k.cuda(), s.v.cuda()
+    binding.hstu_cache_append(s.cache, s.batch, k, v)
+    a = s.host.keep
+    kp, vp, _ = layer.append(s.kp, s.vp, s.k, s.v, s.q, a["q_offsets"], a["kv_lens"], a["page_table"])
+    assert np.array_equal(layer.f64(s.kd), kp, equal_nan=True)
+    assert np.array_equal(layer.f64(s.vd), vp, equal_nan=True)
+
+
+@pytest.mark.parametrize("new,width", [(1, 1), (1, 700), (16, 700)])
+def test_giving_up_before_the_first_block(new, width):
+    s = Setup([5000, 40, 1300], [new, 1, 3], 32, 2, 64, seed=61 + new, width=width)
+    good, ws, q = s.attend(), s.workspace(), s.q.cuda()
+    for _ in range(5):
+        binding.hstu_set_wait_timeout_ns(1)
+        binding.hstu_set_debug_flags(binding.HSTU_DEBUG_UNSIGNALLED_WAIT)
+        try:
+            out = s.attend(q=q, workspace=ws)
+        finally:
+            binding.hstu_set_debug_flags(0)
+            binding.hstu_set_wait_timeout_ns(0)
+        after = s.attend(q=q)
+        status, site = binding.hstu_last_status()
+        assert status == binding.HSTU_ERR_TIMEOUT and site != 0
+        assert (out == 7.0).all() and torch.equal(after, good)
+        ws.zero_()
+        assert torch.equal(s.attend(q=q, workspace=ws), good)

@@ -285,3 +285,32 @@ def test_sums_of_one_cluster_with_a_row_a_cta(rows, width):
     for _ in range(100):
         o = run_bwd(dy_d, z, dev, EPS, in_d, True, 0.5)
         assert torch.equal(o["dgamma"], first["dgamma"]) and torch.equal(o["dbeta"], first["dbeta"])
+
+
+@pytest.mark.parametrize("own_workspace", [True, False])
+@pytest.mark.parametrize("rows,width", [(1000, 256), (300, 1032)])
+def test_captured_in_two_launches(rows, width, own_workspace):
+    # more rows than one cluster takes: parts in a workspace, or in an
+    # allocation inside the graph, and a second launch that sums them
+    a, dy, dz_in = make(rows, width, True, True, seed=8)
+    dev = to_gpu(a)
+    _, z = run_fwd(dev, EPS, 0.5)
+    o = run_bwd(dy.cuda(), z, dev, EPS, dz_in.cuda(), True, 0.5)
+    check_bwd(o, dy, z, a, EPS, dz_in, 0.5)
+    ws = torch.zeros(binding.hstu_norm_bwd_workspace_bytes(width), device="cuda", dtype=torch.uint8) \
+        if own_workspace else None
+    g, d = torch.zeros_like(z), torch.zeros_like(z)
+    p = {n: torch.zeros_like(t) for n, t in o.items()}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.hstu_norm_bwd(g, z, dev["gamma"], dev["beta"], EPS, u=dev["u"], dz_in=d, scale=0.5,
+                              workspace=ws, **p)
+    for _ in range(3):
+        g.copy_(dy), d.copy_(dz_in)
+        for t in p.values():
+            t.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p[n], o[n]) for n in o)
+    assert ws is None or ws.any(), "the gradient ran in one launch"
