@@ -1012,7 +1012,7 @@ int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int p
   w.heads = heads;
   w.extra = extra;
   w.tile_rows = tile_rows;
-  w.tiles = v.rows > 0 && v.batch > 0 ? (v.max_q + tile_rows - 1) / tile_rows : 0;
+  w.tiles = v.rows > 0 && v.batch > 0 && v.max_q > 0 ? (v.max_q - 1) / tile_rows + 1 : 0;
   while ((1 << w.kb_shift) < block_keys) ++w.kb_shift;
   if (units_bound(v, heads, w.tiles, w.kb_shift, extra) > kMostUnits) return HSTU_ERR_INVALID_ARG;
   auto units_of = [&](int e) {
@@ -1105,13 +1105,13 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   hstu::PagedWork w{};
   w.heads = heads;
   w.tile_rows = hstu::kStepRows;
-  w.tiles = (p.max_q + w.tile_rows - 1) / w.tile_rows;
+  w.tiles = (p.max_q - 1) / w.tile_rows + 1;
   w.kb_shift = hstu::kStepShift;  // both kernels' blocks have 128 keys
   w.extra = item_units(d);
   const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra));
   if (tiled) {
     w.tile_rows = HSTU_BLOCK_M;
-    w.tiles = (p.max_q + w.tile_rows - 1) / w.tile_rows;
+    w.tiles = (p.max_q - 1) / w.tile_rows + 1;
   }
   const long long most = units_bound(p, heads, w.tiles, w.kb_shift, w.extra);
   if (most > kMostUnits) return HSTU_ERR_INVALID_ARG;

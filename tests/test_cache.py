@@ -354,3 +354,11 @@ def test_a_batch_keeps_few_structs():
         assert batch.struct(rows) is batch.struct(rows)
     gc.collect()
     assert 0 < count() - before <= 8
+
+
+@pytest.mark.parametrize("tile", [2 ** 30, 2 ** 31 - 1])
+def test_a_tile_of_any_size_holds_all_rows(tile):
+    batch, num_pages, rows = make_batch([100, 0, 300], [9, 40, 1], 16)
+    args = (batch, num_pages, 16, rows, 2)
+    assert np.array_equal(binding.hstu_cache_worklist(*args, tile, 128, 10),
+                          binding.hstu_cache_worklist(*args, 64, 128, 10))
