@@ -192,7 +192,6 @@ __host__ __device__ constexpr int step_per_sm(int d) { return d == 128 ? 1 : 2; 
 struct StepArgs {
   PagedView p;
   PagedWork w;     // total and per are found by the kernel
-  int min_units;
   int stages;
   int red_rows;    // rows of a tile that can exist: min(max_q, tile_rows)
   const uint16_t* q;
@@ -708,7 +707,7 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS)
       for (int x = threadIdx.x; x < a.red_rows * step_red_stride(D); x += C::THREADS) red[x] = 0.f;
     __syncthreads();
   } else {
-    if (!paged_locate<C::WARPS + 1, false>(a.p, &w, a.min_units, &m->start, a.status, &c, &g)) return;
+    if (!paged_locate<C::WARPS + 1, false>(a.p, &w, &m->start, a.status, &c, &g)) return;
   }
   const StepWait wt{a.timeout_ns, &m->abort_flag, a.status};
   if (warp == C::WARPS)
@@ -781,8 +780,7 @@ cudaError_t launch_step(const CUtensorMap& tk, const CUtensorMap& tv, long long 
     return launch_after_in_clusters(kStepCluster, step_kernel<D, true>,
                                     kStepCluster * a.w.tiles * a.p.batch * a.w.heads, C::THREADS, bytes,
                                     stream, tk, tv, a);
-  const int grid = (int)std::min<long long>((long long)PER_SM * sms,
-                                            (most + a.min_units - 1) / a.min_units);
+  const int grid = (int)std::min<long long>((long long)PER_SM * sms, most);
   return launch_after(step_kernel<D, false>, grid, C::THREADS, bytes, stream, tk, tv, a);
 }
 
@@ -1143,7 +1141,6 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     hstu::PagedFwdArgs a{};
     a.p = p;
     a.w = w;
-    a.min_units = 1;
     a.out = static_cast<uint16_t*>(out);
     a.half_alpha = 0.5f * alpha;
     a.inv_n = inv_n;
@@ -1151,13 +1148,12 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     a.parts = parts;
     a.timeout_ns = hstu::host_wait_timeout_ns();
     a.debug_flags = hstu::host_debug_flags();
-    const int grid = (int)std::min<long long>(cache->sms, (most + a.min_units - 1) / a.min_units);
+    const int grid = (int)std::min<long long>(cache->sms, most);
     e = hstu::launch_fwd_paged(d, tq, cache->tk, cache->tv, a, grid, s);
   } else {
     hstu::StepArgs a{};
     a.p = p;
     a.w = w;
-    a.min_units = 1;
     a.red_rows = std::min(p.max_q, w.tile_rows);
     a.q = static_cast<const uint16_t*>(q);
     a.q_stride = q_stride;

@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   PagedSeg first;
   int n_steps;
   // a CTA without work leaves before it allocates TMEM
-  if (!paged_locate<WARPS, true>(a.p, &w, a.min_units, &start, &g_dev_words[0], &from, &first, &n_steps)) return;
+  if (!paged_locate<WARPS, true>(a.p, &w, &start, &g_dev_words[0], &from, &first, &n_steps)) return;
   if (warp == kMmaWarpQK) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),

@@ -187,7 +187,6 @@ cudaError_t read_and_clear_device_status(unsigned* status, unsigned* site);
 struct PagedFwdArgs {
   PagedView p;
   PagedWork w;
-  int min_units;
   uint16_t* out;
   float half_alpha, inv_n;
   unsigned* counters;

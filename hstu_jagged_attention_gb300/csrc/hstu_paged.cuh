@@ -54,8 +54,8 @@ struct PagedFour {
 // it has none.  COUNT: also its blocks, in *steps (a share without blocks is
 // none).  Synchronises the CTA.
 template <int WARPS, bool COUNT>
-__device__ bool paged_locate(const PagedView& p, PagedWork* w, int min_units, PagedStart<WARPS>* m,
-                             unsigned* status, PagedCursor* c, PagedSeg* g, int* steps = nullptr) {
+__device__ bool paged_locate(const PagedView& p, PagedWork* w, PagedStart<WARPS>* m, unsigned* status,
+                             PagedCursor* c, PagedSeg* g, int* steps = nullptr) {
   const int n = w->tiles * p.batch;
   const int each = (n + 32 * WARPS - 1) / (32 * WARPS);
   const int e0 = threadIdx.x * each, e1 = e0 + each < n ? e0 + each : n;
@@ -96,7 +96,7 @@ __device__ bool paged_locate(const PagedView& p, PagedWork* w, int min_units, Pa
     total.y += x.y;
   }
   w->total = total.x;
-  w->per = paged_share(*w, p.batch, gridDim.x, min_units);
+  w->per = paged_share(*w, p.batch, gridDim.x, 1);
   c->cta = blockIdx.x;
   c->u = c->u0 = (int)blockIdx.x * w->per;
   if (c->u >= total.x) return false;

@@ -14,11 +14,6 @@ def f64(t) -> np.ndarray:
     return np.asarray(t, dtype=np.float64)
 
 
-def bf16_bits(t) -> np.ndarray:
-    import torch
-    return t.detach().cpu().contiguous().view(torch.int16).numpy()
-
-
 def rotate(x: np.ndarray, pos: int, table: np.ndarray, pairs: bool) -> np.ndarray:
     """Rotate the first table.shape[1] channels of x (heads, d) to position pos."""
     y = x.copy()
