@@ -616,7 +616,8 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
 // Few items of few blocks: a cluster of kStepCluster CTAs an item, each with
 // an equal part of its blocks.  No CTA looks for its share, and the parts meet
 // in shared memory instead of behind a fence and a counter.  Bound by latency:
-// one token over 513 keys, 4 heads of 64, takes 4.4 us (6.2 as equal shares).
+// one token over 513 keys, 4 heads of 64, takes 4.4 us with pages of 16 (6.2 as
+// equal shares), 4.2 with pages of 64 (6.0).
 constexpr int kStepCluster = 8;
 
 // The cluster's sums, a share of the values each CTA, in the CTAs' order.
@@ -887,9 +888,12 @@ bool use_tiles(const PagedView& v, int d, int sms, long long units) {
 
 // Whether 16-row tiles get a cluster of CTAs an item: where all clusters run
 // at once (`clusters_at_once`), there is more than one block to share, and no
-// CTA has more than 8.  One token, 4 heads of 64, against equal shares: 4.2 us
-// and 3.9 on 64 keys, 4.1 and 6.0 on 513, 6.4 and 7.6 on 4096, 9.2 and 9.2 on
-// 8192, 15.1 and 12.6 on 16384; 9 sequences 16.9 and 18.5 on 8192.
+// CTA has more than 8.  The lengths are not known here, so the table's width
+// bounds the blocks.  One token, 4 heads of 64, pages of 64, as clusters and as
+// equal shares (either without this rule): 4.2 us and 3.9 on 64 keys, one
+// block, for which seven CTAs only start and meet; 4.2 and 6.0 on 513, 6.2 and
+// 7.7 on 4096, 8.9 and 9.3 on 8192, 14.6 and 13.3 on 16384; 9 sequences 17.1
+// and 18.5 on 8192.
 bool use_clusters(const PagedView& v, int heads, int tiles, int clusters_at_once) {
   const long long items = (long long)tiles * v.batch * heads;
   const long long blocks = (((long long)v.max_pages << v.page_shift) + hstu::kStepKeys - 1) >> hstu::kStepShift;

@@ -530,7 +530,8 @@ cudaError_t bwd(NormBwdArgs a, bool res, float* dgamma, float* dbeta, int sms, c
 
 // The lanes and vectors a lane for a row of 8 nvec channels.  Forward: a warp
 // holds up to 1024 channels, so that no barrier is needed.  Backward: one
-// vector a lane, for the registers of the next row and of the sums.
+// vector a lane, for the registers of the row and of its two sums (the rows
+// ahead lie in shared memory); above 4096 channels a CTA's 512 lanes take two.
 #define HSTU_NORM_FWD_PICK(nvec, CALL) \
   ((nvec) <= 8      ? CALL(8, 1)       \
    : (nvec) <= 16   ? CALL(16, 1)      \

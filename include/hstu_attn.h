@@ -658,16 +658,20 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
 /*
  * hstu_cache_worklist -- the shares of work hstu_attn_fwd_cache gives its
  * CTAs, on the host only (no CUDA call; the batch's arrays are host memory).
+ * (Calls that run without the workspace, see there, give each item's blocks
+ * to eight CTAs instead: rank r takes blocks r nb / 8 .. (r + 1) nb / 8 - 1.)
  * A unit is one block of block_keys keys of one (tile of tile_rows new
  * tokens, sequence, head); units are numbered with tiles outermost, then
  * sequences, heads and the blocks a tile walks: those with a key before
  * hist that its last row may see, then its own keys' other blocks.  After an
  * item's blocks come `extra` (0 .. 64) units without work, for what an item
- * costs besides them.  CTA c of `grid` takes units [c per, (c + 1) per), per = max(ceil(units / grid),
- * min_units) or, with fewer than grid / 16 items = tiles * batch * heads, at
- * least ceil(units / (16 items)): no item is cut into many more than 16.  Segment i of host_dst is eight numbers: (CTA, sequence, head,
- * tile, index of its first block in the walk, blocks, first CTA of the item,
- * CTAs that share the item).  tile_rows >= 1, block_keys a power of two.
+ * costs besides them.  CTA c of `grid` takes units [c per, (c + 1) per), per =
+ * max(ceil(units / grid), min_units) or, with fewer than grid / 16 items =
+ * tiles * batch * heads, at least ceil(units / (16 items)): no item is cut into
+ * many more than 16.  (The kernels' min_units is 1.)  Segment i of host_dst is
+ * eight numbers: (CTA, sequence, head, tile, index of its first block in the
+ * walk, blocks, first CTA of the item, CTAs that share the item).
+ * tile_rows >= 1, block_keys a power of two.
  *   capacity    segments host_dst holds; NULL host_dst: count only.
  *   *n_segments receives their number.
  * Errors: HSTU_ERR_INVALID_ARG for bad arguments or a short capacity.
@@ -818,8 +822,8 @@ int hstu_launch_shape(const hstu_plan* plan, int* grid, int* block, int* smem_by
  * HSTU_OK, HSTU_ERR_TIMEOUT if a kernel since the last call gave up on a
  * bounded wait, or else HSTU_ERR_INVALID_ARG if one skipped a sequence, page
  * or position out of range (see hstu_paged_batch); *site (may be NULL)
- * receives an internal code of the first wait that gave up (0 if none).  Kernels running concurrently share the
- * word.
+ * receives an internal code of the first wait that gave up (0 if none).
+ * Kernels running concurrently share the word.
  */
 int hstu_last_status(int* device_status, int* site);
 
