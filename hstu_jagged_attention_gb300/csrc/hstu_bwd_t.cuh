@@ -621,6 +621,7 @@ __global__ void __launch_bounds__(kBwdTThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  settle(abort_flag);
   if (warp == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),

@@ -142,6 +142,18 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
   }
 }
 
+// Called by all threads of a CTA behind its last barrier.  One that gave up
+// stays for a millisecond: its roles wait for what they themselves had in
+// flight where their own wait ran out, but one that had already issued all its
+// copies or products is gone, and those would land in another CTA's memory.
+// They take microseconds.
+__device__ __forceinline__ void settle(const volatile int* abort_flag) {
+  if (!*abort_flag) return;
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 1000000ull) {
+  }
+}
+
 // Trace event codes.
 enum : unsigned {
   kEvQkIssue = 1,  // MMA warp: QK of block index issued
@@ -402,6 +414,17 @@ __device__ __forceinline__ void drain_copies(uint32_t full0, int slots, uint32_t
   }
 }
 
+// The K producer of a CTA that gave up waits for its last copies' QK-ready,
+// which also counts on PV(t), tc <= t < tc + P, where K(t) has landed and so
+// K(t + P) may be on its way.  Those PVs do not come: the PV issuer, with the
+// steps before tc done, arrives for them.  (PV(t - P) is done, so the barrier
+// is in the phase of step t or the next one and the test is exact.)
+template <int P>
+__device__ __forceinline__ void arrive_for_dropped_pv(uint32_t qkready0, uint32_t tc) {
+  for (uint32_t t = tc; t < tc + P; ++t)
+    if (mbar_test(qkready0 + 8u * (t % P), (t / P) & 1u)) mbar_arrive(qkready0 + 8u * (t % P));
+}
+
 // TMA producers (one thread each).  A single thread's bulk-tensor copies
 // are processed one box at a time, so the K stream (with each item's Q
 // block) and the V stream have separate issuing threads in separate warps.
@@ -445,7 +468,8 @@ __device__ void role_producer(const CUtensorMap* tm_a, const CUtensorMap* tm_q, 
       // QK-ready, the first uses included: phase 0 (K landed) must be seen
       // complete before phase 1 is awaited, or a barrier still in phase 0
       // would pass the wait for phase 1.
-      ok = KQ ? wait_one(bar(C::B_SFULL + slot), ((c / C::P) & 1u) ^ 1u, w, kSiteKEmpty)
+      // No further K copies once the CTA has given up (see the PV issuer's end).
+      ok = KQ ? wait_one(bar(C::B_SFULL + slot), ((c / C::P) & 1u) ^ 1u, w, kSiteKEmpty) && !*w.abort_flag
               : wait_one(bar(C::B_QKREADY + slot), (c / C::P) & 1u, w, kSiteVEmpty);
       if (!ok) break;
       trace(a, KQ ? kEvLoadK : kEvLoadV, c);
@@ -643,6 +667,7 @@ __device__ void role_mma_pv(const FwdArgs& a, uint32_t base, uint32_t tmem, cons
   if (!ok) {
     mma_commit(bar(C::B_DRAIN + 1));
     wait_drain(bar(C::B_DRAIN + 1), 0);
+    arrive_for_dropped_pv<P>(bar(C::B_QKREADY), (uint32_t)pc.tc);
   }
 }
 
@@ -1186,6 +1211,7 @@ __global__ void __launch_bounds__(kFwdThreadsOf<D, VAR>, 1)
 
   tc_fence_before();
   __syncthreads();
+  settle(abort_flag);
   if ((a.debug_flags & kDebugTrace) && blockIdx.x == 0 && threadIdx.x < kTraceWarps)
     g_trace_n[threadIdx.x] = trace_counters()[threadIdx.x];
   if (warp == kMmaWarpQK) {

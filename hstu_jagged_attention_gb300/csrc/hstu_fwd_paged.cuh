@@ -288,15 +288,7 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
   }
   mma_commit(bar(C::B_DRAIN + 1));
   wait_drain(bar(C::B_DRAIN + 1), 0);
-  if (!ok) {
-    // The K producer waits for its last copies' QK-ready, which also counts on
-    // PV(t), tc <= t < tc + P, where K(t) has landed and so K(t + P) may be on
-    // its way.  Those PVs do not come: arrive for them.  (PV(t - P) is done, so
-    // the barrier is in the phase of step t or the next one and the test is
-    // exact.)
-    for (uint32_t t = tc; t < tc + P; ++t)
-      if (mbar_test(bar(C::B_QKREADY + (int)(t % P)), (t / P) & 1u)) mbar_arrive(bar(C::B_QKREADY + (int)(t % P)));
-  }
+  if (!ok) arrive_for_dropped_pv<P>(bar(C::B_QKREADY), tc);
 }
 
 // SiLU warpgroups: as role_silu's wide form.  A masked block keeps key k for

@@ -655,6 +655,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  settle(abort_flag);
   cluster_sync_all();  // no CTA leaves while the other's products may read its memory
   if ((a.debug_flags & kDebugTrace) && blockIdx.x == 0 && threadIdx.x < kTraceWarps)
     g_trace_n[threadIdx.x] = trace_counters()[threadIdx.x];
