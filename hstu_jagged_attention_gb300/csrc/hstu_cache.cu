@@ -1100,14 +1100,14 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   int rc = check_batch(batch, &p, cache->num_pages, cache->page_shift);
   if (rc != HSTU_OK) return rc;
   if (workspace && hstu::bad_ptr(workspace, 16)) return HSTU_ERR_INVALID_ARG;
-  if (p.rows == 0 || p.batch == 0 || p.max_q == 0) return HSTU_OK;
+  if (p.rows == 0 || p.batch == 0) return HSTU_OK;
   const int heads = cache->heads, d = cache->d;
   if (bad_rows(q, q_stride, (long long)heads * d) || hstu::bad_ptr(out, 16)) return HSTU_ERR_INVALID_ARG;
   if ((rc = check_device(cache)) != HSTU_OK) return rc;
   hstu::PagedWork w{};
   w.heads = heads;
   w.tile_rows = hstu::kStepRows;
-  w.tiles = (p.max_q - 1) / w.tile_rows + 1;
+  w.tiles = p.max_q > 0 ? (p.max_q - 1) / w.tile_rows + 1 : 1;  // a bound of 0: only the lengths are checked
   w.kb_shift = hstu::kStepShift;  // both kernels' blocks have 128 keys
   w.extra = item_units(d);
   const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra));

@@ -751,3 +751,14 @@ def test_giving_up_before_the_first_block(new, width):
         assert (out == 7.0).all() and torch.equal(after, good)
         ws.zero_()
         assert torch.equal(s.attend(q=q, workspace=ws), good)
+
+
+@pytest.mark.parametrize("width", [1, 700])
+def test_a_bound_of_no_tokens(width):
+    s = Setup([40, 7], [2, 1], 16, 2, 64, seed=82, width=width, max_q=0)
+    out = s.attend()  # both sequences have more new tokens than the bound
+    assert binding.hstu_last_status()[0] == binding.HSTU_ERR_INVALID_ARG
+    assert (out == 7.0).all()
+    s.dev["q_offsets"].zero_()
+    assert (s.attend() == 7.0).all()
+    assert binding.hstu_last_status() == (binding.HSTU_OK, 0)
