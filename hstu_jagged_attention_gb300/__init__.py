@@ -17,7 +17,10 @@ from .binding import (  # noqa: F401
     hstu_attn_fwd_plan,
     hstu_cache_append,
     hstu_cache_create,
+    hstu_cache_create_q4,
     hstu_cache_destroy,
+    hstu_cache_q4_page_bytes,
+    hstu_cache_read,
     hstu_cache_slots,
     hstu_cache_workspace_bytes,
     hstu_cache_worklist,

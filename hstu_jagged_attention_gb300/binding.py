@@ -131,6 +131,9 @@ _SIGNATURES = {
                                                ctypes.c_int, ctypes.c_float, ctypes.c_float, _VP,
                                                _VP]),
     "hstu_cache_create": (_INT, [_VP, _VP, _INT, _INT, _INT, _INT, _I64, ctypes.POINTER(_VP)]),
+    "hstu_cache_q4_page_bytes": (_INT, [_INT, _INT, _INT, ctypes.POINTER(ctypes.c_size_t)]),
+    "hstu_cache_create_q4": (_INT, [_VP, _INT, _INT, _INT, _INT, _I64, ctypes.POINTER(_VP)]),
+    "hstu_cache_read": (_INT, [_VP, _PBP, _VP, _I64, _VP, _I64, _VP]),
     "hstu_cache_destroy": (_INT, [_VP]),
     "hstu_cache_workspace": (_INT, [_VP, ctypes.POINTER(ctypes.c_size_t)]),
     "hstu_cache_slots": (_INT, [_PBP, _INT, _INT, ctypes.POINTER(_I64), _I32P]),
@@ -742,12 +745,13 @@ def _space(t, device, size: int, what: str):
 
 
 class Cache:
-    """Owner of an ``hstu_cache*`` over the caller's page pools, which it keeps alive."""
+    """Owner of an ``hstu_cache*`` over the caller's page pools, which it keeps
+    alive: ``k_pages`` and ``v_pages``, or the codes' ``pages``."""
 
-    def __init__(self, handle: int, k_pages, v_pages):
-        self.handle, self.k_pages, self.v_pages = handle, k_pages, v_pages
-        self.num_pages, self.page_size, self.heads, self.d = (int(n) for n in k_pages.shape)
-        self.device = k_pages.device
+    def __init__(self, handle: int, shape, k_pages=None, v_pages=None, pages=None):
+        self.handle, self.k_pages, self.v_pages, self.pages = handle, k_pages, v_pages, pages
+        self.num_pages, self.page_size, self.heads, self.d = (int(n) for n in shape)
+        self.device = (k_pages if pages is None else pages).device
         n = ctypes.c_size_t()
         _check(lib().hstu_cache_workspace(handle, ctypes.byref(n)), "hstu_cache_workspace")
         self.workspace_bytes = n.value
@@ -835,7 +839,35 @@ def hstu_cache_create(k_pages, v_pages) -> Cache:
     h = _VP()
     _check(lib().hstu_cache_create(k_pages.data_ptr(), v_pages.data_ptr(), *shape, stride,
                                    ctypes.byref(h)), "hstu_cache_create")
-    return Cache(h.value, k_pages, v_pages)
+    return Cache(h.value, shape, k_pages, v_pages)
+
+
+def hstu_cache_q4_page_bytes(page_size: int, heads: int, d: int) -> int:
+    """Bytes of a page of 4-bit codes."""
+    n = ctypes.c_size_t()
+    _check(lib().hstu_cache_q4_page_bytes(int(page_size), int(heads), int(d), ctypes.byref(n)),
+           "hstu_cache_q4_page_bytes")
+    return n.value
+
+
+def hstu_cache_create_q4(pages, page_size: int, heads: int, d: int) -> Cache:
+    """A cache of 4-bit codes over the pool ``pages``: a uint8 device tensor
+    (num_pages, hstu_cache_q4_page_bytes(...)), whose rows may lie further
+    apart.  Zeroed pages hold zeros."""
+    _load_torch()
+    if pages.ndim != 2 or not pages.is_cuda:
+        raise ValueError("pages must be a device tensor (num_pages, page bytes)")
+    if pages.device.index != _torch._C._cuda_getDevice():  # the cache is the current device's
+        raise ValueError(f"pages is on {pages.device}, which is not the current device")
+    shape = (pages.shape[0], hstu_cache_q4_page_bytes(page_size, heads, d))
+    _refuse(pages, _torch.uint8, shape, pages.device, "pages")
+    stride = _odd_row_stride(pages.stride(), shape, "pages")
+    if stride == 0:  # which the library takes for packed pages
+        raise ValueError("pages must not share memory")
+    h = _VP()
+    _check(lib().hstu_cache_create_q4(pages.data_ptr(), shape[0], int(page_size), int(heads), int(d), stride,
+                                      ctypes.byref(h)), "hstu_cache_create_q4")
+    return Cache(h.value, (shape[0], page_size, heads, d), pages=pages)
 
 
 def hstu_cache_destroy(cache: Cache) -> None:
@@ -881,6 +913,20 @@ def hstu_cache_append(cache: Cache, batch: PagedBatch, k, v, q=None, q_out=None,
                                    v.data_ptr(), vs, rot, qo, _cuda_stream(stream, dev))
     if code:
         _check(code, "hstu_cache_append")
+
+
+def hstu_cache_read(cache: Cache, batch: PagedBatch, k, v, stream=None) -> None:
+    """Copy the batch's tokens' keys (as held: rotated) and values out of the
+    cache into ``k`` and ``v``, bf16 (rows, heads, d)."""
+    dev, rows = cache.device, k.shape[0]
+    shape = (rows, cache.heads, cache.d)
+    _batch_on(batch, dev)
+    ks = _row_stride(k, shape, dev, "k")
+    vs = _row_stride(v, shape, dev, "v")
+    code = lib().hstu_cache_read(cache.handle, batch.struct(rows), k.data_ptr(), ks, v.data_ptr(), vs,
+                                 _cuda_stream(stream, dev))
+    if code:
+        _check(code, "hstu_cache_read")
 
 
 def hstu_attn_fwd_cache(cache: Cache, batch: PagedBatch, q, alpha: float, inv_n: float, out,

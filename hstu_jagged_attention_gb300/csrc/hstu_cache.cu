@@ -18,47 +18,17 @@
 #include <new>
 
 #include "hstu_attn.h"
+#include "hstu_bf16x8.cuh"
 #include "hstu_internal.h"
 #include "hstu_paged.cuh"
 #include "hstu_ptx.cuh"
+#include "hstu_q4.cuh"
+#include "hstu_step.cuh"
 
 namespace hstu {
 namespace {
 
 // ------------------------------------------------------------------- append
-struct AppendArgs {
-  PagedView p;
-  const uint16_t *q, *k, *v;
-  long long q_stride, k_stride, v_stride;
-  uint16_t *k_pages, *v_pages, *q_out;
-  long long page_stride;
-  const float* table;  // (positions, rot): rot / 2 cosines, then as many sines; null: no rotation
-  int positions, rot, pairs;
-  int heads, d;
-  unsigned check_ctas;
-  unsigned* status;
-};
-
-struct F8 {
-  float f[8];
-};
-
-__device__ __forceinline__ F8 unpack8(const uint4& p) {
-  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-  F8 v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v.f[2 * i] = __uint_as_float(w[i] << 16);
-    v.f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-  return v;
-}
-
-__device__ __forceinline__ uint4 pack8(const F8& v) {
-  return make_uint4(pack_bf16x2(v.f[0], v.f[1]), pack_bf16x2(v.f[2], v.f[3]),
-                    pack_bf16x2(v.f[4], v.f[5]), pack_bf16x2(v.f[6], v.f[7]));
-}
-
 // 16 channels of one head as two vectors of 8: x = channels at c0, y = those
 // at c1.  Pairs: channels 2i and 2i + 1 turn together, so each vector turns
 // within itself; halves: x[i] turns with y[i].  One rounding, at the end.
@@ -165,6 +135,43 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   }
 }
 
+// ----------------------------------------------------------------- read back
+// As the append, the other way: one thread a (token, head, 16 channels).
+__global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) {
+  after_previous_kernel();
+  const int per_head = a.d / 16, per_token = a.heads * per_head;
+  PagedSeq s;
+  if (blockIdx.x < a.check_ctas) {
+    const long long b = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
+    if (b < a.p.batch && !paged_seq(a.p, (int)b, &s)) atomicOr(a.status, kStatusBadPaged);
+    return;
+  }
+  const long long unit = (long long)(blockIdx.x - a.check_ctas) * kAppendThreads + threadIdx.x;
+  const long long tl = unit / per_token;
+  if (tl >= a.p.rows) return;
+  const int t = (int)tl, w = (int)(unit - tl * per_token);
+  const int b = paged_find(a.p, t);
+  if (b < 0 || !paged_seq(a.p, b, &s)) return;
+  const long long slot = paged_slot(a.p, b, s.kv - s.qn + (t - s.q0));
+  uint4 x[4]{};
+  if (slot < 0) {
+    atomicOr(a.status, kStatusBadPaged);  // read as zeros
+  } else {
+    const long long from = (slot >> a.p.page_shift) * a.page_stride +
+                           (slot & ((1 << a.p.page_shift) - 1)) * a.heads * a.d + 16 * w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[i] = *reinterpret_cast<const uint4*>(a.k_pages + from + 8 * i);
+      x[2 + i] = *reinterpret_cast<const uint4*>(a.v_pages + from + 8 * i);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    *reinterpret_cast<uint4*>(a.k + t * a.k_stride + 16 * w + 8 * i) = x[i];
+    *reinterpret_cast<uint4*>(a.v + t * a.v_stride + 16 * w + 8 * i) = x[2 + i];
+  }
+}
+
 // ------------------------------------------------ attention of a few tokens
 // A tile is up to 16 new tokens of one (sequence, head); it walks blocks of 128
 // keys.  The last warp copies each block's K and V rows, page by page, into a
@@ -179,8 +186,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 // (lengths, share, page numbers: three loads one after the other), then
 // 6.5 TB/s, and 1 us to join the cut items.  The first form of this kernel (64
 // keys a block, 16 a warp, the shares found serially) took 50 us.
-constexpr int kStepRows = 16;
-constexpr int kStepKeys = 128, kStepShift = 7;
 // Warps that compute: 32 keys each, two k16 steps whose chains of products
 // overlap, or at d = 128 (where one step has as many products) 16.  One warp
 // more than a multiple of four puts two on one of the SM's four schedulers, so
@@ -188,50 +193,6 @@ constexpr int kStepKeys = 128, kStepShift = 7;
 // 168, one CTA of nine.
 __host__ __device__ constexpr int step_warps(int d) { return d == 128 ? 8 : 4; }
 __host__ __device__ constexpr int step_per_sm(int d) { return d == 128 ? 1 : 2; }
-
-struct StepArgs {
-  PagedView p;
-  PagedWork w;     // total and per are found by the kernel
-  int stages;
-  int red_rows;    // rows of a tile that can exist: min(max_q, tile_rows)
-  const uint16_t* q;
-  long long q_stride;
-  uint16_t* out;
-  float half_alpha, inv_n;
-  unsigned* counters;
-  float* parts;
-  unsigned* status;
-  unsigned long long timeout_ns;
-  unsigned debug_flags;
-};
-
-struct StepWait {
-  unsigned long long limit_ns;
-  volatile int* abort_flag;
-  unsigned* status;  // [0]: bits, [1]: the first site that gave up
-};
-
-__device__ __noinline__ void step_timeout(const StepWait& w, int site) {
-  atomicOr(w.status, kStatusTimeout);
-  atomicCAS(w.status + 1, 0u, (unsigned)site);
-  *w.abort_flag = 1;
-}
-
-// Bounded wait; false once the CTA has given up.
-__device__ __forceinline__ bool step_wait(uint32_t bar, uint32_t parity, const StepWait& w, int site) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 3u) == 0) {
-      if (*w.abort_flag) return false;
-      if (globaltimer() - t0 > w.limit_ns) {
-        step_timeout(w, site);
-        return false;
-      }
-    }
-  }
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -245,14 +206,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 template <int D>
 struct StepCfg {
   static constexpr int WARPS = step_warps(D);
@@ -282,19 +235,11 @@ struct StepCfg {
 
 // Shared memory behind the stages: the warps' partial sums, the barriers,
 // and the schedule's words.
-// 8 floats between rows, so that eight rows' 8-byte stores meet all banks
-__host__ __device__ constexpr int step_red_stride(int d) { return d + 8; }
 __host__ __device__ constexpr int step_red_bytes(int rows, int d) {
   return step_warps(d) * rows * step_red_stride(d) * (int)sizeof(float);
 }
 constexpr int kStepTailBytes = 2 * 16 * 8 + 64 + 16 * 8;
 
-template <int WARPS>
-struct StepMisc {
-  int abort_flag;
-  unsigned last;  // bits: this CTA arrived last at the items it shares
-  PagedStart<WARPS + 1> start;
-};
 static_assert(sizeof(StepMisc<8>) <= 64 + 16 * 8, "misc");
 
 template <int D>
@@ -358,34 +303,6 @@ __device__ void step_produce(const CUtensorMap* tk, const CUtensorMap* tv, const
       }
   }
   __syncwarp();
-}
-
-template <int WARPS>
-__device__ __forceinline__ void step_barrier() {  // the computing warps
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
-}
-
-// An item whose blocks several CTAs share.
-struct StepCut {
-  uint16_t* out;  // its first row
-  int rows, c0, parts;
-};
-// CTA `cta`'s part of the item that it starts, or that an earlier one does.
-template <int D>
-__device__ __forceinline__ float* step_part(const StepArgs& a, int cta, bool starts) {
-  return a.parts + ((long long)cta * 2 + (starts ? 1 : 0)) * (kStepRows * D);
-}
-__device__ __forceinline__ void add4(float4& a, const float4& b) {
-  a.x += b.x;
-  a.y += b.y;
-  a.z += b.z;
-  a.w += b.w;
-}
-// Values x .. x + 3 of an item's (rows, D) sums.
-template <int D>
-__device__ __forceinline__ void step_store(uint16_t* out, int heads, int x, const float4& v, float inv_n) {
-  *reinterpret_cast<uint2*>(out + (long long)(x / D) * heads * D + x % D) =
-      make_uint2(pack_bf16x2(v.x * inv_n, v.y * inv_n), pack_bf16x2(v.z * inv_n, v.w * inv_n));
 }
 
 // CLUSTER: the item's other parts are in the cluster's other CTAs; this CTA's
@@ -574,82 +491,7 @@ __device__ void step_compute(const StepArgs& a, const PagedWork& w, PagedCursor 
     }
     step_barrier<C::WARPS>();  // red is free for the next item
   }
-  if (cut0.parts == 0 && cut1.parts == 0) return;
-  // The last CTA to arrive at a cut item sums its parts in the CTAs' order, so
-  // that the result does not depend on who is last.  One fence a CTA, after
-  // the barrier and so for all the warps' stores.
-  if (threadIdx.x == 0) {
-    __threadfence();
-    unsigned last = 0;
-    if (cut0.parts && !dead && atomicAdd(a.counters + cut0.c0, 1u) == (unsigned)(cut0.parts - 1)) last |= 1u;
-    if (cut1.parts && !dead && atomicAdd(a.counters + cut1.c0, 1u) == (unsigned)(cut1.parts - 1)) last |= 2u;
-    // ready for the next launch
-    if (last & 1u) a.counters[cut0.c0] = 0;
-    if (last & 2u) a.counters[cut1.c0] = 0;
-    m->last = last;
-  }
-  step_barrier<C::WARPS>();
-  const unsigned last = m->last;
-  if (last) __threadfence();
-#pragma unroll 1
-  for (int k = 0; k < 2; ++k) {
-    if (!(last >> k & 1u)) continue;
-    const StepCut cut = k ? cut1 : cut0;
-    for (int x = 4 * threadIdx.x; x < cut.rows * D; x += 4 * 32 * C::WARPS) {
-      float4 v = __ldcg(reinterpret_cast<const float4*>(step_part<D>(a, cut.c0, true) + x));
-#pragma unroll 1
-      for (int i = 1; i < cut.parts; i += 8) {  // eight loads in flight
-        float4 y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          y[j] = i + j < cut.parts
-                     ? __ldcg(reinterpret_cast<const float4*>(step_part<D>(a, cut.c0 + i + j, false) + x))
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) add4(v, y[j]);
-      }
-      step_store<D>(cut.out, w.heads, x, v, a.inv_n);
-    }
-  }
-}
-
-// Few items of few blocks: a cluster of kStepCluster CTAs an item, each with
-// an equal part of its blocks.  No CTA looks for its share, and the parts meet
-// in shared memory instead of behind a fence and a counter.  Bound by latency:
-// one token over 513 keys, 4 heads of 64, takes 4.4 us with pages of 16 (6.2 as
-// equal shares), 4.2 with pages of 64 (6.0).
-constexpr int kStepCluster = 8;
-
-// The cluster's sums, a share of the values each CTA, in the CTAs' order.
-template <int D>
-__device__ void step_cluster_join(const StepArgs& a, const PagedSeg& g, int rank, const float* red,
-                                  const int* abort_flag) {
-  using C = StepCfg<D>;
-  constexpr int RS = step_red_stride(D);
-  cluster_barrier();
-  const uint32_t mine = smem_u32(red), flag = smem_u32(abort_flag);
-  int stop = 0;
-#pragma unroll
-  for (int r = 0; r < kStepCluster; ++r) {
-    int f;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(f) : "r"(cluster_addr(flag, r)) : "memory");
-    stop |= f;
-  }
-  uint16_t* out = a.out + ((long long)(g.seq.q0 + kStepRows * g.qt) * a.w.heads + g.h) * D;
-  for (int x = 4 * (rank * C::THREADS + (int)threadIdx.x); x < g.walk.rows * D;
-       x += 4 * kStepCluster * C::THREADS) {
-    float4 y[kStepCluster];
-#pragma unroll
-    for (int r = 0; r < kStepCluster; ++r)
-      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(y[r].x), "=f"(y[r].y), "=f"(y[r].z), "=f"(y[r].w)
-                   : "r"(cluster_addr(mine + 4u * (uint32_t)((x / D) * RS + x % D), r))
-                   : "memory");
-#pragma unroll
-    for (int r = 1; r < kStepCluster; ++r) add4(y[0], y[r]);
-    if (!stop) step_store<D>(out, a.w.heads, x, y[0], a.inv_n);
-  }
-  cluster_barrier();  // no CTA leaves while another reads its sums
+  step_join<D, C::WARPS>(a, w, m, cut0, cut1, dead);
 }
 
 template <int D, bool CLUSTER>
@@ -687,24 +529,8 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS)
   int rank = 0;
   if constexpr (CLUSTER) {
     rank = (int)blockIdx.x % kStepCluster;
-    const int item = (int)blockIdx.x / kStepCluster;
-    c.e = item / w.heads;
-    c.h = item - c.e * w.heads;
-    g.qt = c.e / a.p.batch;
-    g.b = c.e - g.qt * a.p.batch;
-    if (!paged_seq(a.p, g.b, &g.seq) && item == g.b * w.heads && rank == 0 && threadIdx.x == 0)
-      atomicOr(a.status, kStatusBadPaged);
-    g.walk = paged_walk(g.seq, g.qt, w.tile_rows, w.kb_shift);
-    if (g.walk.nb == 0) return;  // the same for the whole cluster
-    const int from = rank * g.walk.nb / kStepCluster, to = (rank + 1) * g.walk.nb / kStepCluster;
-    w.per = 1;
-    c.cta = (int)blockIdx.x;
-    c.u = c.u0 = 0;
-    c.u1 = to - from;
-    c.i = from;
-    c.loaded = true;
-    g.h = c.h;
-    if (to == from)  // no block of its own: its sums are zero
+    if (!step_cluster_share(a, rank, &w, &c, &g)) return;  // the same for the whole cluster
+    if (c.u1 == 0)  // no block of its own: its sums are zero
       for (int x = threadIdx.x; x < a.red_rows * step_red_stride(D); x += C::THREADS) red[x] = 0.f;
     __syncthreads();
   } else {
@@ -715,7 +541,7 @@ __global__ void __launch_bounds__(StepCfg<D>::THREADS)
     step_produce<D>(&tk, &tv, a, w, c, g, base, full, empty, wt);
   else
     step_compute<D, CLUSTER>(a, w, c, g, base, full, empty, red, m, wt);
-  if constexpr (CLUSTER) step_cluster_join<D>(a, g, rank, red, &m->abort_flag);
+  if constexpr (CLUSTER) step_cluster_join<D, C::THREADS>(a, g, rank, red, &m->abort_flag);
 }
 
 constexpr int step_ring_bytes(int d) { return 128 * 1024 / step_per_sm(d); }
@@ -740,18 +566,7 @@ template <int D>
 cudaError_t step_clusters(int* n) {
   const cudaError_t e = step_prepare<D>();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kStepCluster);
-  cfg.blockDim = dim3(StepCfg<D>::THREADS);
-  cfg.dynamicSmemBytes = kStepBytesMost<D>;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kStepCluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(n, step_kernel<D, true>, &cfg);
+  return clusters_at_once(step_kernel<D, true>, StepCfg<D>::THREADS, kStepBytesMost<D>, n);
 }
 cudaError_t step_clusters_d(int d, int* n) {
   switch (d) {
@@ -821,7 +636,8 @@ int make_pool_map(CUtensorMap* m, void* ptr, int num_pages, int page_size, int h
 
 // One pool of pages with its tensor maps; immutable after creation.
 struct hstu_cache {
-  void *k_pages, *v_pages;
+  void *k_pages, *v_pages;  // null where the pages hold 4-bit codes
+  hstu::Q4Pool q4;          // whose pages are null where they hold bf16
   int num_pages, page_size, page_shift, heads, d;
   long long page_stride;
   int device, sms;
@@ -908,8 +724,51 @@ int check_geometry(int num_pages, int page_size, int* shift) {
   return HSTU_OK;
 }
 
+// Checks what both kinds of cache are made of, and notes it in *c.
+int check_cache(int num_pages, int page_size, int heads, int d, hstu_cache** cache, hstu_cache* c) {
+  if (!cache) return HSTU_ERR_INVALID_ARG;
+  *cache = nullptr;
+  if (d != 32 && d != 64 && d != 128) return HSTU_ERR_UNSUPPORTED;
+  if (heads < 1 || heads > (1 << 16) || check_geometry(num_pages, page_size, &c->page_shift) != HSTU_OK)
+    return HSTU_ERR_INVALID_ARG;
+  c->num_pages = num_pages;
+  c->page_size = page_size;
+  c->heads = heads;
+  c->d = d;
+  c->q4.tile_shift = std::min(c->page_shift, hstu::kStepShift);
+  c->q4.tiles = page_size >> c->q4.tile_shift;
+  c->q4.tile_bytes = hstu::q4_token_bytes(d) << c->q4.tile_shift;
+  return HSTU_OK;
+}
+long long q4_page_bytes(const hstu_cache& c) { return (long long)c.heads * c.q4.tiles * c.q4.tile_bytes; }
+
+// The current device becomes the cache's.
+int on_device(hstu_cache* c) {
+  const int rc = hstu::host_device_check(&c->sms);
+  if (rc != HSTU_OK) return rc;
+  return cudaGetDevice(&c->device) == cudaSuccess && hstu::device_status_words(&c->status) == cudaSuccess
+             ? HSTU_OK
+             : HSTU_ERR_CUDA;
+}
+
+int keep(const hstu_cache& c, hstu_cache** cache) {
+  *cache = new (std::nothrow) hstu_cache(c);
+  return *cache ? HSTU_OK : HSTU_ERR_NO_MEMORY;
+}
+
 bool bad_rows(const void* p, int64_t stride, long long width) {
   return hstu::bad_ptr(p, 16) || stride < width || (stride & 7);
+}
+
+// CTAs that take 16 channels a thread, behind those that check a sequence a
+// thread; `spare` rows more than there are (the 4-bit cache's kernels round up).
+int unit_grid(const PagedView& p, int width, int spare, unsigned* check_ctas, int* grid) {
+  constexpr int T = hstu::kAppendThreads;
+  *check_ctas = ((unsigned)p.batch + T - 1) / T;
+  const long long all = *check_ctas + (((long long)p.rows + spare) * (width / 16) + T - 1) / T;
+  if (all > 0x7fffffffLL) return HSTU_ERR_INVALID_ARG;
+  *grid = (int)all;
+  return HSTU_OK;
 }
 
 int check_device(const hstu_cache* c) {
@@ -924,41 +783,48 @@ extern "C" {
 
 int hstu_cache_create(void* k_pages, void* v_pages, int num_pages, int page_size, int heads, int d,
                       int64_t page_stride, hstu_cache** cache) {
-  if (!cache) return HSTU_ERR_INVALID_ARG;
-  *cache = nullptr;
-  if (d != 32 && d != 64 && d != 128) return HSTU_ERR_UNSUPPORTED;
-  int shift = 0;
-  if (heads < 1 || heads > (1 << 16) || check_geometry(num_pages, page_size, &shift) != HSTU_OK)
-    return HSTU_ERR_INVALID_ARG;
+  hstu_cache c{};
+  int rc = check_cache(num_pages, page_size, heads, d, cache, &c);
+  if (rc != HSTU_OK) return rc;
   const long long packed = (long long)page_size * heads * d;
   if (page_stride == 0) page_stride = packed;
   if (hstu::bad_ptr(k_pages, 16) || hstu::bad_ptr(v_pages, 16) || page_stride < packed ||
       (page_stride & 7) || page_stride >= (1LL << 39))
     return HSTU_ERR_INVALID_ARG;
-  hstu_cache* c = new (std::nothrow) hstu_cache{};
-  if (!c) return HSTU_ERR_NO_MEMORY;
-  c->k_pages = k_pages;
-  c->v_pages = v_pages;
-  c->num_pages = num_pages;
-  c->page_size = page_size;
-  c->page_shift = shift;
-  c->heads = heads;
-  c->d = d;
-  c->page_stride = page_stride;
-  int rc = hstu::host_device_check(&c->sms);
-  if (rc == HSTU_OK && cudaGetDevice(&c->device) != cudaSuccess) rc = HSTU_ERR_CUDA;
-  if (rc == HSTU_OK && hstu::device_status_words(&c->status) != cudaSuccess) rc = HSTU_ERR_CUDA;
-  if (rc == HSTU_OK) rc = hstu::status_of(hstu::step_clusters_d(d, &c->clusters));
+  c.k_pages = k_pages;
+  c.v_pages = v_pages;
+  c.page_stride = page_stride;
+  if ((rc = on_device(&c)) == HSTU_OK) rc = hstu::status_of(hstu::step_clusters_d(d, &c.clusters));
   if (rc == HSTU_OK)
-    rc = hstu::make_pool_map(&c->tk, k_pages, num_pages, page_size, heads, d, page_stride);
+    rc = hstu::make_pool_map(&c.tk, k_pages, num_pages, page_size, heads, d, page_stride);
   if (rc == HSTU_OK)
-    rc = hstu::make_pool_map(&c->tv, v_pages, num_pages, page_size, heads, d, page_stride);
-  if (rc != HSTU_OK) {
-    delete c;
-    return rc;
-  }
-  *cache = c;
-  return HSTU_OK;
+    rc = hstu::make_pool_map(&c.tv, v_pages, num_pages, page_size, heads, d, page_stride);
+  return rc == HSTU_OK ? keep(c, cache) : rc;
+}
+
+int hstu_cache_q4_page_bytes(int page_size, int heads, int d, size_t* bytes) {
+  if (!bytes) return HSTU_ERR_INVALID_ARG;
+  *bytes = 0;
+  hstu_cache c{}, *none;
+  const int rc = check_cache(1, page_size, heads, d, &none, &c);
+  if (rc == HSTU_OK) *bytes = (size_t)q4_page_bytes(c);
+  return rc;
+}
+
+int hstu_cache_create_q4(void* pages, int num_pages, int page_size, int heads, int d, int64_t page_stride,
+                         hstu_cache** cache) {
+  hstu_cache c{};
+  int rc = check_cache(num_pages, page_size, heads, d, cache, &c);
+  if (rc != HSTU_OK) return rc;
+  const long long packed = q4_page_bytes(c);
+  if (page_stride == 0) page_stride = packed;
+  // no page number times the stride passes 63 bits
+  if (hstu::bad_ptr(pages, 16) || page_stride < packed || (page_stride & 15) || page_stride >= (1LL << 40))
+    return HSTU_ERR_INVALID_ARG;
+  c.q4.pages = static_cast<uint8_t*>(pages);
+  c.q4.page_stride = page_stride;
+  if ((rc = on_device(&c)) == HSTU_OK) rc = hstu::status_of(hstu::step_clusters_q4(d, &c.clusters));
+  return rc == HSTU_OK ? keep(c, cache) : rc;
 }
 
 int hstu_cache_destroy(hstu_cache* cache) {
@@ -1084,11 +950,39 @@ int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, co
   a.heads = cache->heads;
   a.d = cache->d;
   a.status = cache->status;
-  const long long units = (long long)a.p.rows * (width / 16);
-  a.check_ctas = ((unsigned)a.p.batch + hstu::kAppendThreads - 1) / hstu::kAppendThreads;
-  const long long grid = a.check_ctas + (units + hstu::kAppendThreads - 1) / hstu::kAppendThreads;
-  if (grid > 0x7fffffffLL) return HSTU_ERR_INVALID_ARG;
-  return hstu::status_of(hstu::launch_after(hstu::append_kernel, (int)grid, hstu::kAppendThreads, 0,
+  int grid;
+  if ((rc = unit_grid(a.p, width, cache->q4.pages ? 15 : 0, &a.check_ctas, &grid)) != HSTU_OK) return rc;
+  if (cache->q4.pages)
+    return hstu::status_of(hstu::launch_append_q4(cache->q4, a, reinterpret_cast<cudaStream_t>(stream)));
+  return hstu::status_of(hstu::launch_after(hstu::append_kernel, grid, hstu::kAppendThreads, 0,
+                                            reinterpret_cast<cudaStream_t>(stream), a));
+}
+
+int hstu_cache_read(const hstu_cache* cache, const hstu_paged_batch* batch, void* k, int64_t k_stride, void* v,
+                    int64_t v_stride, hstu_stream_t stream) {
+  if (!cache) return HSTU_ERR_INVALID_ARG;
+  hstu::ReadArgs a{};
+  int rc = check_batch(batch, &a.p, cache->num_pages, cache->page_shift);
+  if (rc != HSTU_OK) return rc;
+  if (a.p.rows == 0 || a.p.batch == 0) return HSTU_OK;
+  const int width = cache->heads * cache->d;
+  if (bad_rows(k, k_stride, width) || bad_rows(v, v_stride, width)) return HSTU_ERR_INVALID_ARG;
+  if ((rc = check_device(cache)) != HSTU_OK) return rc;
+  a.k = static_cast<uint16_t*>(k);
+  a.v = static_cast<uint16_t*>(v);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.k_pages = static_cast<const uint16_t*>(cache->k_pages);
+  a.v_pages = static_cast<const uint16_t*>(cache->v_pages);
+  a.page_stride = cache->page_stride;
+  a.heads = cache->heads;
+  a.d = cache->d;
+  a.status = cache->status;
+  int grid;
+  if ((rc = unit_grid(a.p, width, cache->q4.pages ? 15 : 0, &a.check_ctas, &grid)) != HSTU_OK) return rc;
+  if (cache->q4.pages)
+    return hstu::status_of(hstu::launch_read_q4(cache->q4, a, reinterpret_cast<cudaStream_t>(stream)));
+  return hstu::status_of(hstu::launch_after(hstu::read_kernel, grid, hstu::kAppendThreads, 0,
                                             reinterpret_cast<cudaStream_t>(stream), a));
 }
 
@@ -1110,7 +1004,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   w.tiles = p.max_q > 0 ? (p.max_q - 1) / w.tile_rows + 1 : 1;  // a bound of 0: only the lengths are checked
   w.kb_shift = hstu::kStepShift;  // both kernels' blocks have 128 keys
   w.extra = item_units(d);
-  const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra));
+  const bool tiled = !cache->q4.pages && use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra));
   if (tiled) {
     w.tile_rows = HSTU_BLOCK_M;
     w.tiles = (p.max_q - 1) / w.tile_rows + 1;
@@ -1169,7 +1063,8 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     a.status = cache->status;
     a.timeout_ns = hstu::host_wait_timeout_ns();
     a.debug_flags = hstu::host_debug_flags();
-    e = hstu::launch_step_d(d, cache->tk, cache->tv, most, clusters, a, cache->sms, s);
+    e = cache->q4.pages ? hstu::launch_step_q4(d, cache->q4, most, clusters, a, cache->sms, s)
+                        : hstu::launch_step_d(d, cache->tk, cache->tv, most, clusters, a, cache->sms, s);
   }
   rc = hstu::status_of(e);
   if (own && cudaFreeAsync(own, s) != cudaSuccess && rc == HSTU_OK) rc = HSTU_ERR_CUDA;

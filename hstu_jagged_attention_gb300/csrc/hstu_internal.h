@@ -200,6 +200,66 @@ struct PagedFwdArgs {
 cudaError_t launch_fwd_paged(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PagedFwdArgs& a, int grid, cudaStream_t stream);
 
+// Appending a batch's keys and values to a cache (hstu_cache.cu, and
+// hstu_cache_q4.cu for one of 4-bit codes, which has no k_pages, v_pages and
+// page_stride but a Q4Pool).
+struct AppendArgs {
+  PagedView p;
+  const uint16_t *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  uint16_t *k_pages, *v_pages, *q_out;
+  long long page_stride;
+  const float* table;  // (positions, rot): rot / 2 cosines, then as many sines; null: no rotation
+  int positions, rot, pairs;
+  int heads, d;
+  unsigned check_ctas;
+  unsigned* status;
+};
+
+// The attention of few new tokens over the paged cache, on tiles of 16 rows.
+struct StepArgs {
+  PagedView p;
+  PagedWork w;     // total and per are found by the kernel
+  int stages;
+  int red_rows;    // rows of a tile that can exist: min(max_q, tile_rows)
+  const uint16_t* q;
+  long long q_stride;
+  uint16_t* out;
+  float half_alpha, inv_n;
+  unsigned* counters;
+  float* parts;
+  unsigned* status;
+  unsigned long long timeout_ns;
+  unsigned debug_flags;
+};
+
+// The pages of a cache of 4-bit codes (hstu_q4.cuh): a row of bytes each, for
+// every head its `tiles` tiles of 2^tile_shift tokens.
+struct Q4Pool {
+  uint8_t* pages;
+  long long page_stride;  // bytes
+  int tile_shift, tiles, tile_bytes;
+};
+// Reading a batch's keys and values back, from either cache.
+struct ReadArgs {
+  PagedView p;
+  uint16_t *k, *v;
+  long long k_stride, v_stride;
+  const uint16_t *k_pages, *v_pages;
+  long long page_stride;
+  int heads, d;
+  unsigned check_ctas;
+  unsigned* status;
+};
+// a.check_ctas CTAs check the sequences; the host has checked the grid.
+cudaError_t launch_append_q4(const Q4Pool& pool, const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_read_q4(const Q4Pool& pool, const ReadArgs& a, cudaStream_t stream);
+// `most`: CTAs with work, at most; clusters: a cluster of CTAs an item instead.
+cudaError_t launch_step_q4(int d, const Q4Pool& pool, long long most, bool clusters, const StepArgs& a,
+                           int sms, cudaStream_t stream);
+// Clusters of the few-token kernel that run at once.
+cudaError_t step_clusters_q4(int d, int* n);
+
 // Bits of the status word, and the words' device address (the word, then
 // the site of the first wait that gave up) on the current device.
 constexpr unsigned kStatusTimeout = 1u;

@@ -1,0 +1,149 @@
+// The 4-bit codes of a quantised cache.
+//
+//   16 neighbouring channels of a token's key or value share a scale
+//     s_j = (8 + j % 8) 2^(j / 8 - 23),  j = 0 .. 255  (2^-20 .. 1.875 2^11),
+//   the first with 7 s_j >= max |x|, and channel c is held as the integer
+//     q_c in -7 .. 7 nearest to x_c / s_j, ties away from zero.
+//
+// Why this form: an integer below 8 times a scale of four significant bits is
+// a bf16 number, so what is held is exact in bf16 and the products over it
+// need no rounding of their own; a scale's byte becomes a bf16 with a shift
+// and an add; the range needs no calibration.  4.5 bits a channel.  A float
+// format of 4 bits would cost the same bits and one more product of rounding.
+//
+// x is a bf16 number, and so is every tie (n + 1/2) s_j, n < 7: eight bits
+// hold (2 n + 1)(8 + j % 8).  So any other x is off a tie by 2^-8 of it or
+// more, and a product with (1 + 2^-16) / s_j, its errors of a few 2^-24
+// included, rounds to the same integer as the exact quotient does, and a tie
+// away from zero.  The same holds for 7 s_j against max |x|.
+//
+// A 32-bit word holds 8 channels: channel 2 i in bits 4 i .. 4 i + 3, channel
+// 2 i + 1 in bits 16 + 4 i .. 16 + 4 i + 3, two's complement, so that one
+// shift and one logical operation make neighbours a bf16x2.  A tile is
+// min(page_size, 128) tokens of one head: their keys' codes (d / 2 bytes a
+// token), values' codes, keys' scales (d / 16 bytes a token) and values'
+// scales; it is one contiguous piece, so that a block of keys with its values
+// comes with one bulk copy a page.
+#pragma once
+
+#include <stdint.h>
+
+#include "hstu_bf16x8.cuh"
+
+namespace hstu {
+namespace {
+
+constexpr int kQ4Group = 16;  // channels of a scale
+
+// Bytes of a token in one head: its key and its value.
+__host__ __device__ constexpr int q4_token_bytes(int d) { return 2 * (d / 2 + d / kQ4Group); }
+
+// Byte of token row r of a tile: its keys' or values' codes, and scales.
+template <int D>
+struct Q4Tile {
+  static constexpr int CODEB = D / 2, SCALEB = D / kQ4Group;
+  static __device__ __forceinline__ int codes(int shift, int which, int r) {
+    return (which * CODEB << shift) + r * CODEB;
+  }
+  static __device__ __forceinline__ int scales(int shift, int which, int r) {
+    return ((2 * CODEB + which * SCALEB) << shift) + r * SCALEB;
+  }
+};
+
+// ---------------------------------------------------------------- from codes
+// bf16 bits of 16 s_j, in both halves of a word, for two scales' bytes j.
+__device__ __forceinline__ uint32_t q4_scales(uint32_t j_lo, uint32_t j_hi) {
+  return ((j_lo | j_hi << 16) << 4) + (111u << 7) * 0x10001u;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// A scale pair as the products below want it: 16 s and -24 s (exact).
+struct Q4Scale {
+  uint32_t s16, s24;
+};
+__device__ __forceinline__ Q4Scale q4_scale(uint32_t j_lo, uint32_t j_hi) {
+  const uint32_t s = q4_scales(j_lo, j_hi);
+  return Q4Scale{s, mul_bf16x2(s, 0xbfc0bfc0u)};
+}
+// The codes in nibble I of both halves of w: 1 + (8 + q) / 16 as bf16, then
+// 16 s (1 + (8 + q) / 16) - 24 s = q s, exact.
+template <int I>
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, const Q4Scale& s) {
+  const uint32_t at = I == 0 ? w << 3 : w >> (4 * I - 3);
+  return fma_bf16x2((at & 0x00780078u) ^ 0x3fc03fc0u, s.s16, s.s24);
+}
+// A word's 8 channels in their order.
+__device__ __forceinline__ uint4 q4_word(uint32_t w, const Q4Scale& s) {
+  return make_uint4(q4_pair<0>(w, s), q4_pair<1>(w, s), q4_pair<2>(w, s), q4_pair<3>(w, s));
+}
+
+// ------------------------------------------------------------------ to codes
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// NaN as 0, infinities as the largest finite number.
+__device__ __forceinline__ uint32_t q4_finite(uint32_t x) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 32; i += 16) {
+    uint32_t h = x >> i & 0xffffu;
+    if ((h & 0x7fffu) > 0x7f80u)
+      h = 0;
+    else if ((h & 0x7fffu) == 0x7f80u)
+      h -= 1;
+    r |= h << i;
+  }
+  return r;
+}
+
+// A group's codes (two words of 8 channels) and its scale's byte.
+__device__ __forceinline__ uint2 q4_quantise(uint4 x0, uint4 x1, uint32_t* scale) {
+  uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max_u16x2(m, x[i] & 0x7fff7fffu);
+  m = max(m & 0xffffu, m >> 16);
+  if (m >= 0x7f80u) {  // something is not finite
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = q4_finite(x[i]);
+      m = max_u16x2(m, x[i] & 0x7fff7fffu);
+    }
+    m = max(m & 0xffffu, m >> 16);
+  }
+  // max / 7, less 2^-16 of it, rounded up to four significant bits
+  const float seventh = __uint_as_float(m << 16) * (float)((1.0 - 0x1p-16) / 7.0);
+  const int up = (int)((__float_as_uint(seventh) + 0xfffffu) >> 20) - (107 << 3);
+  const int j = min(max(up, 0), 255);
+  *scale = (uint32_t)j;
+  const float s = __uint_as_float((uint32_t)(j + (107 << 3)) << 20);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  inv *= 1.0f + 0x1p-16f;
+  const float most = up > 255 ? 7.0f * s : __uint_as_float(0x7f7fffffu);  // past the largest scale: saturated
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a = __uint_as_float(x[i] << 16), b = __uint_as_float(x[i] & 0xffff0000u);
+    if (up > 255) {
+      a = fminf(fmaxf(a, -most), most);
+      b = fminf(fmaxf(b, -most), most);
+    }
+    // the integer in the low bits of 1.5 2^23 + x / s
+    const float2 y = __ffma2_rn(make_float2(a, b), make_float2(inv, inv), make_float2(12582912.f, 12582912.f));
+    const uint32_t both = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x5410);
+    w[i >> 2] |= (both & 0x000f000fu) << (4 * (i & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+}  // namespace
+}  // namespace hstu

@@ -597,6 +597,39 @@ int hstu_cache_create(void* k_pages, void* v_pages, int num_pages, int page_size
 int hstu_cache_destroy(hstu_cache* cache);
 
 /*
+ * A cache of 4-bit codes -- the same cache in 4.5 bits a channel instead of
+ * 16: hstu_cache_append quantises what it writes, hstu_attn_fwd_cache and
+ * hstu_cache_read take what is held.  Of a token's key or value in one head,
+ * rounded to bf16 (after the rotation), 16 neighbouring channels share a scale
+ *
+ *   s_j = (8 + j % 8) 2^(j / 8 - 23),   j = 0 .. 255 (2^-20 .. 3840),
+ *
+ * the first with 7 s_j >= max |x| (j = 255: the others saturate), and a
+ * channel is held as the integer in -7 .. 7 nearest to x / s_j, ties away from
+ * zero.  It stands for that integer times s_j, which is a bf16 number exactly.
+ * NaN is held as 0, and infinities as the largest finite numbers.
+ *
+ * Layout: page p starts p * page_stride bytes behind `pages` and holds, for
+ * each head, page_size / T tiles of T = min(page_size, 128) tokens, one behind
+ * the other.  A tile is the keys' codes (T rows of d / 2 bytes), the values'
+ * codes, the keys' scales (T rows of d / 16 bytes, j of each 16 channels) and
+ * the values' scales: T * d * 9 / 8 bytes.  A 32-bit little-endian word of
+ * codes holds 8 channels: channel 2 i in bits 4 i .. 4 i + 3 and channel 2 i +
+ * 1 in bits 16 + 4 i .. 16 + 4 i + 3, two's complement.  Zeroed pages hold
+ * zeros; any bytes stand for finite numbers.
+ *
+ * hstu_cache_q4_page_bytes  *bytes of a packed page (host only, no CUDA call).
+ * hstu_cache_create_q4  as hstu_cache_create.
+ *   pages        device, 16-byte aligned, owned by the caller.
+ *   page_stride  bytes, a multiple of 16, >= a packed page; 0: packed.
+ * hstu_cache_destroy, hstu_cache_workspace, hstu_cache_append,
+ * hstu_attn_fwd_cache and hstu_cache_read take such a cache like the other.
+ */
+int hstu_cache_q4_page_bytes(int page_size, int heads, int d, size_t* bytes);
+int hstu_cache_create_q4(void* pages, int num_pages, int page_size, int heads, int d, int64_t page_stride,
+                         hstu_cache** cache);
+
+/*
  * hstu_paged_batch -- a batch of new tokens against a cache.  The arrays are
  * device memory (4-byte aligned) and are read by the kernels when they run,
  * never by the host: a captured call replays with the lengths and pages that
@@ -619,14 +652,15 @@ int hstu_cache_destroy(hstu_cache* cache);
  *                (a padded one) are neither read nor written as tokens.
  *
  * What the device finds wrong is skipped and reported by hstu_last_status
- * as HSTU_ERR_INVALID_ARG, by the append and by the attention (a call without
+ * as HSTU_ERR_INVALID_ARG, by the append, the attention and the reading (a call without
  * rows launches nothing and reports nothing):
  *   - a sequence whose offsets decrease or leave [0, rows], with n_b > max_q,
  *     kv_lens[b] < n_b, more tokens than max_pages pages hold, or
  *     num_targets[b] outside [0, n_b]: none of its rows is written (whether
  *     it has new tokens or not, it is reported);
  *   - a page number outside [0, num_pages): an append there is dropped, and
- *     the attention reads the page as zeros (its keys add nothing).
+ *     the attention and hstu_cache_read read the page as zeros (its keys add
+ *     nothing).
  * max_pages * page_size is at most 2^30, and so are the attention's units:
  * the tiles of 16 or 128 rows in max_q, times batch, heads and (a few more
  * than) the blocks of 128 keys in max_pages (HSTU_ERR_INVALID_ARG).
@@ -714,6 +748,21 @@ typedef struct hstu_rotary {
 int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, const void* q,
                       int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, const hstu_rotary* rotary, void* q_out, hstu_stream_t stream);
+
+/*
+ * hstu_cache_read -- copy the batch's tokens back out of the cache, keys as
+ * they are held (rotated): row t of k and v receives the bf16 numbers that the
+ * cache holds for, or that its codes stand for of, the token that an append of
+ * the same batch writes from row t.  With q_offsets that hold whole sequences
+ * (kv_lens[b] rows each) it reads whole histories, packed as hstu_attn_fwd
+ * takes them.  num_targets changes nothing but what is refused.
+ *   k, v   bf16 device (rows, heads, d), rows k_stride / v_stride elements
+ *          apart, as hstu_cache_append's; written for the rows of the
+ *          sequences only.
+ * Enqueues one kernel and allocates nothing.  Errors: as hstu_cache_append.
+ */
+int hstu_cache_read(const hstu_cache* cache, const hstu_paged_batch* batch, void* k, int64_t k_stride,
+                    void* v, int64_t v_stride, hstu_stream_t stream);
 
 /*
  * hstu_attn_fwd_cache -- the attention of the new tokens over the cache,

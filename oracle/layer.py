@@ -110,3 +110,68 @@ def norm_bwd(dy, z, gamma, beta, eps, u=None, dz_in=None, scale=1.0):
         dz = dz + f64(dz_in)
     return dict(dz=dz, dx=scale * dz, du=dy * (xhat * gamma + beta), dgamma=(g * xhat).sum(axis=0),
                 dbeta=g.sum(axis=0))
+
+
+# ------------------------------------------------------ a cache of 4-bit codes
+SCALES = np.array([(8 + j % 8) * 2.0 ** (j // 8 - 23) for j in range(256)])
+
+
+def q4_codes(x):
+    """(codes, scale numbers) of x (..., d): the integer nearest to x / s, ties
+    away from zero, s the first scale with 7 s >= the group's largest |x|."""
+    g = f64(x)
+    g = np.where(np.isnan(g), 0.0, np.where(np.isinf(g), np.sign(g) * (2.0 - 2.0 ** -7) * 2.0 ** 127, g))
+    g = g.reshape(*g.shape[:-1], -1, 16)
+    most = np.abs(g).max(axis=-1)
+    j = np.minimum(np.searchsorted(7 * SCALES, most), 255)  # the first that holds it
+    q = np.abs(g) / SCALES[j][..., None]
+    code = (np.sign(g) * np.minimum(np.floor(q + 0.5), 7)).astype(np.int64)
+    return code.reshape(*code.shape[:-2], -1), j
+
+
+def q4_values(code, j):
+    return (code.reshape(*j.shape, 16) * SCALES[j][..., None]).reshape(code.shape)
+
+
+def q4_held(x):
+    """What the cache holds for x (..., d)."""
+    return q4_values(*q4_codes(x))
+
+
+def _q4_places(page, heads, d):
+    """Byte places in a page: (keys' codes, values' codes), each (page, heads, d),
+    with the bit that a channel's nibble starts at, and the scales' (page,
+    heads, d / 16)."""
+    t = min(page, 128)
+    p, h, c = (np.arange(n) for n in (page, heads, d))
+    tile = (h[None, :] * (page // t) + p[:, None] // t) * (t * d * 9 // 8)
+    bit = 32 * (c // 8) + 16 * (c % 2) + 4 * (c % 8 // 2)
+    row = (p % t)[:, None, None]
+    codes = [tile[..., None] + w * t * d // 2 + row * (d // 2) + bit // 8 for w in (0, 1)]
+    g = np.arange(d // 16)
+    scales = [tile[..., None] + t * d + w * t * d // 16 + row * (d // 16) + g for w in (0, 1)]
+    return codes, bit % 8, scales
+
+
+def q4_pack(k_pages, v_pages):
+    """Pages of bytes (num_pages, bytes) that hold the values (num_pages, page, heads, d)."""
+    n, page, heads, d = k_pages.shape
+    codes, shift, scales = _q4_places(page, heads, d)
+    out = np.zeros((n, page * heads * d * 9 // 8), dtype=np.uint8)
+    for x, at, sat in zip((k_pages, v_pages), codes, scales):
+        code, j = q4_codes(x)
+        for s in (0, 4):  # no byte twice in one assignment
+            out[:, at[..., shift == s]] |= ((code[..., shift == s] & 15) << s).astype(np.uint8)
+        out[:, sat] = j
+    return out
+
+
+def q4_unpack(pages, page, heads, d):
+    """(keys, values) in float64 (num_pages, page, heads, d) of pages of bytes."""
+    pages = np.asarray(pages)
+    codes, shift, scales = _q4_places(page, heads, d)
+    out = []
+    for at, sat in zip(codes, scales):
+        code = pages[:, at].astype(np.int64) >> shift & 15
+        out.append(q4_values(np.where(code > 7, code - 16, code), pages[:, sat].astype(np.int64)))
+    return out

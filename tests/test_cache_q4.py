@@ -1,0 +1,133 @@
+"""The cache of 4-bit codes without a GPU: the sizes and refusals of its entry
+points, and the 64-bit form of what is held."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from hstu_jagged_attention_gb300 import binding, build
+from oracle import layer
+
+OK, BAD = binding.HSTU_OK, binding.HSTU_ERR_INVALID_ARG
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+@pytest.mark.parametrize("page,heads,d", [(16, 1, 32), (64, 4, 64), (128, 3, 128), (4096, 2, 64)])
+def test_page_bytes(page, heads, d):
+    assert binding.hstu_cache_q4_page_bytes(page, heads, d) == page * heads * (d // 2 + d // 16) * 2
+
+
+def test_refusals_on_the_host():
+    L, h, n = binding.lib(), ctypes.c_void_p(), ctypes.c_size_t()
+    for args, code in (((24, 1, 64), BAD), ((8, 1, 64), BAD), ((8192, 1, 64), BAD), ((16, 0, 64), BAD),
+                       ((16, 65537, 64), BAD), ((16, 1, 96), binding.HSTU_ERR_UNSUPPORTED)):
+        assert L.hstu_cache_q4_page_bytes(*args, ctypes.byref(n)) == code, args
+    assert L.hstu_cache_q4_page_bytes(16, 1, 64, None) == BAD
+    make = lambda **kw: L.hstu_cache_create_q4(*[kw.get(n, v) for n, v in dict(
+        pages=16, num_pages=4, page_size=16, heads=2, d=64, stride=0).items()], ctypes.byref(h))
+    packed = 16 * 2 * 72
+    assert make(d=96) == binding.HSTU_ERR_UNSUPPORTED
+    for kw in (dict(pages=0), dict(pages=8), dict(num_pages=0), dict(page_size=24), dict(page_size=8),
+               dict(page_size=8192), dict(heads=0), dict(stride=packed - 16), dict(stride=packed + 8),
+               dict(stride=-packed), dict(stride=1 << 40)):
+        assert make(**kw) == BAD and not h, kw
+    assert L.hstu_cache_create_q4(16, 4, 16, 2, 64, 0, None) == BAD
+    assert L.hstu_cache_read(None, None, None, 0, None, 0, None) == BAD
+    for kw in (dict(page_size=24), dict(d=40), dict(heads=0)):
+        with pytest.raises(binding.HstuError):
+            binding.hstu_cache_q4_page_bytes(**{**dict(page_size=16, heads=1, d=64), **kw})
+
+
+def test_a_cache_of_another_device_is_refused(monkeypatch):
+    torch = pytest.importorskip("torch")
+
+    class Pool:  # what the binding asks of a tensor on the second GPU
+        shape, is_cuda, ndim, dtype = torch.Size((4, 16 * 2 * 72)), True, 2, torch.uint8
+        device = torch.device("cuda:1")
+        stride = staticmethod(lambda: (16 * 2 * 72, 1))
+        data_ptr = staticmethod(lambda: 1 << 20)
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    with pytest.raises(ValueError, match="current device"):
+        binding.hstu_cache_create_q4(Pool, 16, 2, 64)
+    with pytest.raises(ValueError):
+        binding.hstu_cache_create_q4(torch.zeros(4, 16 * 2 * 72, dtype=torch.uint8), 16, 2, 64)
+
+
+# ------------------------------------------------- the 64-bit form itself
+def bf16(x):
+    torch = pytest.importorskip("torch")
+    return torch.from_numpy(np.asarray(x, dtype=np.float32)).bfloat16().double().numpy()
+
+
+def test_the_scales():
+    s = layer.SCALES
+    assert s[0] == 2.0 ** -20 and s[255] == 3840.0 and np.all(np.diff(s) > 0)
+    assert np.allclose(s[8:] / s[:-8], 2.0, rtol=0, atol=0)
+    # whatever is held is a bf16 number
+    held = (np.arange(-7, 8)[:, None] * s).reshape(-1)
+    assert np.array_equal(bf16(held), held)
+    # and so is every tie, and every bound on a group's largest value
+    ties = ((np.arange(7) + 0.5)[:, None] * s).reshape(-1)
+    assert np.array_equal(bf16(ties), ties) and np.array_equal(bf16(7 * s), 7 * s)
+
+
+def test_what_is_held_is_near():
+    rng = np.random.default_rng(0)
+    x = bf16(rng.standard_normal((4000, 64)) * np.exp(3 * rng.standard_normal((4000, 1))))
+    code, j = layer.q4_codes(x)
+    held, s, most = layer.q4_held(x), layer.SCALES[j], np.abs(x.reshape(4000, 4, 16)).max(axis=-1)
+    fits = most <= 7 * 3840.0
+    assert np.all(np.abs(code) <= 7) and np.all((7 * s >= most)[fits]) and np.all(j[~fits] == 255)
+    assert np.all((7 * layer.SCALES[j - 1] < most)[j > 0])
+    near = np.abs(held - x).reshape(4000, 4, 16).max(axis=-1) <= s / 2
+    assert np.all(near[fits]) and not np.any(near[most > 7.5 * 3840.0])
+    assert np.array_equal(layer.q4_held(-x), -held)
+    four = (j > 0) & (j < 240)  # the scale times 4 is a scale
+    by_group = lambda a: a.reshape(4000, 4, 16)[four]
+    assert np.array_equal(by_group(layer.q4_held(x * 4)), by_group(held * 4))
+
+
+@pytest.mark.parametrize("x,held", [
+    ([0.0] * 16, [0.0] * 16),
+    ([7.0, 0.5, -0.5, 1.5, -2.5, 0.498046875, 6.5, 3.0] + [0.0] * 8,  # s = 1: ties go away from zero
+     [7.0, 1.0, -1.0, 2.0, -3.0, 0.0, 7.0, 3.0] + [0.0] * 8),
+    ([7.03125] + [0.0] * 15, [6 * 1.125] + [0.0] * 15),  # past 7: the next scale is 9 / 8
+    ([np.nan, 7.0] + [2.0] * 14, [0.0, 7.0] + [2.0] * 14),
+    ([np.inf, -np.inf, 7.0] + [26000.0] * 13, [26880.0, -26880.0, 0.0] + [26880.0] * 13),
+    ([1e30, -26880.0, 1920.0, 1900.0] + [0.0] * 12, [26880.0, -26880.0, 3840.0, 0.0] + [0.0] * 12),
+    ([2.0 ** -21, -2.0 ** -22, 2.0 ** -20] + [0.0] * 13, [2.0 ** -20, 0.0, 2.0 ** -20] + [0.0] * 13),
+])
+def test_values_worked_by_hand(x, held):
+    assert layer.q4_held(np.array(x)).tolist() == held
+
+
+@pytest.mark.parametrize("page,heads,d", [(16, 2, 32), (256, 1, 64), (128, 3, 128)])
+def test_pages_hold_what_was_packed(page, heads, d):
+    rng = np.random.default_rng(1)
+    k, v = rng.standard_normal((2, 3, page, heads, d))
+    pages = layer.q4_pack(k, v)
+    assert pages.shape == (3, binding.hstu_cache_q4_page_bytes(page, heads, d))
+    ku, vu = layer.q4_unpack(pages, page, heads, d)
+    assert np.array_equal(ku, layer.q4_held(k)) and np.array_equal(vu, layer.q4_held(v))
+    # by hand: token 5, last head, channels 8 .. 15 are the second word of its codes
+    t = min(page, 128)
+    tile = (heads - 1) * (page // t) * t * d * 9 // 8
+    word = int.from_bytes(pages[1, tile + 5 * d // 2 + 4:tile + 5 * d // 2 + 8].tobytes(), "little")
+    s = layer.SCALES[pages[1, tile + t * d + 5 * d // 16]]
+    for c in range(8):
+        q = word >> (16 * (c % 2) + 4 * (c // 2)) & 15
+        assert ku[1, 5, heads - 1, 8 + c] == ((q ^ 8) - 8) * s
+
+
+def test_zeroed_pages_hold_zeros_and_any_bytes_are_finite():
+    assert not np.any(layer.q4_unpack(np.zeros((1, 16 * 72), np.uint8), 16, 1, 64))
+    ends = np.full((1, 16 * 72), 255, np.uint8)
+    k, v = layer.q4_unpack(ends, 16, 1, 64)
+    assert np.all(k == -3840.0) and np.all(np.isfinite(v))
+
+
