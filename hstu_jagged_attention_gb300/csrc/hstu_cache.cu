@@ -1004,7 +1004,7 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   w.tiles = p.max_q > 0 ? (p.max_q - 1) / w.tile_rows + 1 : 1;  // a bound of 0: only the lengths are checked
   w.kb_shift = hstu::kStepShift;  // both kernels' blocks have 128 keys
   w.extra = item_units(d);
-  const bool tiled = !cache->q4.pages && use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra));
+  const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra));
   if (tiled) {
     w.tile_rows = HSTU_BLOCK_M;
     w.tiles = (p.max_q - 1) / w.tile_rows + 1;
@@ -1047,7 +1047,8 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
     a.timeout_ns = hstu::host_wait_timeout_ns();
     a.debug_flags = hstu::host_debug_flags();
     const int grid = (int)std::min<long long>(cache->sms, most);
-    e = hstu::launch_fwd_paged(d, tq, cache->tk, cache->tv, a, grid, s);
+    e = cache->q4.pages ? hstu::launch_fwd_paged_q4(d, tq, cache->q4, a, grid, s)
+                        : hstu::launch_fwd_paged(d, tq, cache->tk, cache->tv, a, grid, s);
   } else {
     hstu::StepArgs a{};
     a.p = p;

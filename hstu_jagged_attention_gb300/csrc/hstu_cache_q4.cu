@@ -248,13 +248,6 @@ constexpr int kQ4BytesMost =
     Q4Cfg<D>::STAGES * Q4Cfg<D>::STAGEB + q4_red_bytes(Q4Cfg<D>::WARPS, kStepRows, D) + kQ4TailBytes + 128;
 static_assert(sizeof(StepMisc<8>) <= 64 + 16 * 8, "misc");
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 template <int D>
 __device__ void q4_produce(const StepArgs& a, const Q4Pool& pool, const PagedWork& w, PagedCursor c, PagedSeg g,
                            uint32_t base, uint32_t full, uint32_t empty, const StepWait& wt) {

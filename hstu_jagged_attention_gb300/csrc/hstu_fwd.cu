@@ -64,6 +64,7 @@
 #include "hstu_internal.h"
 #include "hstu_paged.cuh"
 #include "hstu_ptx.cuh"
+#include "hstu_q4.cuh"
 
 namespace hstu {
 
@@ -1355,12 +1356,12 @@ cudaError_t launch_fwd_pairs(int d, const CUtensorMap& tq, const CUtensorMap& tk
 
 cudaError_t launch_fwd_paged(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PagedFwdArgs& a, int grid, cudaStream_t stream) {
-  switch (d) {
-    case 32: return launch_paged_d<32>(tq, tk, tv, a, grid, stream);
-    case 64: return launch_paged_d<64>(tq, tk, tv, a, grid, stream);
-    case 128: return launch_paged_d<128>(tq, tk, tv, a, grid, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  return launch_paged(d, tq, PagedMaps{tk, tv}, a, grid, stream);
+}
+
+cudaError_t launch_fwd_paged_q4(int d, const CUtensorMap& tq, const Q4Pool& pool, const PagedFwdArgs& a,
+                                int grid, cudaStream_t stream) {
+  return launch_paged(d, tq, pool, a, grid, stream);
 }
 
 int fwd_smem_bytes(int d) {

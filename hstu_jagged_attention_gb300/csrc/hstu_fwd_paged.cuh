@@ -25,9 +25,21 @@
 // waited for the step's barrier finds it.  When the word of step c is
 // written, QK(c - 3) and so PV(c - 6) are done: 8 step words are enough.  An
 // item is at most 6 steps ahead of the PV issuer, and that at most two items
-// ahead of the epilogue: 16 item words are enough.
-constexpr int kStepWords = 8, kItemWords = 16;
+// ahead of the epilogue: 16 item words are enough.  (The 4-bit form's words are
+// written when the codes' copy is, up to four steps ahead of that, hence 16
+// step words.)
+constexpr int kStepWords = 16, kItemWords = 16;
 constexpr int kPagedThreads = 768;  // four SiLU warpgroups, the wide P layout, at every d
+// What the keys and values come from: the bf16 pools' tensor maps, or the pages
+// of 4-bit codes, which two warps each turn into the bf16 tiles.
+struct PagedMaps {
+  CUtensorMap k, v;
+};
+constexpr int kUnpackWarp0 = kPagedThreads / 32, kUnpackWarps = 2;  // the keys', then the values'
+template <class SRC>
+constexpr bool kHeldInQ4 = std::is_same<SRC, Q4Pool>::value;
+template <class SRC>
+constexpr int kPagedThreadsOf = kPagedThreads + (kHeldInQ4<SRC> ? 2 * 32 * kUnpackWarps : 0);
 struct PagedStep {
   int lim;    // position of the tile's first row, less the block's first key
   int hist;   // history end, less the block's first key
@@ -68,6 +80,14 @@ __device__ __forceinline__ PagedStep read_step(const PagedWords* words, uint32_t
                : "r"(smem_u32(words->step + tc % kStepWords))
                : "memory");
   return s;
+}
+
+// As Cfg's, where the unpacking warps arrive for their part of a tile.
+template <int D, bool Q4>
+__device__ constexpr uint32_t paged_arrivals(int i) {
+  using C = Cfg<D>;
+  const bool k = i >= C::B_QKREADY && i < C::B_QKREADY + C::P, v = i >= C::B_VFULL && i < C::B_VFULL + C::P;
+  return C::arrivals(i, true) + (Q4 && (k || v) ? kUnpackWarps - 1u : 0u);
 }
 
 // One warp: the K stream with each item's Q tile, or the V stream.
@@ -148,8 +168,220 @@ __device__ void paged_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, c
   __syncwarp();
 }
 
-// QK issuer: as role_mma_qk.
+// Shared memory of the 4-bit form.  At d = 128 the tiles fill it, so the keys
+// get two slots instead of three: key slot t mod KP is free once QK(t - KP) has
+// completed.  In that third slot's place (at d <= 64 behind the barriers) are
+// the rings of codes on their way: a stage holds the codes of 128 keys, or
+// values, d / 2 bytes a row, and then their scales, d / 16 bytes a row.
+template <int D, bool Q4>
+struct PagedCfg {
+  using C = Cfg<D>;
+  static constexpr int KP = Q4 && D == 128 ? 2 : C::P;
+  static constexpr int KSTAGES = D == 128 ? 2 : 4, VSTAGES = D == 128 ? 1 : 4;
+  static constexpr int RAWB = kBN * (D / 2 + D / kQ4Group);
+  static constexpr int RAW_OFF = D == 128 ? C::K_OFF + KP * C::TILEB : (C::MISC_OFF + 16 + 127) / 128 * 128;
+  static constexpr int RAW_BARS = RAW_OFF + (KSTAGES + VSTAGES) * RAWB;  // full, then empty
+  static constexpr int RAW_END = RAW_BARS + 16 * (KSTAGES + VSTAGES);
+  static constexpr int SMEM = !Q4 || D == 128 || RAW_END + 1024 <= C::SMEM_LAUNCH ? C::SMEM_LAUNCH : RAW_END + 1024;
+  static_assert(!Q4 || D != 128 || RAW_END <= C::V_OFF, "the codes on their way");
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+// The ring of the keys' (which = 0) or the values' codes: stage s, its full and
+// its empty barrier.
 template <int D>
+struct RawRing {
+  using U = PagedCfg<D, true>;
+  uint32_t base;
+  int which;
+  __device__ __forceinline__ int stages() const { return which ? U::VSTAGES : U::KSTAGES; }
+  __device__ __forceinline__ uint32_t stage(int s) const {
+    return base + U::RAW_OFF + (uint32_t)((which ? U::KSTAGES : 0) + s) * U::RAWB;
+  }
+  __device__ __forceinline__ uint32_t full(int s) const {
+    return base + U::RAW_BARS + 8u * (uint32_t)((which ? U::KSTAGES : 0) + s);
+  }
+  __device__ __forceinline__ uint32_t empty(int s) const { return full(s) + 8u * (U::KSTAGES + U::VSTAGES); }
+};
+
+// The copies of a cache of 4-bit codes, one warp for the keys (which = 0, with
+// the words of every step and item) and one for the values: as paged_producer,
+// two bulk copies a page into the ring of codes.
+template <int D>
+__device__ void paged_copy_codes(const Q4Pool& pool, const PagedFwdArgs& a, const PagedWork& w, PagedCursor cur,
+                                 PagedSeg g, PagedWords* words, uint32_t base, const WaitCtx& wt, int which) {
+  using U = PagedCfg<D, true>;
+  using T = Q4Tile<D>;
+  const RawRing<D> ring{base, which};
+  const int lane = threadIdx.x & 31;
+  const int shift = a.p.page_shift, ps = 1 << shift, ts = pool.tile_shift;
+  uint32_t c = 0, qc = 0, round = 0;
+  int st = 0;
+  bool ok = true;
+  while (ok && cur.next(a.p, w, &g)) {
+    if (which == 0 && lane == 0)
+      words->item[qc % kItemWords] = PagedItem{g.seq.q0 + kBM * g.qt, g.h, g.walk.rows, g.n, g.c0, g.parts};
+    ++qc;
+    const int32_t* row = a.p.page_table + (long long)g.b * a.p.max_pages;
+    const int end = g.walk.end();
+    const int pages = (end + ps - 1) >> shift;
+    PageIds ids;
+    for (int i = 0; i < g.n; ++i) {
+      const int tok0 = kBN * g.walk.block(g.i0 + i);
+      const int p0 = tok0 >> shift;
+      const int valid = end - tok0 < kBN ? end - tok0 : kBN;
+      const int npg = ps >= kBN ? 1 : (valid + ps - 1) >> shift;  // at most 8
+      ids.cover(row, p0, npg, pages);
+      // lanes 0 .. npg - 1 copy codes, lanes 16 .. 16 + npg - 1 scales
+      const int pg = lane & 15, part = lane >> 4;
+      const int page = ids.get(p0 + pg);
+      if (lane == 0)
+        ok = wait_one(ring.empty(st), (round & 1u) ^ 1u, wt, which ? kSiteVEmpty : kSiteKEmpty) && !*wt.abort_flag;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      const bool mine = pg < npg, good = page >= 0 && page < a.p.num_pages;
+      const unsigned bad = __ballot_sync(0xffffffffu, mine && !good);
+      const int bytes = (part ? T::SCALEB : T::CODEB) << ts;
+      const uint32_t dst = ring.stage(st) + (part ? kBN * T::CODEB : 0) + pg * bytes;
+      if (bad) {
+        if (mine && !good) {
+          // read as zeros: silu(0) V = 0
+          atomicOr(&g_dev_words[0], kStatusBadPaged);
+          for (int x = 0; x < bytes; x += 16) st_shared16(dst + x, make_uint4(0u, 0u, 0u, 0u));
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+      }
+      if (lane == 0) {
+        if (which == 0)
+          words->step[c % kStepWords] = make_int4(g.walk.p0 - tok0, g.seq.hist - tok0, g.walk.rows,
+                                                  (i == 0 ? 1 : 0) | (i == g.n - 1 ? 2 : 0));
+        mbar_arrive_expect_tx(ring.full(st),
+                              (uint32_t)((npg - __popc(bad & 0xffffu)) * ((T::CODEB + T::SCALEB) << ts)));
+      }
+      __syncwarp();
+      if (mine && good) {
+        const uint8_t* tile = pool.pages + page * pool.page_stride +
+                              ((long long)g.h * pool.tiles + ((tok0 & (ps - 1)) >> ts)) * pool.tile_bytes;
+        bulk_load(dst, tile + (part ? T::scales(ts, which, 0) : T::codes(ts, which, 0)), (uint32_t)bytes,
+                  ring.full(st));
+      }
+      ++c;
+      if (++st == ring.stages()) {
+        st = 0;
+        ++round;
+      }
+    }
+  }
+  // every copy lands before the CTA ends
+  if (lane == 0) drain_copies(ring.full(0), ring.stages(), c);
+  __syncwarp();
+}
+
+// The keys' (which = 0, with each item's Q tile) or the values' tiles from the
+// codes, by kUnpackWarps warps, this one the `part`-th.  A lane takes 32
+// channels of a key at a time, 16 bytes of codes and two scales, and stores them
+// as bf16 where the bulk-tensor copy of a bf16 pool would put them: 8 lanes'
+// 16-byte stores meet all banks.  Rows behind the last key hold what some codes
+// stand for, finite numbers that P's zeros meet.
+template <int D>
+__device__ void paged_unpack(const CUtensorMap* tm_q, uint32_t steps, const PagedWords* words, uint32_t base,
+                             const WaitCtx& wt, int which, int part) {
+  using C = Cfg<D>;
+  using U = PagedCfg<D, true>;
+  using T = Q4Tile<D>;
+  constexpr int LANES = D < 64 ? 1 : 2;   // that share a row of a chunk of channels
+  constexpr int ROWS = 32 / LANES;        // a warp's rows of a load
+  constexpr int STEP = ROWS * kUnpackWarps;
+  constexpr int GROUPS = kBN / STEP;      // 4, at d = 32 2
+  const RawRing<D> ring{base, which};
+  const uint32_t bars = base + C::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  const int lane = threadIdx.x & 31;
+  const int row0 = part * ROWS + lane / LANES;  // and every STEP rows after it
+  const int sub = lane % LANES;                 // which 32 channels of the chunk
+  // the rows' swizzle is the same for all of a lane's rows
+  const int turn = C::ROWB == 128 ? (row0 & 7) : ((row0 >> 1) & 3);
+  const uint32_t dst = base + (which ? C::V_OFF : C::K_OFF) + row0 * C::ROWB + (((4 * sub) ^ turn) << 4);
+  const uint32_t src = row0 * T::CODEB + 16 * sub;
+  const uint32_t src_sc = kBN * T::CODEB + row0 * T::SCALEB + 2 * sub;
+  const int slots = which ? C::P : U::KP;
+  uint32_t qc = 0, round = 0, raw_round = 0;
+  int slot = 0, raw = 0, j = 0;  // the tile's slot, the codes' stage, c mod P
+  for (uint32_t c = 0; c < steps; ++c) {
+    bool ok = wait_one(ring.full(raw), raw_round & 1u, wt, which ? kSiteVFull : kSiteKFull);
+    if (lane == 0 && ok) {
+      if (which == 0) {
+        if (part == 0 && read_step(words, c).first()) {
+          const int qs = (int)(qc % C::QS);
+          ok = wait_one(bar(C::B_QEMPTY + qs), ((qc / C::QS) & 1u) ^ 1u, wt, kSiteQEmpty);
+          if (ok) {
+            const volatile PagedItem& x = words->item[qc % kItemWords];
+            const int h = x.h, row = x.row0;
+            mbar_arrive_expect_tx(bar(C::B_QFULL + qs), C::TILEB);
+#pragma unroll
+            for (int ch = 0; ch < C::NCHUNK; ++ch)
+              tma_load_3d(base + C::Q_OFF + qs * C::TILEB + ch * C::CHUNKB, tm_q, bar(C::B_QFULL + qs),
+                          ch * C::CHUNK, h, row);
+            ++qc;
+          }
+        }
+        // QK(c - KP) done: its S buffer is written
+        if (ok && round > 0)
+          ok = wait_one(bar(C::B_SFULL + (int)((c - U::KP) % C::P)), ((c - U::KP) / C::P) & 1u, wt, kSiteKEmpty);
+      } else {
+        ok = wait_one(bar(C::B_QKREADY + j), (c / C::P) & 1u, wt, kSiteVEmpty);
+      }
+    }
+    if (!__all_sync(0xffffffffu, ok)) break;
+    const uint32_t from = ring.stage(raw), to = dst + slot * C::TILEB;
+#pragma unroll 1
+    for (int ch = 0; ch < C::NCHUNK; ++ch) {
+      uint4 u[GROUPS];
+      uint32_t sc[GROUPS];
+#pragma unroll
+      for (int x = 0; x < GROUPS; ++x) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u[x].x), "=r"(u[x].y), "=r"(u[x].z), "=r"(u[x].w)
+                     : "r"(from + src + x * STEP * T::CODEB + 32 * ch)
+                     : "memory");
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=r"(sc[x])
+                     : "r"(from + src_sc + x * STEP * T::SCALEB + 4 * ch)
+                     : "memory");
+      }
+#pragma unroll
+      for (int x = 0; x < GROUPS; ++x) {
+        const Q4Scale s0 = q4_scale(sc[x] & 255u, sc[x] & 255u), s1 = q4_scale(sc[x] >> 8, sc[x] >> 8);
+        const uint32_t st = to + x * STEP * C::ROWB + ch * C::CHUNKB;
+        st_shared16(st, q4_word(u[x].x, s0));
+        st_shared16(st ^ 16u, q4_word(u[x].y, s0));
+        st_shared16(st ^ 32u, q4_word(u[x].z, s1));
+        st_shared16(st ^ 48u, q4_word(u[x].w, s1));
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(ring.empty(raw));
+      mbar_arrive(bar((which ? C::B_VFULL : C::B_QKREADY) + j));
+    }
+    if (++j == C::P) j = 0;
+    if (++slot == slots) {
+      slot = 0;
+      ++round;
+    }
+    if (++raw == ring.stages()) {
+      raw = 0;
+      ++raw_round;
+    }
+  }
+  // every copy lands before the CTA ends
+  if (which == 0 && lane == 0) drain_copies(bar(C::B_QFULL), C::QS, qc);
+  __syncwarp();
+}
+
+// QK issuer: as role_mma_qk.
+template <int D, bool Q4>
 __device__ void paged_mma_qk(const PagedFwdArgs& a, uint32_t steps, const PagedWords* words,
                              uint32_t base, uint32_t tmem, const WaitCtx& wt) {
   using C = Cfg<D>;
@@ -166,7 +398,9 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, uint32_t steps, const PagedW
   if (!ok) steps = 0;
   uint32_t tc = 0, it = 0;
   uint32_t ph = 0;
+  constexpr int KP = PagedCfg<D, Q4>::KP;
   for (int J = 0; tc < steps; J = J + 1 == P ? 0 : J + 1) {
+    const int kslot = KP == P ? J : (int)(tc % KP);
     const int qs = C::QS == 1 ? 0 : (int)(it & 1u);
     if (!(ok = wait_one(bar(C::B_QKREADY + J), ph, wt, kSiteKFull))) break;
     const PagedStep st = read_step(words, tc);
@@ -181,7 +415,7 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, uint32_t steps, const PagedW
     for (int kk = 0; kk < QK_STEPS; ++kk) {
       const uint32_t off = (kk / STEPS_PER_CHUNK) * C::CHUNKB + (kk % STEPS_PER_CHUNK) * 32;
       qd[kk] = pin64(qd0 + (uint64_t)(off >> 4));
-      kd[kk] = pin64(k_desc0 + (uint64_t)((J * C::TILEB + off) >> 4));
+      kd[kk] = pin64(k_desc0 + (uint64_t)((kslot * C::TILEB + off) >> 4));
     }
     mma_ss_c<0>(s_tmem, qd[0], kd[0], idesc);
 #pragma unroll
@@ -202,7 +436,8 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, uint32_t steps, const PagedW
 
 // PV issuer: as role_mma_pv, with the block that holds the tile's last keys
 // cut at the first key that no row sees.
-template <int D>
+// Q4: the values come from codes, and rows behind the last key are zeros.
+template <int D, bool Q4>
 __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t base, uint32_t tmem,
                              const WaitCtx& wt) {
   using C = Cfg<D>;
@@ -260,7 +495,7 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
         !(ok = wait_one(bar(C::B_OEMPTY + ob), ((it / C::OB) & 1u) ^ 1u, wt, kSiteOEmpty)))
       break;
     if (!v_ready && !(ok = wait_one(bar(C::B_VFULL + J), ph, wt, kSiteVFull))) break;
-    if (st.end() < cols) {
+    if (!Q4 && st.end() < cols) {
       // keys that no row sees: their P is zero, their V may be anything
       const uint32_t v_addr = base + C::V_OFF + J * C::TILEB;
 #pragma unroll
@@ -288,7 +523,7 @@ __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t b
   }
   mma_commit(bar(C::B_DRAIN + 1));
   wait_drain(bar(C::B_DRAIN + 1), 0);
-  if (!ok) arrive_for_dropped_pv<P>(bar(C::B_QKREADY), tc);
+  if (!Q4 && !ok) arrive_for_dropped_pv<P>(bar(C::B_QKREADY), tc);
 }
 
 // SiLU warpgroups: as role_silu's wide form.  A masked block keeps key k for
@@ -483,12 +718,13 @@ __device__ void paged_join(const PagedFwdArgs& a, PagedWords* words, bool dead) 
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kPagedThreads, 1)
-    hstu_fwd_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const PagedFwdArgs a) {
+template <int D, class SRC>
+__global__ void __launch_bounds__(kPagedThreadsOf<SRC>, 1)
+    hstu_fwd_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ SRC src,
+                          const PagedFwdArgs a) {
   using C = Cfg<D>;
-  constexpr int WARPS = kPagedThreads / 32;
+  constexpr bool Q4 = kHeldInQ4<SRC>;
+  constexpr int WARPS = kPagedThreadsOf<SRC> / 32;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PagedStart<WARPS> start;
   __shared__ PagedWords words;
@@ -500,8 +736,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bars = base + C::BAR_OFF;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NBARS; ++i) mbar_init(bars + 8u * i, C::arrivals(i, true));
+    for (int i = 0; i < C::NBARS; ++i) mbar_init(bars + 8u * i, paged_arrivals<D, Q4>(i));
     for (int j = 0; j < C::P; ++j) mbar_arrive(bars + 8u * (C::B_QKREADY + j));
+    if constexpr (Q4) {
+      for (int which = 0; which < 2; ++which) {
+        const RawRing<D> ring{base, which};
+        for (int s = 0; s < ring.stages(); ++s) {
+          mbar_init(ring.full(s), 1);
+          mbar_init(ring.empty(s), kUnpackWarps);
+        }
+      }
+    }
     *abort_flag = 0;
     words.cut[0].parts = words.cut[1].parts = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -527,15 +772,23 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wt{a.timeout_ns, abort_flag};
   const uint32_t steps = (uint32_t)n_steps;
-  if (warp == kTmaWarpK) {
-    paged_producer<D, true>(&tm_k, &tm_q, a, w, from, first, &words, base, wt);
-  } else if (warp == kTmaWarpV) {
-    paged_producer<D, false>(&tm_v, &tm_q, a, w, from, first, &words, base, wt);
+  if (warp == kTmaWarpK || warp == kTmaWarpV) {
+    if constexpr (Q4)
+      paged_copy_codes<D>(src, a, w, from, first, &words, base, wt, warp == kTmaWarpV);
+    else if (warp == kTmaWarpK)
+      paged_producer<D, true>(&src.k, &tm_q, a, w, from, first, &words, base, wt);
+    else
+      paged_producer<D, false>(&src.v, &tm_q, a, w, from, first, &words, base, wt);
+  } else if (Q4 && warp >= kUnpackWarp0) {
+    if constexpr (Q4) {
+      const int i = warp - kUnpackWarp0;
+      paged_unpack<D>(&tm_q, steps, &words, base, wt, i / kUnpackWarps, i % kUnpackWarps);
+    }
   } else if (warp == kMmaWarpQK) {
-    if (lane == 0) paged_mma_qk<D>(a, steps, &words, base, tmem, wt);
+    if (lane == 0) paged_mma_qk<D, Q4>(a, steps, &words, base, tmem, wt);
     __syncwarp();
   } else if (warp == kMmaWarpPV) {
-    if (lane == 0) paged_mma_pv<D>(steps, &words, base, tmem, wt);
+    if (lane == 0) paged_mma_pv<D, Q4>(steps, &words, base, tmem, wt);
     __syncwarp();
   } else if (warp >= kEwWarp0) {
     paged_silu<D>(a, steps, &words, base, tmem, wt, warp, lane);
@@ -553,16 +806,26 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   paged_join<D>(a, &words, *abort_flag != 0);
 }
 
-template <int D>
-cudaError_t launch_paged_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                           const PagedFwdArgs& a, int grid, cudaStream_t stream) {
-  using C = Cfg<D>;
+template <int D, class SRC>
+cudaError_t launch_paged_d(const CUtensorMap& tq, const SRC& src, const PagedFwdArgs& a, int grid,
+                           cudaStream_t stream) {
+  constexpr int SMEM = PagedCfg<D, kHeldInQ4<SRC>>::SMEM;
   static DeviceOnce once;
   const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(hstu_fwd_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                C::SMEM_LAUNCH);
+    return cudaFuncSetAttribute(hstu_fwd_paged_kernel<D, SRC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                SMEM);
   });
   if (e != cudaSuccess) return e;
-  return launch_after(hstu_fwd_paged_kernel<D>, grid, kPagedThreads, C::SMEM_LAUNCH, stream, tq, tk,
-                      tv, a);
+  return launch_after(hstu_fwd_paged_kernel<D, SRC>, grid, kPagedThreadsOf<SRC>, SMEM, stream, tq,
+                      src, a);
+}
+template <class SRC>
+cudaError_t launch_paged(int d, const CUtensorMap& tq, const SRC& src, const PagedFwdArgs& a, int grid,
+                         cudaStream_t stream) {
+  switch (d) {
+    case 32: return launch_paged_d<32>(tq, src, a, grid, stream);
+    case 64: return launch_paged_d<64>(tq, src, a, grid, stream);
+    case 128: return launch_paged_d<128>(tq, src, a, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }

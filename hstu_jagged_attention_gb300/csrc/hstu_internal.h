@@ -257,6 +257,9 @@ cudaError_t launch_read_q4(const Q4Pool& pool, const ReadArgs& a, cudaStream_t s
 // `most`: CTAs with work, at most; clusters: a cluster of CTAs an item instead.
 cudaError_t launch_step_q4(int d, const Q4Pool& pool, long long most, bool clusters, const StepArgs& a,
                            int sms, cudaStream_t stream);
+// The attention on 128-row tiles over such a cache; tq as launch_fwd_paged.
+cudaError_t launch_fwd_paged_q4(int d, const CUtensorMap& tq, const Q4Pool& pool, const PagedFwdArgs& a,
+                                int grid, cudaStream_t stream);
 // Clusters of the few-token kernel that run at once.
 cudaError_t step_clusters_q4(int d, int* n);
 
