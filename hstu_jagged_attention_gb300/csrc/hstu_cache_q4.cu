@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kQ4Threads) read_q4_kernel(const ReadArgs a, c
     kj = tile[T::scales(pool.tile_shift, 0, r) + u.g];
     vj = tile[T::scales(pool.tile_shift, 1, r) + u.g];
   }
-  const Q4Scale ks = q4_scale(kj, kj), vs = q4_scale(vj, vj);
+  const Q4Scale ks = q4_scale(kj), vs = q4_scale(vj);
   const long long at = (long long)u.h * D + kQ4Group * u.g;
   uint4* ko = reinterpret_cast<uint4*>(a.k + t * a.k_stride + at);
   uint4* vo = reinterpret_cast<uint4*>(a.v + t * a.v_stride + at);
@@ -210,30 +210,34 @@ __global__ void __launch_bounds__(kQ4Threads) read_q4_kernel(const ReadArgs a, c
 // As the bf16 cache's kernel of 16-row tiles (hstu_cache.cu): the last warp
 // copies blocks of 128 keys with their values into a ring of shared-memory
 // stages, one bulk copy a page, and the others take a part of the keys each.
-// The codes become the products' B operands in registers:
-//   S = Q K^T: a lane's operand of key n is channels 2 t .. and 2 t + 8 .. of
+// The codes become the products' A operands (16 keys, or 16 channels) in
+// registers, and the few new tokens are their 8 columns, so that no product's
+// rows are padding:
+//   S^T = K Q^T: a lane's operand of key m is channels 2 t .. and 2 t + 8 .. of
 //     every 16; a sum over channels may take them in any order, so lane t has
 //     the D / 4 consecutive channels whose codes it loads with one access, and
 //     Q's operand the same ones;
-//   O += P V: lane n's operand is channel n of keys 2 t, 2 t + 1, 2 t + 8 and
-//     2 t + 9.  It loads D / 8 consecutive channels of its four keys, and one
-//     byte permutation of two keys' words puts the keys side by side.  Which
-//     channel a column of O is, and which key a column of S, is free, as long
-//     as P's columns are V's rows: key 8 a + 4 e + (t + 2 e) % 4 for column
-//     2 t + e of S's 8-key tile a lets neither load meet a bank twice (at d =
-//     128, (t + e) % 4: K's do not, V's meet two).
-// p is split into two bf16 terms; with up to 8 rows in a tile both terms are
-// one operand, the second in its rows 8 .. 15.
+//   O^T += V^T P^T: lane n's operand is channels n and n + 8 of keys 2 t, 2 t +
+//     1, 2 t + 8 and 2 t + 9.  It loads D / 8 consecutive channels of its four
+//     keys, and one byte permutation of two keys' words puts the keys side by
+//     side.  Which channel a row of O^T is, and which key a row of S^T, is
+//     free, as long as P^T's rows are V^T's columns: key 8 a + 4 e + (t + 2 e)
+//     % 4 for row 8 a + 2 t + e lets neither load meet a bank twice (at d = 128,
+//     (t + e) % 4: K's do not, V's meet two);
+//   P^T's operand is S^T's result transposed: one movmatrix a 8 x 8 tile.
+// p is split into two bf16 terms.  With up to 4 tokens in a tile columns 4 .. 7
+// are the same tokens' and take the second terms: one product for both.
+// G: groups of 8 tokens a tile holds.
 // Keys past a row's last are masked by a select on p; whatever bytes lie
 // there, as codes they are finite, and so add nothing.
 template <int D>
 struct Q4Cfg {
-  static constexpr int WARPS = 8;
+  static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int KEYS = kStepKeys;
   static constexpr int KW = KEYS / WARPS;
   static constexpr int STAGEB = KEYS * q4_token_bytes(D);
-  static constexpr int PER_SM = D == 128 ? 1 : 2;
+  static constexpr int PER_SM = D == 128 ? 2 : 3;
   static constexpr int RING = 128 * 1024 / PER_SM;
   static constexpr int STAGES = RING / STAGEB < 15 ? RING / STAGEB : 15;
   static constexpr int MAX_STAGES = 16;
@@ -313,63 +317,82 @@ __device__ void q4_produce(const StepArgs& a, const Q4Pool& pool, const PagedWor
   __syncwarp();
 }
 
-__device__ __forceinline__ uint32_t lds8(uint32_t at) {
-  uint32_t x;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-  return x;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t at) {
-  uint32_t x;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-  return x;
-}
+// Plain loads and a product that is not volatile, so that the compiler may move
+// them within a block (not across its barriers, which clobber memory).
 template <int WORDS>
-__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[WORDS]) {
-  if constexpr (WORDS == 1)
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
-  else if constexpr (WORDS == 2)
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
-  else
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(at)
-                 : "memory");
+__device__ __forceinline__ void lds_words(const uint8_t* at, uint32_t (&w)[WORDS]) {
+  if constexpr (WORDS == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(at);
+  } else if constexpr (WORDS == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(at);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  }
+}
+__device__ __forceinline__ uint32_t lds16(const uint8_t* at) { return *reinterpret_cast<const uint16_t*>(at); }
+// d = A B, and c += A B
+__device__ __forceinline__ void q4_mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void q4_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The key, of 8, of column 2 t + e of a tile of S.
+// An 8 x 8 tile of 16-bit values, two of a row a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// The key, of 8, of row 2 t + e of a tile of S^T.
 template <int D>
 __device__ __forceinline__ int q4_key(int t, int e) {
   return 4 * e + ((t + (D == 128 ? e : 2 * e)) & 3);
 }
 
-template <int D, bool CLUSTER>
+template <int D, int G, bool CLUSTER>
 __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWork& w, PagedCursor c, PagedSeg g,
-                           uint32_t base, uint32_t full, uint32_t empty, float* red,
+                           const uint8_t* ring, uint32_t full, uint32_t empty, float* red,
                            StepMisc<Q4Cfg<D>::WARPS>* m, const StepWait& wt) {
   using C = Q4Cfg<D>;
   using T = Q4Tile<D>;
-  constexpr int KS = C::KW / 16;            // k16 steps of the P V product
-  constexpr int KWORDS = D / 32;            // words of a lane's channels of a key
+  constexpr int KS = C::KW / 16;                // 16-key steps of a block
+  constexpr int KWORDS = D / 32;                // words of a lane's channels of a key
   constexpr int VWORDS = D >= 64 ? D / 64 : 1;  // of a value: at d = 32 half a word
-  constexpr int NT = D / 8;                 // n tiles of O
+  constexpr int MT = D / 16;                    // tiles of O^T
   constexpr int RS = step_red_stride(D);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
-  // bytes of the lane's keys, values and scales in a stage, for each k16 step
-  uint32_t k_at[KS], v_at[KS], ks_at[KS], vs_at[KS];
-  int key0[KS];  // the step's first key
+  // the lane's keys, values and scales in a stage, for each 16-key step
+  const uint8_t *k_at[KS], *ks_at[KS], *v_at[KS][2], *vs_at[KS][2];
+  const int vk[2] = {q4_key<D>(t4, 0), q4_key<D>(t4, 1)};
+  const int kk = q4_key<D>(g8 >> 1, g8 & 1);
 #pragma unroll
   for (int y = 0; y < KS; ++y) {
-    key0[y] = C::KW * warp + 16 * y;
-    const int sub = key0[y] >> pool.tile_shift, r = key0[y] & ((1 << pool.tile_shift) - 1);
-    const uint32_t tile = base + sub * pool.tile_bytes;
-    const int kr = r + q4_key<D>(g8 >> 1, g8 & 1);
-    k_at[y] = tile + T::codes(pool.tile_shift, 0, kr) + t4 * (D / 8);
-    ks_at[y] = tile + T::scales(pool.tile_shift, 0, kr) + t4 * (D / 4) / kQ4Group;
-    v_at[y] = tile + T::codes(pool.tile_shift, 1, r) + g8 * (D / 16);
-    vs_at[y] = tile + T::scales(pool.tile_shift, 1, r) + g8 * (D / 8) / kQ4Group;
+    const int key0 = C::KW * warp + 16 * y;
+    const int sub = key0 >> pool.tile_shift, r = key0 & ((1 << pool.tile_shift) - 1);
+    const uint8_t* tile = ring + sub * pool.tile_bytes;
+    k_at[y] = tile + T::codes(pool.tile_shift, 0, r + kk) + t4 * (D / 8);
+    ks_at[y] = tile + T::scales(pool.tile_shift, 0, r + kk) + t4 * (D / 4) / kQ4Group;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      v_at[y][e] = tile + T::codes(pool.tile_shift, 1, r + vk[e]) + g8 * (D / 16);
+      vs_at[y][e] = tile + T::scales(pool.tile_shift, 1, r + vk[e]) + g8 * (D / 8) / kQ4Group;
+    }
   }
-  const int vk[2] = {q4_key<D>(t4, 0), q4_key<D>(t4, 1)};
   const float2 ha2 = make_float2(a.half_alpha, a.half_alpha);
   int st = 0;
   uint32_t ph = 0;
@@ -382,84 +405,89 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
     dead = !__all_sync(0xffffffffu, step_wait(full + 8u * C::MAX_STAGES - 8u, 0, wt, kSiteUnsignalledStep));
   while (c.next(a.p, w, &g)) {
     const int rows = g.walk.rows;
-    const bool few = rows <= 8;
-    uint32_t qf[D / 16][4];
-    {
-      const uint16_t* x0 =
-          a.q + (long long)(g.seq.q0 + kStepRows * g.qt + g8) * a.q_stride + (long long)g.h * D + t4 * (D / 4);
-      const uint16_t* x1 = x0 + 8 * a.q_stride;
+    const bool both = G == 1 && rows <= 4;  // columns 4 .. 7: the second terms of tokens 0 .. 3
+    uint32_t qf[G][MT][2];
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+      const int row = both ? (g8 & 3) : 8 * u + g8;
+      const uint16_t* x =
+          a.q + (long long)(g.seq.q0 + w.tile_rows * g.qt + row) * a.q_stride + (long long)g.h * D + t4 * (D / 4);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint4 u = g8 < rows ? load16(x0 + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-        const uint4 v = g8 + 8 < rows ? load16(x1 + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-        qf[2 * i][0] = u.x;
-        qf[2 * i][2] = u.y;
-        qf[2 * i + 1][0] = u.z;
-        qf[2 * i + 1][2] = u.w;
-        qf[2 * i][1] = v.x;
-        qf[2 * i][3] = v.y;
-        qf[2 * i + 1][1] = v.z;
-        qf[2 * i + 1][3] = v.w;
+        const uint4 v = row < rows ? load16(x + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        qf[u][2 * i][0] = v.x;
+        qf[u][2 * i][1] = v.y;
+        qf[u][2 * i + 1][0] = v.z;
+        qf[u][2 * i + 1][1] = v.w;
       }
     }
-    float o[NT][4];
+    float o[G][MT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int u = 0; u < G; ++u)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
+      for (int n = 0; n < MT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[u][n][j] = 0.f;
 
     for (int i = 0; i < g.n && !dead; ++i) {
       const int kb = g.walk.block(g.i0 + i) << kStepShift;
       if ((dead = !__all_sync(0xffffffffu, step_wait(full + 8u * st, ph, wt, kSiteStepFull)))) break;
       const uint32_t off = st * C::STAGEB;
-      float s[2 * KS][4];
-#pragma unroll
-      for (int n = 0; n < 2 * KS; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
+      float s[KS][G][4];
 #pragma unroll
       for (int y = 0; y < KS; ++y) {
+        uint32_t kw[2][KWORDS], j[2];  // keys kk and 8 + kk
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t kw[KWORDS];
-          lds_words<KWORDS>(off + k_at[y] + 8 * h * T::CODEB, kw);
-          const uint32_t sat = off + ks_at[y] + 8 * h * T::SCALEB;
-          const uint32_t j = D == 128 ? lds16(sat) : lds8(sat);
-          Q4Scale sc = q4_scale(j & 255u, j & 255u);
+          lds_words<KWORDS>(k_at[y] + off + 8 * h * T::CODEB, kw[h]);
+          const uint8_t* sat = ks_at[y] + off + 8 * h * T::SCALEB;
+          j[h] = D == 128 ? lds16(sat) : *sat;
+        }
+        Q4Scale s0 = q4_scale(j[0] & 255u), s1 = q4_scale(j[1] & 255u);
 #pragma unroll
-          for (int x = 0; x < KWORDS; ++x) {
-            if (x == 2) sc = q4_scale(j >> 8, j >> 8);
-            mma16816(s[2 * y + h], qf[2 * x], q4_pair<0>(kw[x], sc), q4_pair<1>(kw[x], sc));
-            mma16816(s[2 * y + h], qf[2 * x + 1], q4_pair<2>(kw[x], sc), q4_pair<3>(kw[x], sc));
+        for (int x = 0; x < KWORDS; ++x) {
+          if (x == 2) {
+            s0 = q4_scale(j[0] >> 8);
+            s1 = q4_scale(j[1] >> 8);
+          }
+          const uint32_t a0[4] = {q4_pair<0>(kw[0][x], s0), q4_pair<0>(kw[1][x], s1), q4_pair<1>(kw[0][x], s0),
+                                  q4_pair<1>(kw[1][x], s1)};
+          const uint32_t a1[4] = {q4_pair<2>(kw[0][x], s0), q4_pair<2>(kw[1][x], s1), q4_pair<3>(kw[0][x], s0),
+                                  q4_pair<3>(kw[1][x], s1)};
+#pragma unroll
+          for (int u = 0; u < G; ++u) {
+            if (x == 0)
+              q4_mma_first(s[y][u], a0, qf[u][0][0], qf[u][0][1]);
+            else
+              q4_mma(s[y][u], a0, qf[u][2 * x][0], qf[u][2 * x][1]);
+            q4_mma(s[y][u], a1, qf[u][2 * x + 1][0], qf[u][2 * x + 1][1]);
           }
         }
       }
       // p = silu(alpha S) = h + h tanh(h), h = alpha S / 2
       const bool masked = kb + C::KEYS > g.walk.p0 + 1 || kb + C::KEYS > g.seq.hist;
-      uint32_t hi[KS][4], lo[KS][4];
+      uint32_t hi[KS][G][2], lo[KS][G][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (r == 0 || !few) {
+      for (int y = 0; y < KS; ++y) {
 #pragma unroll
-          for (int n = 0; n < 2 * KS; ++n) {
-            const float2 x = __fmul2_rn(make_float2(s[n][2 * r], s[n][2 * r + 1]), ha2);
+        for (int u = 0; u < G; ++u) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 x = __fmul2_rn(make_float2(s[y][u][2 * h], s[y][u][2 * h + 1]), ha2);
             float2 p = __ffma2_rn(x, make_float2(tanh_approx(x.x), tanh_approx(x.y)), x);
             if (masked) {
-              const int pos = g.walk.p0 + 8 * r + g8, k0 = kb + key0[n >> 1] + 8 * (n & 1);
-              const int x0 = k0 + vk[0], x1 = k0 + vk[1];
-              if (!(x0 <= pos && (x0 < g.seq.hist || x0 == pos))) p.x = 0.f;
-              if (!(x1 <= pos && (x1 < g.seq.hist || x1 == pos))) p.y = 0.f;
+              const int col = both ? 2 * (t4 & 1) : 8 * u + 2 * t4;
+              const int pos = g.walk.p0 + col, key = kb + C::KW * warp + 16 * y + 8 * h + kk;
+              if (!(key <= pos && (key < g.seq.hist || key == pos))) p.x = 0.f;
+              if (!(key <= pos + 1 && (key < g.seq.hist || key == pos + 1))) p.y = 0.f;
             }
             const uint32_t ph2 = pack_bf16x2(p.x, p.y);
             const float2 rest = __fadd2_rn(
                 p, make_float2(-__uint_as_float(ph2 << 16), -__uint_as_float(ph2 & 0xffff0000u)));
-            hi[n >> 1][2 * (n & 1) + r] = ph2;
-            lo[n >> 1][2 * (n & 1) + r] = pack_bf16x2(rest.x, rest.y);
+            const uint32_t pl2 = pack_bf16x2(rest.x, rest.y);
+            hi[y][u][h] = transpose8(both && t4 >= 2 ? pl2 : ph2);
+            if (!both) lo[y][u][h] = transpose8(pl2);
           }
-        } else {
-          // rows 8 .. 15 of the operand: the second terms of rows 0 .. 7
-#pragma unroll
-          for (int n = 0; n < 2 * KS; ++n) hi[n >> 1][2 * (n & 1) + 1] = lo[n >> 1][2 * (n & 1)];
         }
       }
 #pragma unroll
@@ -472,41 +500,51 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
           uint32_t j[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t at = off + v_at[y] + (8 * h + vk[e]) * T::CODEB;
+            const uint8_t* at = v_at[y][e] + off + 8 * h * T::CODEB;
             if constexpr (D == 32)
               vw[h][e][0] = lds16(at);
             else
               lds_words<VWORDS>(at, vw[h][e]);
-            j[e] = lds8(off + vs_at[y] + (8 * h + vk[e]) * T::SCALEB);
+            j[e] = vs_at[y][e][off + 8 * h * T::SCALEB];
           }
           sc[h] = q4_scale(j[0], j[1]);
         }
 #pragma unroll
         for (int x = 0; x < VWORDS; ++x) {
+          uint32_t b[4][4];  // operands of four (at d = 32 two) tiles of O^T
+          uint32_t u[2][2];  // [channels' halves][keys' halves], two keys side by side
 #pragma unroll
-          for (int half = 0; half < (D == 32 ? 1 : 2); ++half) {
-            uint32_t u[2];  // the keys' even, then odd, channels side by side
-#pragma unroll
-            for (int h = 0; h < 2; ++h) u[h] = __byte_perm(vw[h][0][x], vw[h][1][x], half ? 0x7632 : 0x5410);
-            uint32_t b[4][2];
+          for (int h = 0; h < 2; ++h) {
+            u[0][h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x5410);
+            u[1][h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x7632);
+          }
+          if constexpr (D == 32) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              b[0][h] = q4_pair<0>(u[h], sc[h]);
-              b[1][h] = q4_pair<1>(u[h], sc[h]);
-              b[2][h] = q4_pair<2>(u[h], sc[h]);
-              b[3][h] = q4_pair<3>(u[h], sc[h]);
+              b[0][2 * h] = q4_pair<0>(u[0][h], sc[h]);
+              b[0][2 * h + 1] = q4_pair<1>(u[0][h], sc[h]);
+              b[1][2 * h] = q4_pair<2>(u[0][h], sc[h]);
+              b[1][2 * h + 1] = q4_pair<3>(u[0][h], sc[h]);
             }
+          } else {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              float(&acc)[4] = o[D == 32 ? n : 8 * x + 2 * n + half];
-              mma16816(acc, hi[y], b[n][0], b[n][1]);
-            }
-            if (!few) {
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                float(&acc)[4] = o[D == 32 ? n : 8 * x + 2 * n + half];
-                mma16816(acc, lo[y], b[n][0], b[n][1]);
+              for (int r = 0; r < 2; ++r) {
+                b[0][2 * h + r] = q4_pair<0>(u[r][h], sc[h]);
+                b[1][2 * h + r] = q4_pair<1>(u[r][h], sc[h]);
+                b[2][2 * h + r] = q4_pair<2>(u[r][h], sc[h]);
+                b[3][2 * h + r] = q4_pair<3>(u[r][h], sc[h]);
               }
+          }
+          constexpr int N = D == 32 ? 2 : 4;
+#pragma unroll
+          for (int v = 0; v < G; ++v) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) q4_mma(o[v][4 * x + n], b[n], hi[y][v][0], hi[y][v][1]);
+            if (!both) {
+#pragma unroll
+              for (int n = 0; n < N; ++n) q4_mma(o[v][4 * x + n], b[n], lo[y][v][0], lo[y][v][1]);
             }
           }
         }
@@ -519,26 +557,30 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
       }
     }
 
-    // the warps' sums over their keys, then out or this CTA's part.  Columns
-    // 2 t4 + e of O's n tiles are D / 8 consecutive channels.
+    // the warps' sums over their keys, then out or this CTA's part.  The rows
+    // of O^T's tiles are D / 8 consecutive channels (at d = 32 every other one).
+    if (both) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = 8 * r + g8;
-      if (row < rows) {
-        float* dst = red + (warp * a.red_rows + row) * RS + t4 * (D / 4);
-        auto val = [&](int n, int e) { return few ? o[n][e] + o[n][2 + e] : o[n][2 * r + e]; };
-        if constexpr (D == 32) {
+      for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int n = 0; n < 4; n += 2)
-            *reinterpret_cast<float4*>(dst + 2 * n) =
-                make_float4(val(n, 0), val(n, 1), val(n + 1, 0), val(n + 1, 1));
-        } else {
+        for (int j = 0; j < 4; ++j) o[0][n][j] += __shfl_xor_sync(0xffffffffu, o[0][n][j], 2);
+    }
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+    for (int u = 0; u < G; ++u) {
 #pragma unroll
-            for (int n = 0; n < NT; n += 4)
-              *reinterpret_cast<float4*>(dst + e * NT + n) =
-                  make_float4(val(n, e), val(n + 1, e), val(n + 2, e), val(n + 3, e));
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * u + 2 * t4 + e;
+        if (row < rows) {
+          float* dst = red + (warp * a.red_rows + row) * RS;
+          if constexpr (D == 32) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) dst[8 * (g8 >> 1) + 2 * n + (g8 & 1)] = o[u][n >> 1][2 * (n & 1) + e];
+          } else {
+#pragma unroll
+            for (int n = 0; n < MT; n += 2)
+              *reinterpret_cast<float4*>(dst + g8 * (D / 8) + 2 * n) =
+                  make_float4(o[u][n][e], o[u][n][2 + e], o[u][n + 1][e], o[u][n + 1][2 + e]);
+          }
         }
       }
     }
@@ -557,7 +599,7 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
     // one answer for the warp, whose lanes meet again in the next item's waits:
     // the copying warp may give up between two lanes' reads
     dead = __any_sync(0xffffffffu, *static_cast<volatile int*>(&m->abort_flag) != 0);
-    uint16_t* out = a.out + ((long long)(g.seq.q0 + kStepRows * g.qt) * w.heads + g.h) * D;
+    uint16_t* out = a.out + ((long long)(g.seq.q0 + w.tile_rows * g.qt) * w.heads + g.h) * D;
     const bool before = g.c0 != (int)blockIdx.x;
     float* part = step_part<D>(a, blockIdx.x, !before);
     for (int x = 4 * threadIdx.x; x < rows * D; x += 4 * 32 * C::WARPS) {
@@ -583,7 +625,7 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
   step_join<D, C::WARPS>(a, w, m, cut0, cut1, dead);
 }
 
-template <int D, bool CLUSTER>
+template <int D, int G, bool CLUSTER>
 __global__ void __launch_bounds__(Q4Cfg<D>::THREADS, Q4Cfg<D>::PER_SM)
     step_q4_kernel(const StepArgs a, const Q4Pool pool) {
   using C = Q4Cfg<D>;
@@ -624,19 +666,25 @@ __global__ void __launch_bounds__(Q4Cfg<D>::THREADS, Q4Cfg<D>::PER_SM)
   if (warp == C::WARPS)
     q4_produce<D>(a, pool, w, c, g, base, full, empty, wt);
   else
-    q4_compute<D, CLUSTER>(a, pool, w, c, g, base, full, empty, red, m, wt);
+    q4_compute<D, G, CLUSTER>(a, pool, w, c, g, smem_raw + (base - raw), full, empty, red, m, wt);
   if constexpr (CLUSTER) step_cluster_join<D, C::THREADS>(a, g, rank, red, &m->abort_flag);
 }
 
+// The kernels' shared memory, once a device.
 template <int D>
 cudaError_t q4_prepare() {
   static DeviceOnce once;
   return once.run([] {
-    const cudaError_t e = cudaFuncSetAttribute(
-        step_q4_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ4BytesMost<D>);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(step_q4_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kQ4BytesMost<D>);
+    cudaError_t e = cudaSuccess;
+    auto allow = [&e](const void* kernel) {
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ4BytesMost<D>);
+    };
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 1, false>));
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 1, true>));
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 2, false>));
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 2, true>));
+    return e;
   });
 }
 
@@ -644,11 +692,11 @@ template <int D>
 cudaError_t clusters_q4(int* n) {
   const cudaError_t e = q4_prepare<D>();
   if (e != cudaSuccess) return e;
-  return clusters_at_once(step_q4_kernel<D, true>, Q4Cfg<D>::THREADS, kQ4BytesMost<D>, n);
+  return clusters_at_once(step_q4_kernel<D, 2, true>, Q4Cfg<D>::THREADS, kQ4BytesMost<D>, n);
 }
 
-template <int D>
-cudaError_t launch_step_q4_d(const Q4Pool& pool, long long most, bool clusters, StepArgs a, int sms,
+template <int D, int G>
+cudaError_t launch_step_q4_g(const Q4Pool& pool, long long most, bool clusters, StepArgs a, int sms,
                              cudaStream_t stream) {
   using C = Q4Cfg<D>;
   a.stages = C::STAGES;
@@ -656,11 +704,17 @@ cudaError_t launch_step_q4_d(const Q4Pool& pool, long long most, bool clusters, 
   const cudaError_t e = q4_prepare<D>();
   if (e != cudaSuccess) return e;
   if (clusters)
-    return launch_after_in_clusters(kStepCluster, step_q4_kernel<D, true>,
+    return launch_after_in_clusters(kStepCluster, step_q4_kernel<D, G, true>,
                                     kStepCluster * a.w.tiles * a.p.batch * a.w.heads, C::THREADS, bytes,
                                     stream, a, pool);
   const int grid = (int)std::min<long long>((long long)C::PER_SM * sms, most);
-  return launch_after(step_q4_kernel<D, false>, grid, C::THREADS, bytes, stream, a, pool);
+  return launch_after(step_q4_kernel<D, G, false>, grid, C::THREADS, bytes, stream, a, pool);
+}
+template <int D>
+cudaError_t launch_step_q4_d(const Q4Pool& pool, long long most, bool clusters, const StepArgs& a, int sms,
+                             cudaStream_t stream) {
+  return a.red_rows <= 8 ? launch_step_q4_g<D, 1>(pool, most, clusters, a, sms, stream)
+                         : launch_step_q4_g<D, 2>(pool, most, clusters, a, sms, stream);
 }
 
 template <int D>

@@ -31,11 +31,13 @@
 constexpr int kStepWords = 16, kItemWords = 16;
 constexpr int kPagedThreads = 768;  // four SiLU warpgroups, the wide P layout, at every d
 // What the keys and values come from: the bf16 pools' tensor maps, or the pages
-// of 4-bit codes, which two warps each turn into the bf16 tiles.
+// of 4-bit codes, which two warps each turn into the bf16 tiles.  Those are the
+// first four (the keys' on even, the values' on odd schedulers), and the
+// epilogue the last: candidates 332 us, 340 with them the other way round.
 struct PagedMaps {
   CUtensorMap k, v;
 };
-constexpr int kUnpackWarp0 = kPagedThreads / 32, kUnpackWarps = 2;  // the keys', then the values'
+constexpr int kUnpackWarps = 2, kSiluWarps = 16;
 template <class SRC>
 constexpr bool kHeldInQ4 = std::is_same<SRC, Q4Pool>::value;
 template <class SRC>
@@ -292,7 +294,13 @@ __device__ void paged_unpack(const CUtensorMap* tm_q, uint32_t steps, const Page
   constexpr int LANES = D < 64 ? 1 : 2;   // that share a row of a chunk of channels
   constexpr int ROWS = 32 / LANES;        // a warp's rows of a load
   constexpr int STEP = ROWS * kUnpackWarps;
-  constexpr int GROUPS = kBN / STEP;      // 4, at d = 32 2
+  // Loads a round of the loop.  At d = 128 the unpacking itself bounds the
+  // kernel, and four in flight at once are faster (chunks of 100 to 700 tokens
+  // 111 us, 122 with two, 127 with one); else what counts is that the kernel's
+  // loops together fit the instruction cache (candidates 364 us with four, 339
+  // with two, 338 with one).
+  constexpr int GROUPS = D == 128 ? 4 : 2;
+  constexpr int ROUNDS = kBN / STEP / GROUPS;
   const RawRing<D> ring{base, which};
   const uint32_t bars = base + C::BAR_OFF;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
@@ -333,26 +341,33 @@ __device__ void paged_unpack(const CUtensorMap* tm_q, uint32_t steps, const Page
       }
     }
     if (!__all_sync(0xffffffffu, ok)) break;
-    const uint32_t from = ring.stage(raw), to = dst + slot * C::TILEB;
 #pragma unroll 1
-    for (int ch = 0; ch < C::NCHUNK; ++ch) {
+    for (int q = 0; q < C::NCHUNK * ROUNDS; ++q) {
+      const int ch = q / ROUNDS, first = (q % ROUNDS) * GROUPS * STEP;
+      const uint32_t from = ring.stage(raw) + src + first * T::CODEB + 32 * ch;
+      const uint32_t from_sc = ring.stage(raw) + src_sc + first * T::SCALEB + 4 * ch;
+      const uint32_t to = dst + slot * C::TILEB + first * C::ROWB + ch * C::CHUNKB;
       uint4 u[GROUPS];
       uint32_t sc[GROUPS];
 #pragma unroll
       for (int x = 0; x < GROUPS; ++x) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(u[x].x), "=r"(u[x].y), "=r"(u[x].z), "=r"(u[x].w)
-                     : "r"(from + src + x * STEP * T::CODEB + 32 * ch)
+                     : "r"(from + x * STEP * T::CODEB)
                      : "memory");
-        asm volatile("ld.shared.u16 %0, [%1];"
-                     : "=r"(sc[x])
-                     : "r"(from + src_sc + x * STEP * T::SCALEB + 4 * ch)
-                     : "memory");
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc[x]) : "r"(from_sc + x * STEP * T::SCALEB) : "memory");
+      }
+      if (D == 128 && q == C::NCHUNK * ROUNDS - 1) {
+        // the stage is read: its next codes may come while these are converted
+        // (chunks of 100 to 700 tokens 110 us, 123 without; at d = 64, with four
+        // stages, the candidates would take 431 us, 364 without)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.empty(raw));
       }
 #pragma unroll
       for (int x = 0; x < GROUPS; ++x) {
-        const Q4Scale s0 = q4_scale(sc[x] & 255u, sc[x] & 255u), s1 = q4_scale(sc[x] >> 8, sc[x] >> 8);
-        const uint32_t st = to + x * STEP * C::ROWB + ch * C::CHUNKB;
+        const Q4Scale s0 = q4_scale(sc[x] & 255u), s1 = q4_scale(sc[x] >> 8);
+        const uint32_t st = to + x * STEP * C::ROWB;
         st_shared16(st, q4_word(u[x].x, s0));
         st_shared16(st ^ 16u, q4_word(u[x].y, s0));
         st_shared16(st ^ 32u, q4_word(u[x].z, s1));
@@ -362,7 +377,7 @@ __device__ void paged_unpack(const CUtensorMap* tm_q, uint32_t steps, const Page
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(ring.empty(raw));
+      if (D != 128) mbar_arrive(ring.empty(raw));
       mbar_arrive(bar((which ? C::B_VFULL : C::B_QKREADY) + j));
     }
     if (++j == C::P) j = 0;
@@ -662,7 +677,7 @@ __device__ void paged_epilogue(const PagedFwdArgs& a, uint32_t steps, PagedWords
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + ob));
-    if (threadIdx.x == 0) words->cut[starts] = g;
+    if (row == 0) words->cut[starts] = g;
   }
 }
 
@@ -779,18 +794,15 @@ __global__ void __launch_bounds__(kPagedThreadsOf<SRC>, 1)
       paged_producer<D, true>(&src.k, &tm_q, a, w, from, first, &words, base, wt);
     else
       paged_producer<D, false>(&src.v, &tm_q, a, w, from, first, &words, base, wt);
-  } else if (Q4 && warp >= kUnpackWarp0) {
-    if constexpr (Q4) {
-      const int i = warp - kUnpackWarp0;
-      paged_unpack<D>(&tm_q, steps, &words, base, wt, i / kUnpackWarps, i % kUnpackWarps);
-    }
+  } else if (Q4 && warp < 2 * kUnpackWarps) {
+    if constexpr (Q4) paged_unpack<D>(&tm_q, steps, &words, base, wt, warp & 1, warp >> 1);
   } else if (warp == kMmaWarpQK) {
     if (lane == 0) paged_mma_qk<D, Q4>(a, steps, &words, base, tmem, wt);
     __syncwarp();
   } else if (warp == kMmaWarpPV) {
     if (lane == 0) paged_mma_pv<D, Q4>(steps, &words, base, tmem, wt);
     __syncwarp();
-  } else if (warp >= kEwWarp0) {
+  } else if (warp >= kEwWarp0 && warp < kEwWarp0 + kSiluWarps) {
     paged_silu<D>(a, steps, &words, base, tmem, wt, warp, lane);
   } else {
     paged_epilogue<D>(a, steps, &words, base, tmem, wt, warp, lane);

@@ -51,10 +51,12 @@ struct Q4Tile {
 };
 
 // ---------------------------------------------------------------- from codes
-// bf16 bits of 16 s_j, in both halves of a word, for two scales' bytes j.
+// bf16 bits of 16 s_j, in both halves of a word, for two scales' bytes j, and
+// for one.
 __device__ __forceinline__ uint32_t q4_scales(uint32_t j_lo, uint32_t j_hi) {
-  return ((j_lo | j_hi << 16) << 4) + (111u << 7) * 0x10001u;
+  return j_lo * 0x10u + (j_hi * 0x100000u + (111u << 7) * 0x10001u);
 }
+__device__ __forceinline__ uint32_t q4_scales(uint32_t j) { return j * 0x100010u + (111u << 7) * 0x10001u; }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -69,10 +71,11 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 struct Q4Scale {
   uint32_t s16, s24;
 };
+__device__ __forceinline__ Q4Scale q4_scale_of(uint32_t s) { return Q4Scale{s, mul_bf16x2(s, 0xbfc0bfc0u)}; }
 __device__ __forceinline__ Q4Scale q4_scale(uint32_t j_lo, uint32_t j_hi) {
-  const uint32_t s = q4_scales(j_lo, j_hi);
-  return Q4Scale{s, mul_bf16x2(s, 0xbfc0bfc0u)};
+  return q4_scale_of(q4_scales(j_lo, j_hi));
 }
+__device__ __forceinline__ Q4Scale q4_scale(uint32_t j) { return q4_scale_of(q4_scales(j)); }
 // The codes in nibble I of both halves of w: 1 + (8 + q) / 16 as bf16, then
 // 16 s (1 + (8 + q) / 16) - 24 s = q s, exact.
 template <int I>
