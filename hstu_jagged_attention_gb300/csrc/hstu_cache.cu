@@ -675,6 +675,12 @@ int check_batch(const hstu_paged_batch* b, PagedView* v, int num_pages, int page
 
 constexpr long long kMostUnits = 1 << 30;
 
+// Parts of an item, on average at most: the last of its CTAs sums them alone.
+// The 4-bit cache's CTAs take a block apart for longer than they wait for it, so
+// there more of them pay (four sequences of 10240 to 20480 tokens, 16 items:
+// 13.0 us with 32 parts, 15.6 with 16).
+constexpr int kMostParts = 16, kMostPartsQ4 = 32;
+
 // Units for what an item costs besides its blocks (its queries' load, the
 // pipeline's filling, its rows' way out).  With 0, 1, 2 and 3 of them, 16 x
 // 4096 tokens from an empty cache (items of 1 to 32 blocks) took 300, 242, 249
@@ -879,6 +885,7 @@ int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int p
   hstu::PagedWork w{};
   w.heads = heads;
   w.extra = extra;
+  w.most_parts = kMostParts;
   w.tile_rows = tile_rows;
   w.tiles = v.rows > 0 && v.batch > 0 && v.max_q > 0 ? (v.max_q - 1) / tile_rows + 1 : 0;
   while ((1 << w.kb_shift) < block_keys) ++w.kb_shift;
@@ -1004,11 +1011,13 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   w.tiles = p.max_q > 0 ? (p.max_q - 1) / w.tile_rows + 1 : 1;  // a bound of 0: only the lengths are checked
   w.kb_shift = hstu::kStepShift;  // both kernels' blocks have 128 keys
   w.extra = item_units(d);
+  w.most_parts = kMostParts;
   const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra));
   if (tiled) {
     w.tile_rows = HSTU_BLOCK_M;
     w.tiles = (p.max_q - 1) / w.tile_rows + 1;
   }
+  if (cache->q4.pages && !tiled) w.most_parts = kMostPartsQ4;
   const long long most = units_bound(p, heads, w.tiles, w.kb_shift, w.extra);
   if (most > kMostUnits) return HSTU_ERR_INVALID_ARG;
   const bool clusters = !tiled && use_clusters(p, heads, w.tiles, cache->clusters);

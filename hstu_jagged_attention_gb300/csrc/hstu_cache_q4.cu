@@ -14,6 +14,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "hstu_attn.h"
 #include "hstu_internal.h"
@@ -225,9 +226,9 @@ __global__ void __launch_bounds__(kQ4Threads) read_q4_kernel(const ReadArgs a, c
 //     % 4 for row 8 a + 2 t + e lets neither load meet a bank twice (at d = 128,
 //     (t + e) % 4: K's do not, V's meet two);
 //   P^T's operand is S^T's result transposed: one movmatrix a 8 x 8 tile.
-// p is split into two bf16 terms.  With up to 4 tokens in a tile columns 4 .. 7
-// are the same tokens' and take the second terms: one product for both.
-// G: groups of 8 tokens a tile holds.
+// p is split into two bf16 terms.  TOKENS: what a tile holds, 4, 8 or 16 (two
+// groups of columns).  With 4, columns 4 .. 7 are the same tokens' and take the
+// second terms: one product for both.
 // Keys past a row's last are masked by a select on p; whatever bytes lie
 // there, as codes they are finite, and so add nothing.
 template <int D>
@@ -363,12 +364,14 @@ __device__ __forceinline__ int q4_key(int t, int e) {
   return 4 * e + ((t + (D == 128 ? e : 2 * e)) & 3);
 }
 
-template <int D, int G, bool CLUSTER>
+template <int D, int TOKENS, bool CLUSTER>
 __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWork& w, PagedCursor c, PagedSeg g,
                            const uint8_t* ring, uint32_t full, uint32_t empty, float* red,
                            StepMisc<Q4Cfg<D>::WARPS>* m, const StepWait& wt) {
   using C = Q4Cfg<D>;
   using T = Q4Tile<D>;
+  constexpr int G = TOKENS == 16 ? 2 : 1;       // groups of 8 columns
+  constexpr bool both = TOKENS == 4;            // columns 4 .. 7: the second terms of tokens 0 .. 3
   constexpr int KS = C::KW / 16;                // 16-key steps of a block
   constexpr int KWORDS = D / 32;                // words of a lane's channels of a key
   constexpr int VWORDS = D >= 64 ? D / 64 : 1;  // of a value: at d = 32 half a word
@@ -405,7 +408,6 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
     dead = !__all_sync(0xffffffffu, step_wait(full + 8u * C::MAX_STAGES - 8u, 0, wt, kSiteUnsignalledStep));
   while (c.next(a.p, w, &g)) {
     const int rows = g.walk.rows;
-    const bool both = G == 1 && rows <= 4;  // columns 4 .. 7: the second terms of tokens 0 .. 3
     uint32_t qf[G][MT][2];
 #pragma unroll
     for (int u = 0; u < G; ++u) {
@@ -465,31 +467,38 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
         }
       }
       // p = silu(alpha S) = h + h tanh(h), h = alpha S / 2
-      const bool masked = kb + C::KEYS > g.walk.p0 + 1 || kb + C::KEYS > g.seq.hist;
       uint32_t hi[KS][G][2], lo[KS][G][2];
+      auto silu = [&](auto masked) {
 #pragma unroll
-      for (int y = 0; y < KS; ++y) {
+        for (int y = 0; y < KS; ++y) {
 #pragma unroll
-        for (int u = 0; u < G; ++u) {
+          for (int u = 0; u < G; ++u) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float2 x = __fmul2_rn(make_float2(s[y][u][2 * h], s[y][u][2 * h + 1]), ha2);
-            float2 p = __ffma2_rn(x, make_float2(tanh_approx(x.x), tanh_approx(x.y)), x);
-            if (masked) {
-              const int col = both ? 2 * (t4 & 1) : 8 * u + 2 * t4;
-              const int pos = g.walk.p0 + col, key = kb + C::KW * warp + 16 * y + 8 * h + kk;
-              if (!(key <= pos && (key < g.seq.hist || key == pos))) p.x = 0.f;
-              if (!(key <= pos + 1 && (key < g.seq.hist || key == pos + 1))) p.y = 0.f;
+            for (int h = 0; h < 2; ++h) {
+              const float2 x = __fmul2_rn(make_float2(s[y][u][2 * h], s[y][u][2 * h + 1]), ha2);
+              float2 p = __ffma2_rn(x, make_float2(tanh_approx(x.x), tanh_approx(x.y)), x);
+              if constexpr (decltype(masked)::value) {
+                const int pos = g.walk.p0 + (both ? 2 * (t4 & 1) : 8 * u + 2 * t4);
+                const int key = kb + C::KW * warp + 16 * y + 8 * h + kk;
+                if (!(key <= pos && (key < g.seq.hist || key == pos))) p.x = 0.f;
+                if (!(key <= pos + 1 && (key < g.seq.hist || key == pos + 1))) p.y = 0.f;
+              }
+              const uint32_t ph2 = pack_bf16x2(p.x, p.y);
+              const float2 rest = __fadd2_rn(
+                  p, make_float2(-__uint_as_float(ph2 << 16), -__uint_as_float(ph2 & 0xffff0000u)));
+              const uint32_t pl2 = pack_bf16x2(rest.x, rest.y);
+              hi[y][u][h] = transpose8(both && t4 >= 2 ? pl2 : ph2);
+              if constexpr (!both) lo[y][u][h] = transpose8(pl2);
             }
-            const uint32_t ph2 = pack_bf16x2(p.x, p.y);
-            const float2 rest = __fadd2_rn(
-                p, make_float2(-__uint_as_float(ph2 << 16), -__uint_as_float(ph2 & 0xffff0000u)));
-            const uint32_t pl2 = pack_bf16x2(rest.x, rest.y);
-            hi[y][u][h] = transpose8(both && t4 >= 2 ? pl2 : ph2);
-            if (!both) lo[y][u][h] = transpose8(pl2);
           }
         }
-      }
+      };
+      // two copies: the tests of a masked block, merged into one, would be
+      // issued in every block
+      if (kb + C::KEYS > g.walk.p0 + 1 || kb + C::KEYS > g.seq.hist)
+        silu(std::true_type{});
+      else
+        silu(std::false_type{});
 #pragma unroll
       for (int y = 0; y < KS; ++y) {
         // four keys: vw[h][e] is key 8 h + vk[e] of the step
@@ -542,7 +551,7 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
           for (int v = 0; v < G; ++v) {
 #pragma unroll
             for (int n = 0; n < N; ++n) q4_mma(o[v][4 * x + n], b[n], hi[y][v][0], hi[y][v][1]);
-            if (!both) {
+            if constexpr (!both) {
 #pragma unroll
               for (int n = 0; n < N; ++n) q4_mma(o[v][4 * x + n], b[n], lo[y][v][0], lo[y][v][1]);
             }
@@ -559,7 +568,7 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
 
     // the warps' sums over their keys, then out or this CTA's part.  The rows
     // of O^T's tiles are D / 8 consecutive channels (at d = 32 every other one).
-    if (both) {
+    if constexpr (both) {
 #pragma unroll
       for (int n = 0; n < MT; ++n)
 #pragma unroll
@@ -625,7 +634,7 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
   step_join<D, C::WARPS>(a, w, m, cut0, cut1, dead);
 }
 
-template <int D, int G, bool CLUSTER>
+template <int D, int TOKENS, bool CLUSTER>
 __global__ void __launch_bounds__(Q4Cfg<D>::THREADS, Q4Cfg<D>::PER_SM)
     step_q4_kernel(const StepArgs a, const Q4Pool pool) {
   using C = Q4Cfg<D>;
@@ -666,7 +675,7 @@ __global__ void __launch_bounds__(Q4Cfg<D>::THREADS, Q4Cfg<D>::PER_SM)
   if (warp == C::WARPS)
     q4_produce<D>(a, pool, w, c, g, base, full, empty, wt);
   else
-    q4_compute<D, G, CLUSTER>(a, pool, w, c, g, smem_raw + (base - raw), full, empty, red, m, wt);
+    q4_compute<D, TOKENS, CLUSTER>(a, pool, w, c, g, smem_raw + (base - raw), full, empty, red, m, wt);
   if constexpr (CLUSTER) step_cluster_join<D, C::THREADS>(a, g, rank, red, &m->abort_flag);
 }
 
@@ -680,10 +689,12 @@ cudaError_t q4_prepare() {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ4BytesMost<D>);
     };
-    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 1, false>));
-    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 1, true>));
-    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 2, false>));
-    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 2, true>));
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 4, false>));
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 4, true>));
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 8, false>));
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 8, true>));
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 16, false>));
+    allow(reinterpret_cast<const void*>(step_q4_kernel<D, 16, true>));
     return e;
   });
 }
@@ -692,11 +703,11 @@ template <int D>
 cudaError_t clusters_q4(int* n) {
   const cudaError_t e = q4_prepare<D>();
   if (e != cudaSuccess) return e;
-  return clusters_at_once(step_q4_kernel<D, 2, true>, Q4Cfg<D>::THREADS, kQ4BytesMost<D>, n);
+  return clusters_at_once(step_q4_kernel<D, 16, true>, Q4Cfg<D>::THREADS, kQ4BytesMost<D>, n);
 }
 
-template <int D, int G>
-cudaError_t launch_step_q4_g(const Q4Pool& pool, long long most, bool clusters, StepArgs a, int sms,
+template <int D, int TOKENS>
+cudaError_t launch_step_q4_t(const Q4Pool& pool, long long most, bool clusters, StepArgs a, int sms,
                              cudaStream_t stream) {
   using C = Q4Cfg<D>;
   a.stages = C::STAGES;
@@ -704,17 +715,19 @@ cudaError_t launch_step_q4_g(const Q4Pool& pool, long long most, bool clusters, 
   const cudaError_t e = q4_prepare<D>();
   if (e != cudaSuccess) return e;
   if (clusters)
-    return launch_after_in_clusters(kStepCluster, step_q4_kernel<D, G, true>,
+    return launch_after_in_clusters(kStepCluster, step_q4_kernel<D, TOKENS, true>,
                                     kStepCluster * a.w.tiles * a.p.batch * a.w.heads, C::THREADS, bytes,
                                     stream, a, pool);
   const int grid = (int)std::min<long long>((long long)C::PER_SM * sms, most);
-  return launch_after(step_q4_kernel<D, G, false>, grid, C::THREADS, bytes, stream, a, pool);
+  return launch_after(step_q4_kernel<D, TOKENS, false>, grid, C::THREADS, bytes, stream, a, pool);
 }
 template <int D>
 cudaError_t launch_step_q4_d(const Q4Pool& pool, long long most, bool clusters, const StepArgs& a, int sms,
                              cudaStream_t stream) {
-  return a.red_rows <= 8 ? launch_step_q4_g<D, 1>(pool, most, clusters, a, sms, stream)
-                         : launch_step_q4_g<D, 2>(pool, most, clusters, a, sms, stream);
+  // red_rows: the most new tokens that a tile can hold
+  if (a.red_rows <= 4) return launch_step_q4_t<D, 4>(pool, most, clusters, a, sms, stream);
+  if (a.red_rows <= 8) return launch_step_q4_t<D, 8>(pool, most, clusters, a, sms, stream);
+  return launch_step_q4_t<D, 16>(pool, most, clusters, a, sms, stream);
 }
 
 template <int D>

@@ -117,20 +117,20 @@ HSTU_HD PagedWalk paged_walk(const PagedSeq& s, int qt, int tile_rows, int kb_sh
 // share's end cuts is summed from the CTAs' parts, in their order.
 struct PagedWork {
   int heads, tiles, tile_rows, kb_shift, extra;
+  int most_parts;  // see paged_share
   int total, per;  // units (at most 2^30: the host checks) and units a CTA
 };
 
-// Units a CTA: an equal share, but no item cut into more than kMostParts parts
+// Units a CTA: an equal share, but no item cut into more than most_parts parts
 // on average, which the last of its CTAs would sum alone.
-constexpr int kMostParts = 16;
 HSTU_HD int paged_share(const PagedWork& w, int batch, int grid, int min_units) {
   const unsigned total = (unsigned)w.total, items = (unsigned)w.tiles * (unsigned)batch * (unsigned)w.heads;
   // ceil(total / grid), from the fp32 quotient (a few off for the largest totals)
   unsigned per = (unsigned)((float)total / (float)grid);
   while (per * (unsigned)grid < total) ++per;
   while (per > 0 && (per - 1u) * (unsigned)grid >= total) --per;
-  if (items < (unsigned)grid / kMostParts) {
-    const unsigned least = (total + kMostParts * items - 1u) / (kMostParts * items);
+  if (items < (unsigned)grid / w.most_parts) {
+    const unsigned least = (total + w.most_parts * items - 1u) / (w.most_parts * items);
     if (per < least) per = least;
   }
   return per > (unsigned)min_units ? (int)per : min_units;

@@ -702,7 +702,8 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
  * costs besides them.  CTA c of `grid` takes units [c per, (c + 1) per), per =
  * max(ceil(units / grid), min_units) or, with fewer than grid / 16 items =
  * tiles * batch * heads, at least ceil(units / (16 items)): no item is cut into
- * many more than 16.  (The kernels' min_units is 1.)  Segment i of host_dst is
+ * many more than 16.  (The kernels' min_units is 1, and a cache of 4-bit codes
+ * allows 32 parts to an item of 16-row tiles.)  Segment i of host_dst is
  * eight numbers: (CTA, sequence, head, tile, index of its first block in the
  * walk, blocks, first CTA of the item, CTAs that share the item).
  * tile_rows >= 1, block_keys a power of two.
