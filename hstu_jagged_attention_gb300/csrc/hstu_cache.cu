@@ -766,12 +766,11 @@ bool bad_rows(const void* p, int64_t stride, long long width) {
   return hstu::bad_ptr(p, 16) || stride < width || (stride & 7);
 }
 
-// CTAs that take 16 channels a thread, behind those that check a sequence a
-// thread; `spare` rows more than there are (the 4-bit cache's kernels round up).
-int unit_grid(const PagedView& p, int width, int spare, unsigned* check_ctas, int* grid) {
-  constexpr int T = hstu::kAppendThreads;
-  *check_ctas = ((unsigned)p.batch + T - 1) / T;
-  const long long all = *check_ctas + (((long long)p.rows + spare) * (width / 16) + T - 1) / T;
+// CTAs of `threads` threads that take 16 channels a thread, behind those that
+// check a sequence a thread.
+int unit_grid(const PagedView& p, int width, int threads, unsigned* check_ctas, int* grid) {
+  *check_ctas = ((unsigned)p.batch + threads - 1) / threads;
+  const long long all = *check_ctas + ((long long)p.rows * (width / 16) + threads - 1) / threads;
   if (all > 0x7fffffffLL) return HSTU_ERR_INVALID_ARG;
   *grid = (int)all;
   return HSTU_OK;
@@ -957,10 +956,12 @@ int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, co
   a.heads = cache->heads;
   a.d = cache->d;
   a.status = cache->status;
-  int grid;
-  if ((rc = unit_grid(a.p, width, cache->q4.pages ? 15 : 0, &a.check_ctas, &grid)) != HSTU_OK) return rc;
-  if (cache->q4.pages)
+  if (cache->q4.pages) {
+    if (!hstu::q4_rows_fit(a.p, a.heads, a.d)) return HSTU_ERR_INVALID_ARG;
     return hstu::status_of(hstu::launch_append_q4(cache->q4, a, reinterpret_cast<cudaStream_t>(stream)));
+  }
+  int grid;
+  if ((rc = unit_grid(a.p, width, hstu::kAppendThreads, &a.check_ctas, &grid)) != HSTU_OK) return rc;
   return hstu::status_of(hstu::launch_after(hstu::append_kernel, grid, hstu::kAppendThreads, 0,
                                             reinterpret_cast<cudaStream_t>(stream), a));
 }
@@ -985,10 +986,12 @@ int hstu_cache_read(const hstu_cache* cache, const hstu_paged_batch* batch, void
   a.heads = cache->heads;
   a.d = cache->d;
   a.status = cache->status;
-  int grid;
-  if ((rc = unit_grid(a.p, width, cache->q4.pages ? 15 : 0, &a.check_ctas, &grid)) != HSTU_OK) return rc;
-  if (cache->q4.pages)
+  if (cache->q4.pages) {
+    if (!hstu::q4_rows_fit(a.p, a.heads, a.d)) return HSTU_ERR_INVALID_ARG;
     return hstu::status_of(hstu::launch_read_q4(cache->q4, a, reinterpret_cast<cudaStream_t>(stream)));
+  }
+  int grid;
+  if ((rc = unit_grid(a.p, width, hstu::kAppendThreads, &a.check_ctas, &grid)) != HSTU_OK) return rc;
   return hstu::status_of(hstu::launch_after(hstu::read_kernel, grid, hstu::kAppendThreads, 0,
                                             reinterpret_cast<cudaStream_t>(stream), a));
 }

@@ -26,31 +26,31 @@
 namespace hstu {
 namespace {
 
-constexpr int kQ4Threads = 256;
+constexpr int kQ4Threads = 128;
+// Accesses in flight of the append (each three rows) and of the reading.
+constexpr int kQ4AppendIter = 2, kQ4ReadIter = 4;
 
-// Where a thread of the append and of the reading works: a group of 16
-// channels of one head of one token.  A warp takes consecutive tokens of one
-// head, whose codes are consecutive bytes.
-struct Q4Unit {
-  long long t;
-  int h, g;
+// How a warp of the append and of the reading works: a lane has 8 channels (a
+// word of codes) of one head, D / 8 neighbouring lanes a token, so that each
+// access of the warp is to whole rows one behind the other, and ITER such
+// accesses are in flight.  The first lanes look the warp's tokens up, a token
+// each, and hand out what they found.
+template <int D, int ITER>
+struct Q4Rows {
+  static constexpr int LANES = D / 8;         // of a token
+  static constexpr int TOKENS = 32 / LANES;   // of an access
+  static constexpr int ALL = TOKENS * ITER;   // of a warp
+  static_assert(ALL <= 32, "a lane a token");
 };
-template <int D>
-__device__ __forceinline__ Q4Unit q4_unit(unsigned block, int heads) {
-  constexpr int G = D / kQ4Group, TOKENS = 32 / G;
-  const long long w = ((long long)block * kQ4Threads + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const long long tb = w / heads;
-  return Q4Unit{tb * TOKENS + lane / G, (int)(w - tb * heads), lane % G};
-}
-template <int D>
+template <int D, int ITER>
 long long q4_blocks(long long rows, int heads) {
-  constexpr int TOKENS = 32 / (D / kQ4Group);
-  return ((rows + TOKENS - 1) / TOKENS * heads * 32 + kQ4Threads - 1) / kQ4Threads;
+  constexpr int ALL = Q4Rows<D, ITER>::ALL;
+  return ((rows + ALL - 1) / ALL * heads * 32 + kQ4Threads - 1) / kQ4Threads;
 }
 
 // The first CTAs check a sequence a thread: one that contradicts itself may
 // have no row.
+unsigned q4_check_ctas(const PagedView& p) { return ((unsigned)p.batch + kQ4Threads - 1) / kQ4Threads; }
 __device__ __forceinline__ bool q4_checks(const PagedView& p, unsigned check_ctas, unsigned* status) {
   if (blockIdx.x >= check_ctas) return false;
   const long long b = (long long)blockIdx.x * kQ4Threads + threadIdx.x;
@@ -59,152 +59,184 @@ __device__ __forceinline__ bool q4_checks(const PagedView& p, unsigned check_cta
   return true;
 }
 
-// Byte of tile row 0 of token slot `slot`, and its row there.
-__device__ __forceinline__ long long q4_tile(const Q4Pool& pool, int page_shift, long long slot, int h, int* r) {
-  const int in_page = (int)(slot & ((1 << page_shift) - 1));
-  *r = in_page & ((1 << pool.tile_shift) - 1);
-  return (slot >> page_shift) * pool.page_stride +
-         ((long long)h * pool.tiles + (in_page >> pool.tile_shift)) * pool.tile_bytes;
+// A token's place: its tile, its row there (-1: it has none, -2: its page is
+// out of range), and the position it is turned to.
+struct Q4Place {
+  long long tile;  // bytes
+  int row, turned_at;
+};
+__device__ __forceinline__ Q4Place q4_place(const PagedView& p, const Q4Pool& pool, long long t, int h) {
+  Q4Place x{0, -1, 0};
+  PagedSeq s;
+  if (t >= p.rows) return x;
+  const int b = paged_find(p, (int)t);
+  if (b < 0 || !paged_seq(p, b, &s)) return x;  // of no sequence, or of one that is reported
+  const int pos = s.kv - s.qn + ((int)t - s.q0);
+  const long long slot = paged_slot(p, b, pos);
+  x.turned_at = pos < s.hist ? pos : s.hist;  // a candidate stands right behind the history
+  x.row = -2;
+  if (slot < 0) return x;
+  const int in_page = (int)(slot & ((1 << p.page_shift) - 1));
+  x.row = in_page & ((1 << pool.tile_shift) - 1);
+  x.tile = (slot >> p.page_shift) * pool.page_stride +
+           ((long long)h * pool.tiles + (in_page >> pool.tile_shift)) * pool.tile_bytes;
+  return x;
+}
+__device__ __forceinline__ Q4Place q4_place_of(const Q4Place& mine, int lane) {
+  return Q4Place{__shfl_sync(0xffffffffu, mine.tile, lane), __shfl_sync(0xffffffffu, mine.row, lane),
+                 __shfl_sync(0xffffffffu, mine.turned_at, lane)};
 }
 
-// 8 channels c .. c + 7 of a head, x, rotated with its partner block y where
-// the channels turn in halves.  The products are rounded one by one, as a
-// plain form does: what is quantised then is the same number, not one beside
-// it across a border.
-__device__ __forceinline__ uint4 q4_turn(const uint4& x, const uint4& y, const float* tab, int c, int rot,
-                                         bool pairs) {
+__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// This lane's 8 channels x, of c .. c + 7 of the head, rotated; c < rot.  Where
+// the channels turn in halves its partner's are rot / 16 lanes away.  The
+// products are rounded one by one, as a plain form does: what is quantised then
+// is the same number, not one beside it across a border.  Whole-warp call.
+__device__ __forceinline__ uint4 q4_turn(const uint4& x, const float4 (&cs)[2], const float4 (&sn)[2], int c,
+                                         int rot, bool pairs) {
   F8 a = unpack8(x);
-  const int half = rot >> 1;
+  const float cc[8] = {cs[0].x, cs[0].y, cs[0].z, cs[0].w, cs[1].x, cs[1].y, cs[1].z, cs[1].w};
+  const float ss[8] = {sn[0].x, sn[0].y, sn[0].z, sn[0].w, sn[1].x, sn[1].y, sn[1].z, sn[1].w};
   if (pairs) {
-    const float4 cs = __ldg(reinterpret_cast<const float4*>(tab + (c >> 1)));
-    const float4 sn = __ldg(reinterpret_cast<const float4*>(tab + half + (c >> 1)));
-    const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float u = a.f[2 * i], v = a.f[2 * i + 1];
       a.f[2 * i] = __fsub_rn(__fmul_rn(u, cc[i]), __fmul_rn(v, ss[i]));
       a.f[2 * i + 1] = __fadd_rn(__fmul_rn(v, cc[i]), __fmul_rn(u, ss[i]));
     }
-  } else {
-    const bool first = c < half;
-    const float* at = tab + (first ? c : c - half);
-    const F8 b = unpack8(y);
+    return pack8(a);
+  }
+  const bool first = c < rot >> 1;
+  const int other = (threadIdx.x & 31) + (c >= rot ? 0 : first ? rot >> 4 : -(rot >> 4));
+  const uint4 y = make_uint4(__shfl_sync(0xffffffffu, x.x, other), __shfl_sync(0xffffffffu, x.y, other),
+                             __shfl_sync(0xffffffffu, x.z, other), __shfl_sync(0xffffffffu, x.w, other));
+  const F8 b = unpack8(y);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4 cs = __ldg(reinterpret_cast<const float4*>(at) + k);
-      const float4 sn = __ldg(reinterpret_cast<const float4*>(at + half) + k);
-      const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float s = first ? -ss[i] : ss[i];
-        a.f[4 * k + i] = __fadd_rn(__fmul_rn(a.f[4 * k + i], cc[i]), __fmul_rn(b.f[4 * k + i], s));
-      }
-    }
+  for (int i = 0; i < 8; i += 2) {
+    const float2 s = first ? make_float2(-ss[i], -ss[i + 1]) : make_float2(ss[i], ss[i + 1]);
+    const float2 r = __fadd2_rn(__fmul2_rn(make_float2(a.f[i], a.f[i + 1]), make_float2(cc[i], cc[i + 1])),
+                                __fmul2_rn(make_float2(b.f[i], b.f[i + 1]), s));
+    a.f[i] = r.x;
+    a.f[i + 1] = r.y;
   }
   return pack8(a);
 }
 
-__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
-
+// Bound by memory: 65,536 tokens of 4 heads of 64 with their queries, rotated,
+// are 153 MB.
 template <int D>
 __global__ void __launch_bounds__(kQ4Threads) append_q4_kernel(const AppendArgs a, const Q4Pool pool) {
   using T = Q4Tile<D>;
+  constexpr int ITER = kQ4AppendIter;
+  using R = Q4Rows<D, ITER>;
   after_previous_kernel();
   if (q4_checks(a.p, a.check_ctas, a.status)) return;
-  const Q4Unit u = q4_unit<D>(blockIdx.x - a.check_ctas, a.heads);
-  if (u.t >= a.p.rows) return;
-  const int t = (int)u.t, c0 = kQ4Group * u.g, c1 = c0 + 8;
-  const bool turn = a.table && c0 < a.rot;
-  const int half = a.rot >> 1;
-  const bool halves = turn && !a.pairs;
-  // the partners' blocks, where channels turn in halves
-  const int y0 = !halves ? c0 : c0 < half ? c0 + half : c0 - half;
-  const int y1 = !halves ? c1 : c1 < half ? c1 + half : c1 - half;
-  const long long at = (long long)u.h * D;
-  const uint16_t* kr = a.k + t * a.k_stride + at;
-  const uint16_t* vr = a.v + t * a.v_stride + at;
-  const int total = a.p.q_offsets[a.p.batch];
-  uint4 k0 = load16(kr + c0), k1 = load16(kr + c1), kp0{}, kp1{}, q0{}, q1{}, qp0{}, qp1{};
-  const uint4 v0 = load16(vr + c0), v1 = load16(vr + c1);
-  if (halves) {
-    kp0 = load16(kr + y0);
-    kp1 = load16(kr + y1);
-  }
-  if (a.q) {
-    const uint16_t* qr = a.q + t * a.q_stride + at;
-    q0 = load16(qr + c0);
-    q1 = load16(qr + c1);
-    if (halves) {
-      qp0 = load16(qr + y0);
-      qp1 = load16(qr + y1);
+  const int lane = threadIdx.x & 31;
+  const long long w = ((long long)(blockIdx.x - a.check_ctas) * kQ4Threads + threadIdx.x) >> 5;
+  const long long t0 = w / a.heads * R::ALL;
+  if (t0 >= a.p.rows) return;  // the same for the warp
+  const int h = (int)(w % a.heads);
+  const int c = 8 * (lane % R::LANES);  // the lane's channels of the head
+  const long long at = (long long)h * D + c;
+  uint4 k[ITER], v[ITER], q[ITER];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const long long t = t0 + i * R::TOKENS + lane / R::LANES;
+    k[i] = v[i] = q[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (t < a.p.rows) {
+      k[i] = load16(a.k + t * a.k_stride + at);
+      v[i] = load16(a.v + t * a.v_stride + at);
+      if (a.q) q[i] = load16(a.q + t * a.q_stride + at);
     }
   }
-  if (t >= total) return;  // a row behind the last sequence
-  PagedSeq s;
-  const int b = paged_find(a.p, t);
-  if (b < 0 || !paged_seq(a.p, b, &s)) return;  // before the first sequence, or of one that is reported
-  const int pos = s.kv - s.qn + (t - s.q0);
-  const long long slot = paged_slot(a.p, b, pos);
-  const int turned_at = pos < s.hist ? pos : s.hist;  // a candidate stands right behind the history
-  if (slot < 0 || (a.table && turned_at >= a.positions)) {
-    atomicOr(a.status, kStatusBadPaged);
-    return;
-  }
-  if (turn) {
-    const float* tab = a.table + (long long)turned_at * a.rot;
-    k0 = q4_turn(k0, kp0, tab, c0, a.rot, a.pairs);
-    k1 = q4_turn(k1, kp1, tab, c1, a.rot, a.pairs);
-    if (a.q) {
-      q0 = q4_turn(q0, qp0, tab, c0, a.rot, a.pairs);
-      q1 = q4_turn(q1, qp1, tab, c1, a.rot, a.pairs);
+  Q4Place mine{0, -1, 0};
+  if (lane < R::ALL) {
+    mine = q4_place(a.p, pool, t0 + lane, h);
+    if (mine.row == -2 || (mine.row >= 0 && a.table && mine.turned_at >= a.positions)) {
+      atomicOr(a.status, kStatusBadPaged);  // dropped
+      mine.row = -1;
     }
   }
-  int r;
-  uint8_t* tile = pool.pages + q4_tile(pool, a.p.page_shift, slot, u.h, &r);
-  uint32_t j;
-  *reinterpret_cast<uint2*>(tile + T::codes(pool.tile_shift, 0, r) + 8 * u.g) = q4_quantise(k0, k1, &j);
-  tile[T::scales(pool.tile_shift, 0, r) + u.g] = (uint8_t)j;
-  *reinterpret_cast<uint2*>(tile + T::codes(pool.tile_shift, 1, r) + 8 * u.g) = q4_quantise(v0, v1, &j);
-  tile[T::scales(pool.tile_shift, 1, r) + u.g] = (uint8_t)j;
-  if (a.q) {
-    uint4* qo = reinterpret_cast<uint4*>(a.q_out + (long long)t * a.heads * D + at + c0);
-    qo[0] = q0;
-    qo[1] = q1;
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int token = i * R::TOKENS + lane / R::LANES;
+    const Q4Place x = q4_place_of(mine, token);
+    if (a.table) {
+      float4 cs[2], sn[2];
+      cs[0] = cs[1] = sn[0] = sn[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int half = a.rot >> 1;
+      if (x.row >= 0 && c < a.rot) {
+        // pairs of channels: 4 angles; halves: 8
+        const float* tab = a.table + (long long)x.turned_at * a.rot + (a.pairs ? c >> 1 : c < half ? c : c - half);
+        cs[0] = __ldg(reinterpret_cast<const float4*>(tab));
+        sn[0] = __ldg(reinterpret_cast<const float4*>(tab + half));
+        if (!a.pairs) {
+          cs[1] = __ldg(reinterpret_cast<const float4*>(tab) + 1);
+          sn[1] = __ldg(reinterpret_cast<const float4*>(tab + half) + 1);
+        }
+      }
+      const uint4 kt = q4_turn(k[i], cs, sn, c, a.rot, a.pairs);
+      if (c < a.rot) k[i] = kt;
+      if (a.q) {
+        const uint4 qt = q4_turn(q[i], cs, sn, c, a.rot, a.pairs);
+        if (c < a.rot) q[i] = qt;
+      }
+    }
+    uint32_t kj, vj;
+    const uint32_t kc = q4_quantise(k[i], &kj), vc = q4_quantise(v[i], &vj);
+    if (x.row < 0) continue;  // behind the whole-warp calls
+    uint8_t* tile = pool.pages + x.tile;
+    *reinterpret_cast<uint32_t*>(tile + T::codes(pool.tile_shift, 0, x.row) + c / 2) = kc;
+    *reinterpret_cast<uint32_t*>(tile + T::codes(pool.tile_shift, 1, x.row) + c / 2) = vc;
+    if (lane & 1)
+      tile[T::scales(pool.tile_shift, 1, x.row) + c / kQ4Group] = (uint8_t)vj;
+    else
+      tile[T::scales(pool.tile_shift, 0, x.row) + c / kQ4Group] = (uint8_t)kj;
+    if (a.q) *reinterpret_cast<uint4*>(a.q_out + (t0 + token) * a.heads * D + at) = q[i];
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kQ4Threads) read_q4_kernel(const ReadArgs a, const Q4Pool pool) {
   using T = Q4Tile<D>;
+  constexpr int ITER = kQ4ReadIter;
+  using R = Q4Rows<D, ITER>;
   after_previous_kernel();
   if (q4_checks(a.p, a.check_ctas, a.status)) return;
-  const Q4Unit u = q4_unit<D>(blockIdx.x - a.check_ctas, a.heads);
-  if (u.t >= a.p.rows) return;
-  const int t = (int)u.t;
-  PagedSeq s;
-  const int b = paged_find(a.p, t);
-  if (b < 0 || !paged_seq(a.p, b, &s)) return;
-  const long long slot = paged_slot(a.p, b, s.kv - s.qn + (t - s.q0));
-  uint2 kc{}, vc{};
-  uint32_t kj = 0, vj = 0;
-  if (slot < 0) {
-    atomicOr(a.status, kStatusBadPaged);  // read as zeros
-  } else {
-    int r;
-    const uint8_t* tile = pool.pages + q4_tile(pool, a.p.page_shift, slot, u.h, &r);
-    kc = *reinterpret_cast<const uint2*>(tile + T::codes(pool.tile_shift, 0, r) + 8 * u.g);
-    vc = *reinterpret_cast<const uint2*>(tile + T::codes(pool.tile_shift, 1, r) + 8 * u.g);
-    kj = tile[T::scales(pool.tile_shift, 0, r) + u.g];
-    vj = tile[T::scales(pool.tile_shift, 1, r) + u.g];
+  const int lane = threadIdx.x & 31;
+  const long long w = ((long long)(blockIdx.x - a.check_ctas) * kQ4Threads + threadIdx.x) >> 5;
+  const long long t0 = w / a.heads * R::ALL;
+  if (t0 >= a.p.rows) return;  // the same for the warp
+  const int h = (int)(w % a.heads);
+  const int c = 8 * (lane % R::LANES);
+  Q4Place mine{0, -1, 0};
+  if (lane < R::ALL) {
+    mine = q4_place(a.p, pool, t0 + lane, h);
+    if (mine.row == -2) atomicOr(a.status, kStatusBadPaged);  // read as zeros
   }
-  const Q4Scale ks = q4_scale(kj), vs = q4_scale(vj);
-  const long long at = (long long)u.h * D + kQ4Group * u.g;
-  uint4* ko = reinterpret_cast<uint4*>(a.k + t * a.k_stride + at);
-  uint4* vo = reinterpret_cast<uint4*>(a.v + t * a.v_stride + at);
-  ko[0] = q4_word(kc.x, ks);
-  ko[1] = q4_word(kc.y, ks);
-  vo[0] = q4_word(vc.x, vs);
-  vo[1] = q4_word(vc.y, vs);
+  uint32_t kc[ITER], vc[ITER], kj[ITER], vj[ITER];
+  bool live[ITER];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const Q4Place x = q4_place_of(mine, i * R::TOKENS + lane / R::LANES);
+    live[i] = x.row != -1;
+    kc[i] = vc[i] = kj[i] = vj[i] = 0;
+    if (x.row >= 0) {
+      const uint8_t* tile = pool.pages + x.tile;
+      kc[i] = *reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 0, x.row) + c / 2);
+      vc[i] = *reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 1, x.row) + c / 2);
+      kj[i] = tile[T::scales(pool.tile_shift, 0, x.row) + c / kQ4Group];
+      vj[i] = tile[T::scales(pool.tile_shift, 1, x.row) + c / kQ4Group];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    if (!live[i]) continue;
+    const long long t = t0 + i * R::TOKENS + lane / R::LANES, at = (long long)h * D + c;
+    *reinterpret_cast<uint4*>(a.k + t * a.k_stride + at) = q4_word(kc[i], q4_scale(kj[i]));
+    *reinterpret_cast<uint4*>(a.v + t * a.v_stride + at) = q4_word(vc[i], q4_scale(vj[i]));
+  }
 }
 
 // ------------------------------------------------ attention of a few tokens
@@ -731,18 +763,29 @@ cudaError_t launch_step_q4_d(const Q4Pool& pool, long long most, bool clusters, 
 }
 
 template <int D>
-cudaError_t launch_append_q4_d(const Q4Pool& pool, const AppendArgs& a, cudaStream_t stream) {
-  const int grid = (int)(a.check_ctas + q4_blocks<D>(a.p.rows, a.heads));
+cudaError_t launch_append_q4_d(const Q4Pool& pool, AppendArgs a, cudaStream_t stream) {
+  a.check_ctas = q4_check_ctas(a.p);
+  const int grid = (int)(a.check_ctas + q4_blocks<D, kQ4AppendIter>(a.p.rows, a.heads));
   return launch_after(append_q4_kernel<D>, grid, kQ4Threads, 0, stream, a, pool);
 }
 
 template <int D>
-cudaError_t launch_read_q4_d(const Q4Pool& pool, const ReadArgs& a, cudaStream_t stream) {
-  const int grid = (int)(a.check_ctas + q4_blocks<D>(a.p.rows, a.heads));
+cudaError_t launch_read_q4_d(const Q4Pool& pool, ReadArgs a, cudaStream_t stream) {
+  a.check_ctas = q4_check_ctas(a.p);
+  const int grid = (int)(a.check_ctas + q4_blocks<D, kQ4ReadIter>(a.p.rows, a.heads));
   return launch_after(read_q4_kernel<D>, grid, kQ4Threads, 0, stream, a, pool);
 }
 
 }  // namespace
+
+bool q4_rows_fit(const PagedView& p, int heads, int d) {
+  // the append's CTAs, which are more than the reading's
+  const long long blocks = d == 32   ? q4_blocks<32, kQ4AppendIter>(p.rows, heads)
+                           : d == 64 ? q4_blocks<64, kQ4AppendIter>(p.rows, heads)
+                                     : q4_blocks<128, kQ4AppendIter>(p.rows, heads);
+  static_assert(kQ4AppendIter <= kQ4ReadIter, "more CTAs");
+  return q4_check_ctas(p) + blocks <= 0x7fffffffLL;
+}
 
 cudaError_t launch_append_q4(const Q4Pool& pool, const AppendArgs& a, cudaStream_t stream) {
   switch (a.d) {

@@ -251,7 +251,8 @@ struct ReadArgs {
   unsigned check_ctas;
   unsigned* status;
 };
-// a.check_ctas CTAs check the sequences; the host has checked the grid.
+// Whether the launches below have a grid for the batch.
+bool q4_rows_fit(const PagedView& p, int heads, int d);
 cudaError_t launch_append_q4(const Q4Pool& pool, const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_read_q4(const Q4Pool& pool, const ReadArgs& a, cudaStream_t stream);
 // `most`: CTAs with work, at most; clusters: a cluster of CTAs an item instead.

@@ -89,8 +89,6 @@ __device__ __forceinline__ uint4 q4_word(uint32_t w, const Q4Scale& s) {
 }
 
 // ------------------------------------------------------------------ to codes
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
 // NaN as 0, infinities as the largest finite number.
 __device__ __forceinline__ uint32_t q4_finite(uint32_t x) {
   uint32_t r = 0;
@@ -106,21 +104,23 @@ __device__ __forceinline__ uint32_t q4_finite(uint32_t x) {
   return r;
 }
 
-// A group's codes (two words of 8 channels) and its scale's byte.
-__device__ __forceinline__ uint2 q4_quantise(uint4 x0, uint4 x1, uint32_t* scale) {
-  uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-  uint32_t m = 0;
+// The codes of this lane's half of a group, 8 channels, and the group's scale's
+// byte; the other half is the next lane's (or the one's before).  Whole-warp
+// call.
+__device__ __forceinline__ uint32_t q4_quantise(const uint4& half, uint32_t* scale) {
+  uint32_t x[4] = {half.x, half.y, half.z, half.w};
+  auto largest = [&x] {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_u16x2(m, x[i] & 0x7fff7fffu);
-  m = max(m & 0xffffu, m >> 16);
-  if (m >= 0x7f80u) {  // something is not finite
-    m = 0;
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, x[i] & 0x7fff7fffu);
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m & 0xffffu, m >> 16);
+  };
+  uint32_t m = largest();
+  if (__any_sync(0xffffffffu, m >= 0x7f80u)) {  // something is not finite
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = q4_finite(x[i]);
-      m = max_u16x2(m, x[i] & 0x7fff7fffu);
-    }
-    m = max(m & 0xffffu, m >> 16);
+    for (int i = 0; i < 4; ++i) x[i] = q4_finite(x[i]);
+    m = largest();
   }
   // max / 7, less 2^-16 of it, rounded up to four significant bits
   const float seventh = __uint_as_float(m << 16) * (float)((1.0 - 0x1p-16) / 7.0);
@@ -131,21 +131,20 @@ __device__ __forceinline__ uint2 q4_quantise(uint4 x0, uint4 x1, uint32_t* scale
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   inv *= 1.0f + 0x1p-16f;
-  const float most = up > 255 ? 7.0f * s : __uint_as_float(0x7f7fffffu);  // past the largest scale: saturated
-  uint32_t w[2] = {0u, 0u};
+  uint32_t w = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     float a = __uint_as_float(x[i] << 16), b = __uint_as_float(x[i] & 0xffff0000u);
-    if (up > 255) {
-      a = fminf(fmaxf(a, -most), most);
-      b = fminf(fmaxf(b, -most), most);
+    if (up > 255) {  // past the largest scale: saturated
+      a = fminf(fmaxf(a, -7.0f * s), 7.0f * s);
+      b = fminf(fmaxf(b, -7.0f * s), 7.0f * s);
     }
     // the integer in the low bits of 1.5 2^23 + x / s
     const float2 y = __ffma2_rn(make_float2(a, b), make_float2(inv, inv), make_float2(12582912.f, 12582912.f));
     const uint32_t both = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x5410);
-    w[i >> 2] |= (both & 0x000f000fu) << (4 * (i & 3));
+    w |= (both & 0x000f000fu) << (4 * i);
   }
-  return make_uint2(w[0], w[1]);
+  return w;
 }
 
 }  // namespace

@@ -215,6 +215,32 @@ def test_append_from_a_fused_projection_and_in_place():
     q2 = torch.zeros_like(q_out)
     binding.hstu_cache_append(s.cache, s.batch, proj[:, 3], proj[:, 2], q=proj[:, 1], q_out=q2, rotary=table)
     assert torch.equal(q_out, q2) and torch.equal(first, s.pages)
+    q3 = s.q.cuda()
+    binding.hstu_cache_append(s.cache, s.batch, s.k.cuda(), s.v.cuda(), q=q3, q_out=q3, rotary=table)
+    assert torch.equal(q3[:s.total], q_out[:s.total]) and torch.equal(first, s.pages)
+    assert torch.equal(q3[s.total:].cpu(), s.q[s.total:])  # a padded batch's rows stay
+
+
+def test_every_sequence_is_checked():
+    # more sequences than a CTA of the check has threads, wrong ones among them
+    n = 700
+    s = Q4([3] * n, [1] * n, 16, 1, 32, seed=8)
+    good = s.read()
+    binding.hstu_cache_append(s.cache, s.batch, s.k.cuda(), s.v.cuda())
+    assert binding.hstu_last_status() == (binding.HSTU_OK, 0)
+    for b in (0, 127, 128, 255, 256, 511, 699):
+        s.pages.copy_(torch.from_numpy(s.bytes))
+        s.dev["kv_lens"][b] = -1
+        k, v = s.read()
+        assert binding.hstu_last_status()[0] == binding.HSTU_ERR_INVALID_ARG
+        assert (k[b] == 7).all() and torch.equal(k[b + 1:], good[0][b + 1:]) and torch.equal(v[:b], good[1][:b])
+        binding.hstu_cache_append(s.cache, s.batch, s.k.cuda(), s.v.cuda())
+        assert binding.hstu_last_status()[0] == binding.HSTU_ERR_INVALID_ARG
+        s.dev["kv_lens"][b] = 4
+        held = s.held()[0]
+        for t, pg, slot, _, _ in s.slots():
+            ref = s.kp[pg, slot] if t == b else layer.q4_held(s.k[t])
+            assert np.array_equal(held[pg, slot], layer.f64(ref))
 
 
 # ------------------------------------------------------------------ attention
