@@ -958,7 +958,7 @@ int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, co
   a.status = cache->status;
   if (cache->q4.pages) {
     if (!hstu::q4_rows_fit(a.p, a.heads, a.d)) return HSTU_ERR_INVALID_ARG;
-    return hstu::status_of(hstu::launch_append_q4(cache->q4, a, reinterpret_cast<cudaStream_t>(stream)));
+    return hstu::status_of(hstu::launch_append_q4(cache->q4, a, cache->sms, reinterpret_cast<cudaStream_t>(stream)));
   }
   int grid;
   if ((rc = unit_grid(a.p, width, hstu::kAppendThreads, &a.check_ctas, &grid)) != HSTU_OK) return rc;
@@ -988,7 +988,7 @@ int hstu_cache_read(const hstu_cache* cache, const hstu_paged_batch* batch, void
   a.status = cache->status;
   if (cache->q4.pages) {
     if (!hstu::q4_rows_fit(a.p, a.heads, a.d)) return HSTU_ERR_INVALID_ARG;
-    return hstu::status_of(hstu::launch_read_q4(cache->q4, a, reinterpret_cast<cudaStream_t>(stream)));
+    return hstu::status_of(hstu::launch_read_q4(cache->q4, a, cache->sms, reinterpret_cast<cudaStream_t>(stream)));
   }
   int grid;
   if ((rc = unit_grid(a.p, width, hstu::kAppendThreads, &a.check_ctas, &grid)) != HSTU_OK) return rc;

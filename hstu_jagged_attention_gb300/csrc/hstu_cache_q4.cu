@@ -26,9 +26,16 @@
 namespace hstu {
 namespace {
 
-constexpr int kQ4Threads = 128;
-// Accesses in flight of the append (each three rows) and of the reading.
-constexpr int kQ4AppendIter = 2, kQ4ReadIter = 4;
+constexpr int kQ4Threads = 256;
+// Accesses in flight, each to whole rows: of the append, which has three rows,
+// the next head's, and the rotation's angles in registers, and of the reading.
+// 65,536 tokens of 4 heads of 64: append 33.2 us with one, 34.1 with two;
+// reading 19.4 with one, 17.8 with two, 18.6 with four.
+constexpr int kQ4AppendIter = 1, kQ4ReadIter = 2;
+// Warps an SM below which a warp takes one head only: 6,400 tokens of 4 heads of
+// 128 are appended in 6.8 us with 16, 9.3 with 24 (the heads are not looped over
+// then), and 65,536 in 33.2 with the loop, 59 without.
+constexpr int kQ4Warps = 16;
 
 // How a warp of the append and of the reading works: a lane has 8 channels (a
 // word of codes) of one head, D / 8 neighbouring lanes a token, so that each
@@ -42,10 +49,20 @@ struct Q4Rows {
   static constexpr int ALL = TOKENS * ITER;   // of a warp
   static_assert(ALL <= 32, "a lane a token");
 };
+// Warps that take all the tokens' heads `step` at a time, and the CTAs of them.
 template <int D, int ITER>
-long long q4_blocks(long long rows, int heads) {
+long long q4_blocks(long long rows, int heads, int step) {
   constexpr int ALL = Q4Rows<D, ITER>::ALL;
-  return ((rows + ALL - 1) / ALL * heads * 32 + kQ4Threads - 1) / kQ4Threads;
+  return ((rows + ALL - 1) / ALL * ((heads + step - 1) / step) * 32 + kQ4Threads - 1) / kQ4Threads;
+}
+// A warp looks its tokens up once for all the heads it takes, and has the next
+// head's rows in flight while it works on one's; but it takes only as many as
+// leave kQ4Warps an SM.
+template <int D, int ITER>
+int q4_head_step(long long rows, int heads, int sms) {
+  constexpr int ALL = Q4Rows<D, ITER>::ALL;
+  const long long warps = (rows + ALL - 1) / ALL * heads;
+  return (int)std::max<long long>(1, std::min<long long>(heads, warps / ((long long)kQ4Warps * sms)));
 }
 
 // The first CTAs check a sequence a thread: one that contradicts itself may
@@ -59,13 +76,13 @@ __device__ __forceinline__ bool q4_checks(const PagedView& p, unsigned check_cta
   return true;
 }
 
-// A token's place: its tile, its row there (-1: it has none, -2: its page is
+// A token's place: its tile in the first head, its row there (-1: it has none, -2: its page is
 // out of range), and the position it is turned to.
 struct Q4Place {
   long long tile;  // bytes
   int row, turned_at;
 };
-__device__ __forceinline__ Q4Place q4_place(const PagedView& p, const Q4Pool& pool, long long t, int h) {
+__device__ __forceinline__ Q4Place q4_place(const PagedView& p, const Q4Pool& pool, long long t) {
   Q4Place x{0, -1, 0};
   PagedSeq s;
   if (t >= p.rows) return x;
@@ -78,8 +95,7 @@ __device__ __forceinline__ Q4Place q4_place(const PagedView& p, const Q4Pool& po
   if (slot < 0) return x;
   const int in_page = (int)(slot & ((1 << p.page_shift) - 1));
   x.row = in_page & ((1 << pool.tile_shift) - 1);
-  x.tile = (slot >> p.page_shift) * pool.page_stride +
-           ((long long)h * pool.tiles + (in_page >> pool.tile_shift)) * pool.tile_bytes;
+  x.tile = (slot >> p.page_shift) * pool.page_stride + (long long)(in_page >> pool.tile_shift) * pool.tile_bytes;
   return x;
 }
 __device__ __forceinline__ Q4Place q4_place_of(const Q4Place& mine, int lane) {
@@ -89,44 +105,47 @@ __device__ __forceinline__ Q4Place q4_place_of(const Q4Place& mine, int lane) {
 
 __device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// This lane's 8 channels x, of c .. c + 7 of the head, rotated; c < rot.  Where
-// the channels turn in halves its partner's are rot / 16 lanes away.  The
+// The angles of a lane's 8 channels: cosines, and the sines that its partner's
+// channels are multiplied with (pairs of channels: 4 angles, halves: 8).
+struct Q4Angles {
+  float cs[8], sn[8];
+};
+// This lane's channels x, of c .. c + 7 of the head, rotated if c < rot.  Where
+// the channels turn in halves the partner's are rot / 16 lanes away.  The
 // products are rounded one by one, as a plain form does: what is quantised then
 // is the same number, not one beside it across a border.  Whole-warp call.
-__device__ __forceinline__ uint4 q4_turn(const uint4& x, const float4 (&cs)[2], const float4 (&sn)[2], int c,
-                                         int rot, bool pairs) {
+__device__ __forceinline__ uint4 q4_turn(const uint4& x, const Q4Angles& g, int c, int rot, bool pairs) {
   F8 a = unpack8(x);
-  const float cc[8] = {cs[0].x, cs[0].y, cs[0].z, cs[0].w, cs[1].x, cs[1].y, cs[1].z, cs[1].w};
-  const float ss[8] = {sn[0].x, sn[0].y, sn[0].z, sn[0].w, sn[1].x, sn[1].y, sn[1].z, sn[1].w};
   if (pairs) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float u = a.f[2 * i], v = a.f[2 * i + 1];
-      a.f[2 * i] = __fsub_rn(__fmul_rn(u, cc[i]), __fmul_rn(v, ss[i]));
-      a.f[2 * i + 1] = __fadd_rn(__fmul_rn(v, cc[i]), __fmul_rn(u, ss[i]));
+      a.f[2 * i] = __fsub_rn(__fmul_rn(u, g.cs[i]), __fmul_rn(v, g.sn[i]));
+      a.f[2 * i + 1] = __fadd_rn(__fmul_rn(v, g.cs[i]), __fmul_rn(u, g.sn[i]));
     }
-    return pack8(a);
-  }
-  const bool first = c < rot >> 1;
-  const int other = (threadIdx.x & 31) + (c >= rot ? 0 : first ? rot >> 4 : -(rot >> 4));
-  const uint4 y = make_uint4(__shfl_sync(0xffffffffu, x.x, other), __shfl_sync(0xffffffffu, x.y, other),
-                             __shfl_sync(0xffffffffu, x.z, other), __shfl_sync(0xffffffffu, x.w, other));
-  const F8 b = unpack8(y);
+  } else {
+    const int other = (threadIdx.x & 31) + (c >= rot ? 0 : c < rot >> 1 ? rot >> 4 : -(rot >> 4));
+    const uint4 y = make_uint4(__shfl_sync(0xffffffffu, x.x, other), __shfl_sync(0xffffffffu, x.y, other),
+                               __shfl_sync(0xffffffffu, x.z, other), __shfl_sync(0xffffffffu, x.w, other));
+    const F8 b = unpack8(y);
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 s = first ? make_float2(-ss[i], -ss[i + 1]) : make_float2(ss[i], ss[i + 1]);
-    const float2 r = __fadd2_rn(__fmul2_rn(make_float2(a.f[i], a.f[i + 1]), make_float2(cc[i], cc[i + 1])),
-                                __fmul2_rn(make_float2(b.f[i], b.f[i + 1]), s));
-    a.f[i] = r.x;
-    a.f[i + 1] = r.y;
+    for (int i = 0; i < 8; i += 2) {
+      const float2 r =
+          __fadd2_rn(__fmul2_rn(make_float2(a.f[i], a.f[i + 1]), make_float2(g.cs[i], g.cs[i + 1])),
+                     __fmul2_rn(make_float2(b.f[i], b.f[i + 1]), make_float2(g.sn[i], g.sn[i + 1])));
+      a.f[i] = r.x;
+      a.f[i + 1] = r.y;
+    }
   }
-  return pack8(a);
+  return c < rot ? pack8(a) : x;
 }
 
-// Bound by memory: 65,536 tokens of 4 heads of 64 with their queries, rotated,
-// are 153 MB.
+// 65,536 tokens of 4 heads of 64 with their queries, rotated, take 33.2 us (153
+// MB, 4.6 TB/s): about 230 instructions for 8 channels of k, v and q, half of
+// them on the integer pipe at half rate, weigh as much as the memory.
 template <int D>
-__global__ void __launch_bounds__(kQ4Threads) append_q4_kernel(const AppendArgs a, const Q4Pool pool) {
+__global__ void __launch_bounds__(kQ4Threads)
+    append_q4_kernel(const AppendArgs a, const Q4Pool pool, const int head_step) {
   using T = Q4Tile<D>;
   constexpr int ITER = kQ4AppendIter;
   using R = Q4Rows<D, ITER>;
@@ -134,71 +153,99 @@ __global__ void __launch_bounds__(kQ4Threads) append_q4_kernel(const AppendArgs 
   if (q4_checks(a.p, a.check_ctas, a.status)) return;
   const int lane = threadIdx.x & 31;
   const long long w = ((long long)(blockIdx.x - a.check_ctas) * kQ4Threads + threadIdx.x) >> 5;
-  const long long t0 = w / a.heads * R::ALL;
+  const int parts = (a.heads + head_step - 1) / head_step;
+  const long long t0 = w / parts * R::ALL;
   if (t0 >= a.p.rows) return;  // the same for the warp
-  const int h = (int)(w % a.heads);
-  const int c = 8 * (lane % R::LANES);  // the lane's channels of the head
-  const long long at = (long long)h * D + c;
-  uint4 k[ITER], v[ITER], q[ITER];
+  int h = (int)(w % parts) * head_step;
+  const int h1 = h + head_step < a.heads ? h + head_step : a.heads;
+  const int c = 8 * (lane % R::LANES);  // the lane's channels of a head
+  const long long mine_t = t0 + lane / R::LANES;
+  struct Rows {
+    uint4 k[ITER], v[ITER], q[ITER];
+  };
+  auto load = [&](Rows& x, int head) {
+    const long long at = (long long)head * D + c;
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    const long long t = t0 + i * R::TOKENS + lane / R::LANES;
-    k[i] = v[i] = q[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (t < a.p.rows) {
-      k[i] = load16(a.k + t * a.k_stride + at);
-      v[i] = load16(a.v + t * a.v_stride + at);
-      if (a.q) q[i] = load16(a.q + t * a.q_stride + at);
+    for (int i = 0; i < ITER; ++i) {
+      const long long t = mine_t + i * R::TOKENS;
+      x.k[i] = x.v[i] = x.q[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (t < a.p.rows) {
+        x.k[i] = load16(a.k + t * a.k_stride + at);
+        x.v[i] = load16(a.v + t * a.v_stride + at);
+        if (a.q) x.q[i] = load16(a.q + t * a.q_stride + at);
+      }
     }
-  }
-  Q4Place mine{0, -1, 0};
+  };
+  Rows next;
+  load(next, h);
+  Q4Place mine{0, -1, 0}, place[ITER];
   if (lane < R::ALL) {
-    mine = q4_place(a.p, pool, t0 + lane, h);
+    mine = q4_place(a.p, pool, t0 + lane);
     if (mine.row == -2 || (mine.row >= 0 && a.table && mine.turned_at >= a.positions)) {
       atomicOr(a.status, kStatusBadPaged);  // dropped
       mine.row = -1;
     }
   }
+  Q4Angles angles[ITER];
+  const int half = a.rot >> 1;
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
-    const int token = i * R::TOKENS + lane / R::LANES;
-    const Q4Place x = q4_place_of(mine, token);
-    if (a.table) {
-      float4 cs[2], sn[2];
-      cs[0] = cs[1] = sn[0] = sn[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int half = a.rot >> 1;
-      if (x.row >= 0 && c < a.rot) {
-        // pairs of channels: 4 angles; halves: 8
-        const float* tab = a.table + (long long)x.turned_at * a.rot + (a.pairs ? c >> 1 : c < half ? c : c - half);
-        cs[0] = __ldg(reinterpret_cast<const float4*>(tab));
-        sn[0] = __ldg(reinterpret_cast<const float4*>(tab + half));
-        if (!a.pairs) {
-          cs[1] = __ldg(reinterpret_cast<const float4*>(tab) + 1);
-          sn[1] = __ldg(reinterpret_cast<const float4*>(tab + half) + 1);
-        }
-      }
-      const uint4 kt = q4_turn(k[i], cs, sn, c, a.rot, a.pairs);
-      if (c < a.rot) k[i] = kt;
-      if (a.q) {
-        const uint4 qt = q4_turn(q[i], cs, sn, c, a.rot, a.pairs);
-        if (c < a.rot) q[i] = qt;
+    place[i] = q4_place_of(mine, i * R::TOKENS + lane / R::LANES);
+    float4 cs[2], sn[2];
+    cs[0] = cs[1] = sn[0] = sn[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.table && place[i].row >= 0 && c < a.rot) {
+      const float* tab =
+          a.table + (long long)place[i].turned_at * a.rot + (a.pairs ? c >> 1 : c < half ? c : c - half);
+      cs[0] = __ldg(reinterpret_cast<const float4*>(tab));
+      sn[0] = __ldg(reinterpret_cast<const float4*>(tab + half));
+      if (!a.pairs) {
+        cs[1] = __ldg(reinterpret_cast<const float4*>(tab) + 1);
+        sn[1] = __ldg(reinterpret_cast<const float4*>(tab + half) + 1);
       }
     }
-    uint32_t kj, vj;
-    const uint32_t kc = q4_quantise(k[i], &kj), vc = q4_quantise(v[i], &vj);
-    if (x.row < 0) continue;  // behind the whole-warp calls
-    uint8_t* tile = pool.pages + x.tile;
-    *reinterpret_cast<uint32_t*>(tile + T::codes(pool.tile_shift, 0, x.row) + c / 2) = kc;
-    *reinterpret_cast<uint32_t*>(tile + T::codes(pool.tile_shift, 1, x.row) + c / 2) = vc;
-    if (lane & 1)
-      tile[T::scales(pool.tile_shift, 1, x.row) + c / kQ4Group] = (uint8_t)vj;
-    else
-      tile[T::scales(pool.tile_shift, 0, x.row) + c / kQ4Group] = (uint8_t)kj;
-    if (a.q) *reinterpret_cast<uint4*>(a.q_out + (t0 + token) * a.heads * D + at) = q[i];
+    const float sign = !a.pairs && c < half ? -1.f : 1.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float cc[4] = {cs[k].x, cs[k].y, cs[k].z, cs[k].w}, ss[4] = {sn[k].x, sn[k].y, sn[k].z, sn[k].w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        angles[i].cs[4 * k + m] = cc[m];
+        angles[i].sn[4 * k + m] = sign * ss[m];
+      }
+    }
+  }
+#pragma unroll 1
+  for (; h < h1; ++h) {
+    Rows x = next;
+    if (h + 1 < h1) load(next, h + 1);
+    const long long head = (long long)h * pool.tiles * pool.tile_bytes;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      if (a.table) {
+        x.k[i] = q4_turn(x.k[i], angles[i], c, a.rot, a.pairs);
+        if (a.q) x.q[i] = q4_turn(x.q[i], angles[i], c, a.rot, a.pairs);
+      }
+      uint32_t kj, vj;
+      const uint32_t kc = q4_quantise(x.k[i], &kj), vc = q4_quantise(x.v[i], &vj);
+      const int row = place[i].row;
+      if (row >= 0) {
+        uint8_t* tile = pool.pages + place[i].tile + head;
+        *reinterpret_cast<uint32_t*>(tile + T::codes(pool.tile_shift, 0, row) + c / 2) = kc;
+        *reinterpret_cast<uint32_t*>(tile + T::codes(pool.tile_shift, 1, row) + c / 2) = vc;
+        if (lane & 1)
+          tile[T::scales(pool.tile_shift, 1, row) + c / kQ4Group] = (uint8_t)vj;
+        else
+          tile[T::scales(pool.tile_shift, 0, row) + c / kQ4Group] = (uint8_t)kj;
+        if (a.q)
+          *reinterpret_cast<uint4*>(a.q_out + ((mine_t + i * R::TOKENS) * a.heads + h) * D + c) = x.q[i];
+      }
+    }
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kQ4Threads) read_q4_kernel(const ReadArgs a, const Q4Pool pool) {
+__global__ void __launch_bounds__(kQ4Threads)
+    read_q4_kernel(const ReadArgs a, const Q4Pool pool, const int head_step) {
   using T = Q4Tile<D>;
   constexpr int ITER = kQ4ReadIter;
   using R = Q4Rows<D, ITER>;
@@ -206,36 +253,50 @@ __global__ void __launch_bounds__(kQ4Threads) read_q4_kernel(const ReadArgs a, c
   if (q4_checks(a.p, a.check_ctas, a.status)) return;
   const int lane = threadIdx.x & 31;
   const long long w = ((long long)(blockIdx.x - a.check_ctas) * kQ4Threads + threadIdx.x) >> 5;
-  const long long t0 = w / a.heads * R::ALL;
+  const int parts = (a.heads + head_step - 1) / head_step;
+  const long long t0 = w / parts * R::ALL;
   if (t0 >= a.p.rows) return;  // the same for the warp
-  const int h = (int)(w % a.heads);
+  int h = (int)(w % parts) * head_step;
+  const int h1 = h + head_step < a.heads ? h + head_step : a.heads;
   const int c = 8 * (lane % R::LANES);
-  Q4Place mine{0, -1, 0};
+  Q4Place mine{0, -1, 0}, place[ITER];
   if (lane < R::ALL) {
-    mine = q4_place(a.p, pool, t0 + lane, h);
+    mine = q4_place(a.p, pool, t0 + lane);
     if (mine.row == -2) atomicOr(a.status, kStatusBadPaged);  // read as zeros
   }
-  uint32_t kc[ITER], vc[ITER], kj[ITER], vj[ITER];
-  bool live[ITER];
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    const Q4Place x = q4_place_of(mine, i * R::TOKENS + lane / R::LANES);
-    live[i] = x.row != -1;
-    kc[i] = vc[i] = kj[i] = vj[i] = 0;
-    if (x.row >= 0) {
-      const uint8_t* tile = pool.pages + x.tile;
-      kc[i] = *reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 0, x.row) + c / 2);
-      vc[i] = *reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 1, x.row) + c / 2);
-      kj[i] = tile[T::scales(pool.tile_shift, 0, x.row) + c / kQ4Group];
-      vj[i] = tile[T::scales(pool.tile_shift, 1, x.row) + c / kQ4Group];
+  for (int i = 0; i < ITER; ++i) place[i] = q4_place_of(mine, i * R::TOKENS + lane / R::LANES);
+  struct Codes {
+    uint32_t kc[ITER], vc[ITER], kj[ITER], vj[ITER];
+  };
+  auto load = [&](Codes& x, int head) {
+    const long long off = (long long)head * pool.tiles * pool.tile_bytes;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      x.kc[i] = x.vc[i] = x.kj[i] = x.vj[i] = 0;
+      const int row = place[i].row;
+      if (row >= 0) {
+        const uint8_t* tile = pool.pages + place[i].tile + off;
+        x.kc[i] = __ldg(reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 0, row) + c / 2));
+        x.vc[i] = __ldg(reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 1, row) + c / 2));
+        x.kj[i] = __ldg(tile + T::scales(pool.tile_shift, 0, row) + c / kQ4Group);
+        x.vj[i] = __ldg(tile + T::scales(pool.tile_shift, 1, row) + c / kQ4Group);
+      }
     }
-  }
+  };
+  Codes next;
+  load(next, h);
+#pragma unroll 1
+  for (; h < h1; ++h) {
+    const Codes x = next;
+    if (h + 1 < h1) load(next, h + 1);
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    if (!live[i]) continue;
-    const long long t = t0 + i * R::TOKENS + lane / R::LANES, at = (long long)h * D + c;
-    *reinterpret_cast<uint4*>(a.k + t * a.k_stride + at) = q4_word(kc[i], q4_scale(kj[i]));
-    *reinterpret_cast<uint4*>(a.v + t * a.v_stride + at) = q4_word(vc[i], q4_scale(vj[i]));
+    for (int i = 0; i < ITER; ++i) {
+      if (place[i].row == -1) continue;
+      const long long t = t0 + i * R::TOKENS + lane / R::LANES, at = (long long)h * D + c;
+      *reinterpret_cast<uint4*>(a.k + t * a.k_stride + at) = q4_word(x.kc[i], q4_scale(x.kj[i]));
+      *reinterpret_cast<uint4*>(a.v + t * a.v_stride + at) = q4_word(x.vc[i], q4_scale(x.vj[i]));
+    }
   }
 }
 
@@ -763,43 +824,45 @@ cudaError_t launch_step_q4_d(const Q4Pool& pool, long long most, bool clusters, 
 }
 
 template <int D>
-cudaError_t launch_append_q4_d(const Q4Pool& pool, AppendArgs a, cudaStream_t stream) {
+cudaError_t launch_append_q4_d(const Q4Pool& pool, AppendArgs a, int sms, cudaStream_t stream) {
   a.check_ctas = q4_check_ctas(a.p);
-  const int grid = (int)(a.check_ctas + q4_blocks<D, kQ4AppendIter>(a.p.rows, a.heads));
-  return launch_after(append_q4_kernel<D>, grid, kQ4Threads, 0, stream, a, pool);
+  const int step = q4_head_step<D, kQ4AppendIter>(a.p.rows, a.heads, sms);
+  const int grid = (int)(a.check_ctas + q4_blocks<D, kQ4AppendIter>(a.p.rows, a.heads, step));
+  return launch_after(append_q4_kernel<D>, grid, kQ4Threads, 0, stream, a, pool, step);
 }
 
 template <int D>
-cudaError_t launch_read_q4_d(const Q4Pool& pool, ReadArgs a, cudaStream_t stream) {
+cudaError_t launch_read_q4_d(const Q4Pool& pool, ReadArgs a, int sms, cudaStream_t stream) {
   a.check_ctas = q4_check_ctas(a.p);
-  const int grid = (int)(a.check_ctas + q4_blocks<D, kQ4ReadIter>(a.p.rows, a.heads));
-  return launch_after(read_q4_kernel<D>, grid, kQ4Threads, 0, stream, a, pool);
+  const int step = q4_head_step<D, kQ4ReadIter>(a.p.rows, a.heads, sms);
+  const int grid = (int)(a.check_ctas + q4_blocks<D, kQ4ReadIter>(a.p.rows, a.heads, step));
+  return launch_after(read_q4_kernel<D>, grid, kQ4Threads, 0, stream, a, pool, step);
 }
 
 }  // namespace
 
 bool q4_rows_fit(const PagedView& p, int heads, int d) {
   // the append's CTAs, which are more than the reading's
-  const long long blocks = d == 32   ? q4_blocks<32, kQ4AppendIter>(p.rows, heads)
-                           : d == 64 ? q4_blocks<64, kQ4AppendIter>(p.rows, heads)
-                                     : q4_blocks<128, kQ4AppendIter>(p.rows, heads);
+  const long long blocks = d == 32   ? q4_blocks<32, kQ4AppendIter>(p.rows, heads, 1)
+                           : d == 64 ? q4_blocks<64, kQ4AppendIter>(p.rows, heads, 1)
+                                     : q4_blocks<128, kQ4AppendIter>(p.rows, heads, 1);
   static_assert(kQ4AppendIter <= kQ4ReadIter, "more CTAs");
   return q4_check_ctas(p) + blocks <= 0x7fffffffLL;
 }
 
-cudaError_t launch_append_q4(const Q4Pool& pool, const AppendArgs& a, cudaStream_t stream) {
+cudaError_t launch_append_q4(const Q4Pool& pool, const AppendArgs& a, int sms, cudaStream_t stream) {
   switch (a.d) {
-    case 32: return launch_append_q4_d<32>(pool, a, stream);
-    case 64: return launch_append_q4_d<64>(pool, a, stream);
-    default: return launch_append_q4_d<128>(pool, a, stream);
+    case 32: return launch_append_q4_d<32>(pool, a, sms, stream);
+    case 64: return launch_append_q4_d<64>(pool, a, sms, stream);
+    default: return launch_append_q4_d<128>(pool, a, sms, stream);
   }
 }
 
-cudaError_t launch_read_q4(const Q4Pool& pool, const ReadArgs& a, cudaStream_t stream) {
+cudaError_t launch_read_q4(const Q4Pool& pool, const ReadArgs& a, int sms, cudaStream_t stream) {
   switch (a.d) {
-    case 32: return launch_read_q4_d<32>(pool, a, stream);
-    case 64: return launch_read_q4_d<64>(pool, a, stream);
-    default: return launch_read_q4_d<128>(pool, a, stream);
+    case 32: return launch_read_q4_d<32>(pool, a, sms, stream);
+    case 64: return launch_read_q4_d<64>(pool, a, sms, stream);
+    default: return launch_read_q4_d<128>(pool, a, sms, stream);
   }
 }
 

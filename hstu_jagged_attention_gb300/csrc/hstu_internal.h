@@ -253,8 +253,8 @@ struct ReadArgs {
 };
 // Whether the launches below have a grid for the batch.
 bool q4_rows_fit(const PagedView& p, int heads, int d);
-cudaError_t launch_append_q4(const Q4Pool& pool, const AppendArgs& a, cudaStream_t stream);
-cudaError_t launch_read_q4(const Q4Pool& pool, const ReadArgs& a, cudaStream_t stream);
+cudaError_t launch_append_q4(const Q4Pool& pool, const AppendArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_read_q4(const Q4Pool& pool, const ReadArgs& a, int sms, cudaStream_t stream);
 // `most`: CTAs with work, at most; clusters: a cluster of CTAs an item instead.
 cudaError_t launch_step_q4(int d, const Q4Pool& pool, long long most, bool clusters, const StepArgs& a,
                            int sms, cudaStream_t stream);

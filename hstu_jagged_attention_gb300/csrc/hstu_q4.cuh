@@ -89,17 +89,15 @@ __device__ __forceinline__ uint4 q4_word(uint32_t w, const Q4Scale& s) {
 }
 
 // ------------------------------------------------------------------ to codes
-// NaN as 0, infinities as the largest finite number.
-__device__ __forceinline__ uint32_t q4_finite(uint32_t x) {
+// Two bf16 numbers as they are held at most: +-26880, 7 times the largest scale
+// (0x46d2), and NaN as 0.
+constexpr uint32_t kQ4Most = 0x46d2u;
+__device__ __forceinline__ uint32_t q4_clamp(uint32_t x) {
   uint32_t r = 0;
 #pragma unroll
   for (int i = 0; i < 32; i += 16) {
-    uint32_t h = x >> i & 0xffffu;
-    if ((h & 0x7fffu) > 0x7f80u)
-      h = 0;
-    else if ((h & 0x7fffu) == 0x7f80u)
-      h -= 1;
-    r |= h << i;
+    const uint32_t h = x >> i & 0xffffu, m = h & 0x7fffu;
+    r |= (m > 0x7f80u ? 0u : m > kQ4Most ? (h & 0x8000u) | kQ4Most : h) << i;
   }
   return r;
 }
@@ -117,30 +115,25 @@ __device__ __forceinline__ uint32_t q4_quantise(const uint4& half, uint32_t* sca
     return max(m & 0xffffu, m >> 16);
   };
   uint32_t m = largest();
-  if (__any_sync(0xffffffffu, m >= 0x7f80u)) {  // something is not finite
+  if (__any_sync(0xffffffffu, m > kQ4Most)) {  // past the largest scale, or not finite
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = q4_finite(x[i]);
+    for (int i = 0; i < 4; ++i) x[i] = q4_clamp(x[i]);
     m = largest();
   }
   // max / 7, less 2^-16 of it, rounded up to four significant bits
   const float seventh = __uint_as_float(m << 16) * (float)((1.0 - 0x1p-16) / 7.0);
-  const int up = (int)((__float_as_uint(seventh) + 0xfffffu) >> 20) - (107 << 3);
-  const int j = min(max(up, 0), 255);
+  const int j = max((int)((__float_as_uint(seventh) + 0xfffffu) >> 20) - (107 << 3), 0);  // <= 255: m is clamped
   *scale = (uint32_t)j;
-  const float s = __uint_as_float((uint32_t)(j + (107 << 3)) << 20);
   float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__uint_as_float((uint32_t)(j + (107 << 3)) << 20)));
   inv *= 1.0f + 0x1p-16f;
   uint32_t w = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float a = __uint_as_float(x[i] << 16), b = __uint_as_float(x[i] & 0xffff0000u);
-    if (up > 255) {  // past the largest scale: saturated
-      a = fminf(fmaxf(a, -7.0f * s), 7.0f * s);
-      b = fminf(fmaxf(b, -7.0f * s), 7.0f * s);
-    }
-    // the integer in the low bits of 1.5 2^23 + x / s
-    const float2 y = __ffma2_rn(make_float2(a, b), make_float2(inv, inv), make_float2(12582912.f, 12582912.f));
+    // the integers in the low bits of 1.5 2^23 + x / s
+    const float2 y =
+        __ffma2_rn(make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)),
+                   make_float2(inv, inv), make_float2(12582912.f, 12582912.f));
     const uint32_t both = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x5410);
     w |= (both & 0x000f000fu) << (4 * i);
   }
