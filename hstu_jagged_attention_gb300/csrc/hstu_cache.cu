@@ -703,7 +703,15 @@ long long units_bound(const PagedView& v, int heads, int tiles, int kb_shift, in
 // 16 x 4096.  At d = 128 the blocks cost more: 32 rows 11.0 and 13.5 on
 // 4 x 2000, 19.0 and 16.7 on 8 x 2000.  `units`: blocks of the 16-row tiles, at
 // most.
-bool use_tiles(const PagedView& v, int d, int sms, long long units) {
+// A cache of 4-bit codes: its 128-row tiles take 7 us more to fill their
+// pipeline, and its 16-row tiles, whose products have no padding, half as long
+// per block and tile as those per block.  On 16 x 4096 (4 heads, 16-row against
+// 128-row tiles) 32 rows took 23.6 us and 26.7 at d = 64, 38.5 and 44.5 at d =
+// 128, 48 rows 29.8 and 27.6, 51.8 and 46.2; on 8 x 2000, d = 64, 64 rows 15.6
+// and 16.0, 96 rows 20.2 and 18.4; on 1 x 4000 128 rows 10.3 and 18.0; at d =
+// 32, 16 x 4096, 48 rows 20.8 and 24.6, 64 rows 25.7 and 24.6.
+bool use_tiles(const PagedView& v, int d, int sms, long long units, bool q4) {
+  if (q4) return v.max_q > 2 * hstu::kStepRows && units > (d == 128 ? 14LL : d == 64 ? 20LL : 50LL) * sms;
   if (v.max_q <= hstu::kStepRows) return false;
   return v.max_q > 64 || units > (d == 128 ? 5LL : 20LL) * sms;
 }
@@ -1015,7 +1023,8 @@ int hstu_attn_fwd_cache(const hstu_cache* cache, const hstu_paged_batch* batch, 
   w.kb_shift = hstu::kStepShift;  // both kernels' blocks have 128 keys
   w.extra = item_units(d);
   w.most_parts = kMostParts;
-  const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra));
+  const bool tiled = use_tiles(p, d, cache->sms, units_bound(p, heads, w.tiles, w.kb_shift, w.extra),
+                               cache->q4.pages != nullptr);
   if (tiled) {
     w.tile_rows = HSTU_BLOCK_M;
     w.tiles = (p.max_q - 1) / w.tile_rows + 1;

@@ -263,11 +263,23 @@ def test_many_items():
     s.check(s.attend())
 
 
+# a table of 2000 pages of 64 asks for 128-row tiles where a bound of more than
+# 32 new tokens allows them
+@pytest.mark.parametrize("width", [1, 2000])
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("new,targets,max_q", [(33, 0, None), (47, 47, None), (64, 20, None), (9, 3, 130),
                                                (130, 0, None), (200, 200, None), (257, 9, None)])
-def test_several_tiles(d, new, targets, max_q):
-    s = Q4([0, 140, 300], [new, 1, 17], 64, 2, d, [targets, 0, 17], seed=30 + d, max_q=max_q)
+def test_several_tiles(d, new, targets, max_q, width):
+    s = Q4([0, 140, 300], [new, 1, 17], 64, 2, d, [targets, 0, 17], seed=30 + d, max_q=max_q, width=width)
+    s.check(s.attend())
+
+
+@pytest.mark.parametrize("d,heads,page", GEOMETRY + [(64, 3, 512), (128, 1, 4096)])
+@pytest.mark.parametrize("name", SHAPES)
+def test_few_rows_on_large_tiles(name, d, heads, page):
+    # a bound on the new tokens and a table that ask for 128-row tiles
+    hist, new, nt = SHAPES[name]
+    s = Q4(hist, new, page, heads, d, nt, seed=20 + d, pad=140, max_q=140, width=200000 // page)
     s.check(s.attend())
 
 
@@ -329,9 +341,10 @@ def test_a_pool_past_32_bits():
     assert torch.equal(big[move:], small.pages)
 
 
-@pytest.mark.parametrize("new", [[1, 2, 1, 40], [130, 2, 1, 40]])
-def test_bytes_past_the_end_never_matter(new):
-    outs = [Q4([100, 63, 0, 30], new, 64, 2, 64, [0, 2, 1, 5], seed=5, garbage=g).attend() for g in range(3)]
+@pytest.mark.parametrize("new,width", [([1, 2, 1, 40], 1), ([130, 2, 1, 40], 1), ([130, 2, 1, 40], 2000)])
+def test_bytes_past_the_end_never_matter(new, width):
+    outs = [Q4([100, 63, 0, 30], new, 64, 2, 64, [0, 2, 1, 5], seed=5, garbage=g, width=width).attend()
+            for g in range(3)]
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
@@ -344,7 +357,7 @@ def test_a_shared_prefix_is_read_from_shared_pages():
 
 
 @pytest.mark.parametrize("new", [[2, 2, 1], [70, 2, 130]])
-@pytest.mark.parametrize("page,width", [(16, 1), (16, 600), (128, 1), (256, 80)])
+@pytest.mark.parametrize("page,width", [(16, 1), (16, 600), (16, 8000), (128, 1), (256, 500)])
 def test_bad_lengths_and_pages_are_skipped_and_reported(page, width, new):
     s = Q4([100, 340, 70], new, page, 1, 64, seed=7, width=width)
     good, whole = s.attend(), s.read()
@@ -397,9 +410,9 @@ def test_bad_lengths_and_pages_are_skipped_and_reported(page, width, new):
             assert np.array_equal(now[1][pg, slot], layer.f64(s.vp[pg, slot]) if kept else layer.q4_held(s.v[t]))
 
 
-@pytest.mark.parametrize("new", [1, 40, 130])
-def test_rows_before_the_first_sequence_stay(new):
-    s = Q4([100, 0, 700], [3, new, 1], 16, 2, 64, seed=81)
+@pytest.mark.parametrize("new,width", [(1, 1), (40, 1), (130, 1), (130, 8000)])
+def test_rows_before_the_first_sequence_stay(new, width):
+    s = Q4([100, 0, 700], [3, new, 1], 16, 2, 64, seed=81, width=width)
     good, kv = s.attend(), s.read()
     s.dev["q_offsets"].add_(4)
     lead = torch.full((4, 2, 64), float("nan"), device="cuda", dtype=torch.bfloat16)
@@ -418,7 +431,7 @@ def test_rows_before_the_first_sequence_stay(new):
 
 # table widths (pages of 16) and new tokens that send a call to each of the
 # kernels: clusters and shares of 16-row tiles, 128-row tiles
-FORMS = [(1, [1, 1, 1]), (600, [1, 1, 1]), (600, [5, 1, 16]), (40, [70, 3, 130])]
+FORMS = [(1, [1, 1, 1]), (600, [1, 1, 1]), (600, [5, 1, 16]), (40, [70, 3, 130]), (8000, [70, 3, 130])]
 
 
 class Growing:
@@ -525,7 +538,7 @@ def test_graphs_that_take_turns_share_a_workspace():
             g.check(i)
 
 
-@pytest.mark.parametrize("first,second", [(0, 1), (1, 2), (1, 3), (3, 3)])
+@pytest.mark.parametrize("first,second", [(0, 1), (1, 2), (1, 3), (3, 4), (4, 4)])
 def test_two_streams(first, second):
     a, b = (Growing([3000, 90, 700], FORMS[f][1], FORMS[f][0], 1, 2, 64, seed=97 + f) for f in (first, second))
     a.step(0), b.step(0)
@@ -557,7 +570,7 @@ def test_large_pages_and_many_heads(wide, name, d, heads, page):
 
 
 @pytest.mark.parametrize("d", [32, 64, 128])
-@pytest.mark.parametrize("new,width", [(1, 1), (1, 700), (16, 700), (200, 1)])
+@pytest.mark.parametrize("new,width", [(1, 1), (1, 700), (16, 700), (200, 1), (200, 4000)])
 @pytest.mark.parametrize("flags", [0, binding.HSTU_DEBUG_UNSIGNALLED_WAIT])
 def test_giving_up_at_once_leaves_nothing_behind(flags, new, width, d):
     # a limit that runs out while the first copies are on their way: they land
@@ -581,7 +594,7 @@ def test_giving_up_at_once_leaves_nothing_behind(flags, new, width, d):
         assert torch.equal(s.attend(q=q, workspace=ws), good)
 
 
-@pytest.mark.parametrize("new,width", [(1, 1), (1, 400), (70, 1)])
+@pytest.mark.parametrize("new,width", [(1, 1), (1, 400), (70, 1), (70, 4000)])
 def test_a_wait_that_runs_out_is_reported(new, width):
     s = Q4([900, 40], [new, 1], 32, 2, 64, seed=40 + new, width=width)
     good, ws = s.attend(), s.workspace()
