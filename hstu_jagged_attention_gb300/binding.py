@@ -836,6 +836,8 @@ def hstu_cache_create(k_pages, v_pages) -> Cache:
     stride = _odd_row_stride(k_pages.stride(), shape, "k_pages")
     if _odd_row_stride(v_pages.stride(), shape, "v_pages") != stride:
         raise ValueError("k_pages and v_pages must have the same page stride")
+    if stride == 0:  # which the library takes for packed pages
+        raise ValueError("k_pages and v_pages must not share memory between pages")
     h = _VP()
     _check(lib().hstu_cache_create(k_pages.data_ptr(), v_pages.data_ptr(), *shape, stride,
                                    ctypes.byref(h)), "hstu_cache_create")

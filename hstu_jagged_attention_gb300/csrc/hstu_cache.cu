@@ -831,8 +831,9 @@ int hstu_cache_create_q4(void* pages, int num_pages, int page_size, int heads, i
   if (rc != HSTU_OK) return rc;
   const long long packed = q4_page_bytes(c);
   if (page_stride == 0) page_stride = packed;
-  // no page number times the stride passes 63 bits
-  if (hstu::bad_ptr(pages, 16) || page_stride < packed || (page_stride & 15) || page_stride >= (1LL << 40))
+  // a page number times the stride is at most 2^62
+  if (hstu::bad_ptr(pages, 16) || page_stride < packed || (page_stride & 15) ||
+      page_stride > (1LL << 62) / num_pages)
     return HSTU_ERR_INVALID_ARG;
   c.q4.pages = static_cast<uint8_t*>(pages);
   c.q4.page_stride = page_stride;

@@ -33,7 +33,8 @@ def test_refusals_on_the_host():
     assert make(d=96) == binding.HSTU_ERR_UNSUPPORTED
     for kw in (dict(pages=0), dict(pages=8), dict(num_pages=0), dict(page_size=24), dict(page_size=8),
                dict(page_size=8192), dict(heads=0), dict(stride=packed - 16), dict(stride=packed + 8),
-               dict(stride=-packed), dict(stride=1 << 40)):
+               dict(stride=-packed), dict(stride=1 << 61),
+               dict(num_pages=2 ** 31 - 1, stride=1 << 40)):
         assert make(**kw) == BAD and not h, kw
     assert L.hstu_cache_create_q4(16, 4, 16, 2, 64, 0, None) == BAD
     assert L.hstu_cache_read(None, None, None, 0, None, 0, None) == BAD
@@ -56,6 +57,23 @@ def test_a_cache_of_another_device_is_refused(monkeypatch):
         binding.hstu_cache_create_q4(Pool, 16, 2, 64)
     with pytest.raises(ValueError):
         binding.hstu_cache_create_q4(torch.zeros(4, 16 * 2 * 72, dtype=torch.uint8), 16, 2, 64)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_pages_that_share_memory_are_refused(monkeypatch, q4):
+    # a broadcast pool's stride is 0, which the library would take for packed
+    # pages, past the end of the one page that there is
+    torch = pytest.importorskip("torch")
+
+    class Pool:  # what the binding asks of a device tensor
+        shape = torch.Size((4, 16 * 2 * 72) if q4 else (4, 16, 2, 64))
+        is_cuda, ndim, dtype, device = True, len(shape), torch.uint8 if q4 else torch.bfloat16, torch.device("cuda:0")
+        stride = staticmethod(lambda: (0, 1) if q4 else (0, 128, 64, 1))
+        data_ptr = staticmethod(lambda: 1 << 20)
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    with pytest.raises(ValueError, match="share memory"):
+        binding.hstu_cache_create_q4(Pool, 16, 2, 64) if q4 else binding.hstu_cache_create(Pool, Pool)
 
 
 # ------------------------------------------------- the 64-bit form itself
