@@ -113,7 +113,8 @@ struct Q4Angles {
 // This lane's channels x, of c .. c + 7 of the head, rotated if c < rot.  Where
 // the channels turn in halves the partner's are rot / 16 lanes away.  The
 // products are rounded one by one, as a plain form does: what is quantised then
-// is the same number, not one beside it across a border.  Whole-warp call.
+// is the same number, not one beside it across a border.  (Products and sums of
+// two floats at once come out fused.)  Whole-warp call.
 __device__ __forceinline__ uint4 q4_turn(const uint4& x, const Q4Angles& g, int c, int rot, bool pairs) {
   F8 a = unpack8(x);
   if (pairs) {
@@ -129,13 +130,8 @@ __device__ __forceinline__ uint4 q4_turn(const uint4& x, const Q4Angles& g, int 
                                __shfl_sync(0xffffffffu, x.z, other), __shfl_sync(0xffffffffu, x.w, other));
     const F8 b = unpack8(y);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float2 r =
-          __fadd2_rn(__fmul2_rn(make_float2(a.f[i], a.f[i + 1]), make_float2(g.cs[i], g.cs[i + 1])),
-                     __fmul2_rn(make_float2(b.f[i], b.f[i + 1]), make_float2(g.sn[i], g.sn[i + 1])));
-      a.f[i] = r.x;
-      a.f[i + 1] = r.y;
-    }
+    for (int i = 0; i < 8; ++i)
+      a.f[i] = __fadd_rn(__fmul_rn(a.f[i], g.cs[i]), __fmul_rn(b.f[i], g.sn[i]));
   }
   return c < rot ? pack8(a) : x;
 }

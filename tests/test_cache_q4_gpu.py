@@ -221,6 +221,25 @@ def test_append_from_a_fused_projection_and_in_place():
     assert torch.equal(q3[s.total:].cpu(), s.q[s.total:])  # a padded batch's rows stay
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+def test_the_rotation_rounds_each_product(pairs):
+    # enough values that a fused product would show
+    s = Q4([0] * 4, [4000] * 4, 128, 1, 64, seed=15)
+    table = rotary_table(4000, 64)
+    q_out = torch.zeros(s.rows, 1, 64, device="cuda", dtype=torch.bfloat16)
+    binding.hstu_cache_append(s.cache, s.batch, s.k.cuda(), s.v.cuda(), q=s.q.cuda(), q_out=q_out,
+                              rotary=table.cuda(), rotary_pairs=pairs)
+    k_back, _ = s.read()
+    at = np.tile(np.arange(4000), 4)
+    c, sn = table.numpy()[at, None, :32], table.numpy()[at, None, 32:]
+    a, b = (slice(0, 64, 2), slice(1, 64, 2)) if pairs else (slice(0, 32), slice(32, 64))
+    for x, got, held in ((s.q, q_out, lambda y: y), (s.k, k_back, layer.q4_held)):
+        x = x.float().numpy()
+        y = np.empty_like(x)
+        y[..., a], y[..., b] = x[..., a] * c - x[..., b] * sn, x[..., b] * c + x[..., a] * sn
+        assert np.array_equal(layer.f64(got), held(layer.f64(torch.from_numpy(y).bfloat16())))
+
+
 def test_every_sequence_is_checked():
     # more sequences than a CTA of the check has threads, wrong ones among them
     n = 700
