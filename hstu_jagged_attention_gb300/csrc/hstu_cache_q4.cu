@@ -328,6 +328,7 @@ struct Q4Cfg {
   static constexpr int KW = KEYS / WARPS;
   static constexpr int STAGEB = KEYS * q4_token_bytes(D);
   static constexpr int PER_SM = D == 128 ? 2 : 3;
+  static constexpr int UNROLL = 2;  // 16-key steps of a warp in one piece of code
   static constexpr int RING = 128 * 1024 / PER_SM;
   static constexpr int STAGES = RING / STAGEB < 15 ? RING / STAGEB : 15;
   static constexpr int MAX_STAGES = 16;
@@ -468,22 +469,23 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
   constexpr int RS = step_red_stride(D);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
-  // the lane's keys, values and scales in a stage, for each 16-key step
-  const uint8_t *k_at[KS], *ks_at[KS], *v_at[KS][2], *vs_at[KS][2];
+  // the lane's keys, values and scales in a stage, for its first 16 keys, and
+  // how far the next 16's are: in the same tile, or the next one
   const int vk[2] = {q4_key<D>(t4, 0), q4_key<D>(t4, 1)};
   const int kk = q4_key<D>(g8 >> 1, g8 & 1);
+  static_assert(KS <= 2, "two steps are in one tile, or in two");
+  const int row0 = (C::KW * warp) & ((1 << pool.tile_shift) - 1);
+  const uint8_t* tile = ring + ((C::KW * warp) >> pool.tile_shift) * pool.tile_bytes;
+  const bool apart = pool.tile_shift == 4;
+  const int codes_step = apart ? pool.tile_bytes : 16 * T::CODEB;
+  const int scales_step = apart ? pool.tile_bytes : 16 * T::SCALEB;
+  const uint8_t* k_at = tile + T::codes(pool.tile_shift, 0, row0 + kk) + t4 * (D / 8);
+  const uint8_t* ks_at = tile + T::scales(pool.tile_shift, 0, row0 + kk) + t4 * (D / 4) / kQ4Group;
+  const uint8_t *v_at[2], *vs_at[2];
 #pragma unroll
-  for (int y = 0; y < KS; ++y) {
-    const int key0 = C::KW * warp + 16 * y;
-    const int sub = key0 >> pool.tile_shift, r = key0 & ((1 << pool.tile_shift) - 1);
-    const uint8_t* tile = ring + sub * pool.tile_bytes;
-    k_at[y] = tile + T::codes(pool.tile_shift, 0, r + kk) + t4 * (D / 8);
-    ks_at[y] = tile + T::scales(pool.tile_shift, 0, r + kk) + t4 * (D / 4) / kQ4Group;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      v_at[y][e] = tile + T::codes(pool.tile_shift, 1, r + vk[e]) + g8 * (D / 16);
-      vs_at[y][e] = tile + T::scales(pool.tile_shift, 1, r + vk[e]) + g8 * (D / 8) / kQ4Group;
-    }
+  for (int e = 0; e < 2; ++e) {
+    v_at[e] = tile + T::codes(pool.tile_shift, 1, row0 + vk[e]) + g8 * (D / 16);
+    vs_at[e] = tile + T::scales(pool.tile_shift, 1, row0 + vk[e]) + g8 * (D / 8) / kQ4Group;
   }
   const float2 ha2 = make_float2(a.half_alpha, a.half_alpha);
   int st = 0;
@@ -523,73 +525,72 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
     for (int i = 0; i < g.n && !dead; ++i) {
       const int kb = g.walk.block(g.i0 + i) << kStepShift;
       if ((dead = !__all_sync(0xffffffffu, step_wait(full + 8u * st, ph, wt, kSiteStepFull)))) break;
-      const uint32_t off = st * C::STAGEB;
-      float s[KS][G][4];
-#pragma unroll
+      const bool masked = kb + C::KEYS > g.walk.p0 + 1 || kb + C::KEYS > g.seq.hist;
+#pragma unroll C::UNROLL
       for (int y = 0; y < KS; ++y) {
-        uint32_t kw[2][KWORDS], j[2];  // keys kk and 8 + kk
+        const uint32_t off = st * C::STAGEB + y * codes_step, off_sc = st * C::STAGEB + y * scales_step;
+        float s[G][4];
+        {
+          uint32_t kw[2][KWORDS], j[2];  // keys kk and 8 + kk
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          lds_words<KWORDS>(k_at[y] + off + 8 * h * T::CODEB, kw[h]);
-          const uint8_t* sat = ks_at[y] + off + 8 * h * T::SCALEB;
-          j[h] = D == 128 ? lds16(sat) : *sat;
-        }
-        Q4Scale s0 = q4_scale(j[0] & 255u), s1 = q4_scale(j[1] & 255u);
-#pragma unroll
-        for (int x = 0; x < KWORDS; ++x) {
-          if (x == 2) {
-            s0 = q4_scale(j[0] >> 8);
-            s1 = q4_scale(j[1] >> 8);
+          for (int h = 0; h < 2; ++h) {
+            lds_words<KWORDS>(k_at + off + 8 * h * T::CODEB, kw[h]);
+            const uint8_t* sat = ks_at + off_sc + 8 * h * T::SCALEB;
+            j[h] = D == 128 ? lds16(sat) : *sat;
           }
-          const uint32_t a0[4] = {q4_pair<0>(kw[0][x], s0), q4_pair<0>(kw[1][x], s1), q4_pair<1>(kw[0][x], s0),
-                                  q4_pair<1>(kw[1][x], s1)};
-          const uint32_t a1[4] = {q4_pair<2>(kw[0][x], s0), q4_pair<2>(kw[1][x], s1), q4_pair<3>(kw[0][x], s0),
-                                  q4_pair<3>(kw[1][x], s1)};
+          Q4Scale s0 = q4_scale(j[0] & 255u), s1 = q4_scale(j[1] & 255u);
 #pragma unroll
-          for (int u = 0; u < G; ++u) {
-            if (x == 0)
-              q4_mma_first(s[y][u], a0, qf[u][0][0], qf[u][0][1]);
-            else
-              q4_mma(s[y][u], a0, qf[u][2 * x][0], qf[u][2 * x][1]);
-            q4_mma(s[y][u], a1, qf[u][2 * x + 1][0], qf[u][2 * x + 1][1]);
-          }
-        }
-      }
-      // p = silu(alpha S) = h + h tanh(h), h = alpha S / 2
-      uint32_t hi[KS][G][2], lo[KS][G][2];
-      auto silu = [&](auto masked) {
+          for (int x = 0; x < KWORDS; ++x) {
+            if (x == 2) {
+              s0 = q4_scale(j[0] >> 8);
+              s1 = q4_scale(j[1] >> 8);
+            }
+            const uint32_t a0[4] = {q4_pair<0>(kw[0][x], s0), q4_pair<0>(kw[1][x], s1), q4_pair<1>(kw[0][x], s0),
+                                    q4_pair<1>(kw[1][x], s1)};
+            const uint32_t a1[4] = {q4_pair<2>(kw[0][x], s0), q4_pair<2>(kw[1][x], s1), q4_pair<3>(kw[0][x], s0),
+                                    q4_pair<3>(kw[1][x], s1)};
 #pragma unroll
-        for (int y = 0; y < KS; ++y) {
-#pragma unroll
-          for (int u = 0; u < G; ++u) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float2 x = __fmul2_rn(make_float2(s[y][u][2 * h], s[y][u][2 * h + 1]), ha2);
-              float2 p = __ffma2_rn(x, make_float2(tanh_approx(x.x), tanh_approx(x.y)), x);
-              if constexpr (decltype(masked)::value) {
-                const int pos = g.walk.p0 + (both ? 2 * (t4 & 1) : 8 * u + 2 * t4);
-                const int key = kb + C::KW * warp + 16 * y + 8 * h + kk;
-                if (!(key <= pos && (key < g.seq.hist || key == pos))) p.x = 0.f;
-                if (!(key <= pos + 1 && (key < g.seq.hist || key == pos + 1))) p.y = 0.f;
-              }
-              const uint32_t ph2 = pack_bf16x2(p.x, p.y);
-              const float2 rest = __fadd2_rn(
-                  p, make_float2(-__uint_as_float(ph2 << 16), -__uint_as_float(ph2 & 0xffff0000u)));
-              const uint32_t pl2 = pack_bf16x2(rest.x, rest.y);
-              hi[y][u][h] = transpose8(both && t4 >= 2 ? pl2 : ph2);
-              if constexpr (!both) lo[y][u][h] = transpose8(pl2);
+            for (int u = 0; u < G; ++u) {
+              if (x == 0)
+                q4_mma_first(s[u], a0, qf[u][0][0], qf[u][0][1]);
+              else
+                q4_mma(s[u], a0, qf[u][2 * x][0], qf[u][2 * x][1]);
+              q4_mma(s[u], a1, qf[u][2 * x + 1][0], qf[u][2 * x + 1][1]);
             }
           }
         }
-      };
-      // two copies: the tests of a masked block, merged into one, would be
-      // issued in every block
-      if (kb + C::KEYS > g.walk.p0 + 1 || kb + C::KEYS > g.seq.hist)
-        silu(std::true_type{});
-      else
-        silu(std::false_type{});
+        // p = silu(alpha S) = h + h tanh(h), h = alpha S / 2
+        float2 p[G][2];
 #pragma unroll
-      for (int y = 0; y < KS; ++y) {
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 x = __fmul2_rn(make_float2(s[u][2 * h], s[u][2 * h + 1]), ha2);
+            p[u][h] = __ffma2_rn(x, make_float2(tanh_approx(x.x), tanh_approx(x.y)), x);
+          }
+        if (masked) {
+          const int key0 = kb + C::KW * warp + 16 * y + kk;
+#pragma unroll
+          for (int u = 0; u < G; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int pos = g.walk.p0 + (both ? 2 * (t4 & 1) : 8 * u + 2 * t4), key = key0 + 8 * h;
+              if (!(key <= pos && (key < g.seq.hist || key == pos))) p[u][h].x = 0.f;
+              if (!(key <= pos + 1 && (key < g.seq.hist || key == pos + 1))) p[u][h].y = 0.f;
+            }
+        }
+        uint32_t hi[G][2], lo[G][2];
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t ph2 = pack_bf16x2(p[u][h].x, p[u][h].y);
+            const float2 rest = __fadd2_rn(
+                p[u][h], make_float2(-__uint_as_float(ph2 << 16), -__uint_as_float(ph2 & 0xffff0000u)));
+            const uint32_t pl2 = pack_bf16x2(rest.x, rest.y);
+            hi[u][h] = transpose8(both && t4 >= 2 ? pl2 : ph2);
+            if constexpr (!both) lo[u][h] = transpose8(pl2);
+          }
         // four keys: vw[h][e] is key 8 h + vk[e] of the step
         uint32_t vw[2][2][VWORDS];
         Q4Scale sc[2];
@@ -598,12 +599,12 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
           uint32_t j[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint8_t* at = v_at[y][e] + off + 8 * h * T::CODEB;
+            const uint8_t* at = v_at[e] + off + 8 * h * T::CODEB;
             if constexpr (D == 32)
               vw[h][e][0] = lds16(at);
             else
               lds_words<VWORDS>(at, vw[h][e]);
-            j[e] = vs_at[y][e][off + 8 * h * T::SCALEB];
+            j[e] = vs_at[e][off_sc + 8 * h * T::SCALEB];
           }
           sc[h] = q4_scale(j[0], j[1]);
         }
@@ -639,10 +640,10 @@ __device__ void q4_compute(const StepArgs& a, const Q4Pool& pool, const PagedWor
 #pragma unroll
           for (int v = 0; v < G; ++v) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) q4_mma(o[v][4 * x + n], b[n], hi[y][v][0], hi[y][v][1]);
+            for (int n = 0; n < N; ++n) q4_mma(o[v][4 * x + n], b[n], hi[v][0], hi[v][1]);
             if constexpr (!both) {
 #pragma unroll
-              for (int n = 0; n < N; ++n) q4_mma(o[v][4 * x + n], b[n], lo[y][v][0], lo[y][v][1]);
+              for (int n = 0; n < N; ++n) q4_mma(o[v][4 * x + n], b[n], lo[v][0], lo[v][1]);
             }
           }
         }
