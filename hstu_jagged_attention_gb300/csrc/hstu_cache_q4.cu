@@ -136,7 +136,7 @@ __device__ __forceinline__ uint4 q4_turn(const uint4& x, const Q4Angles& g, int 
   return c < rot ? pack8(a) : x;
 }
 
-// 65,536 tokens of 4 heads of 64 with their queries, rotated, take 33.2 us (153
+// 65,536 tokens of 4 heads of 64 with their queries, rotated, take 33.5 us (153
 // MB, 4.6 TB/s): about 230 instructions for 8 channels of k, v and q, half of
 // them on the integer pipe at half rate, weigh as much as the memory.
 template <int D>
@@ -320,6 +320,12 @@ __global__ void __launch_bounds__(kQ4Threads)
 // second terms: one product for both.
 // Keys past a row's last are masked by a select on p; whatever bytes lie
 // there, as codes they are finite, and so add nothing.
+// Bound by the instructions that make codes into numbers, at 0.55 a cycle and
+// scheduler, and by the way in and out: one token for 512 sequences (log-normal
+// lengths, 2 heads of 64, 59 MB) takes 27.4 us, 4 of them until the first codes
+// are there.  Four warps of 32 keys and three CTAs an SM: 29.3 us when two took
+// 31.6, four (96 registers a thread) 31.3, and two of eight warps of 16 keys
+// 34.6; at d = 128 registers allow two.
 template <int D>
 struct Q4Cfg {
   static constexpr int WARPS = 4;
@@ -328,7 +334,8 @@ struct Q4Cfg {
   static constexpr int KW = KEYS / WARPS;
   static constexpr int STAGEB = KEYS * q4_token_bytes(D);
   static constexpr int PER_SM = D == 128 ? 2 : 3;
-  static constexpr int UNROLL = 2;  // 16-key steps of a warp in one piece of code
+  // 16-key steps of a warp in one piece of code (with one: 28.9 us)
+  static constexpr int UNROLL = 2;
   static constexpr int RING = 128 * 1024 / PER_SM;
   static constexpr int STAGES = RING / STAGEB < 15 ? RING / STAGEB : 15;
   static constexpr int MAX_STAGES = 16;
