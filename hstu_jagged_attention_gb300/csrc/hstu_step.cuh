@@ -95,15 +95,13 @@ __device__ __forceinline__ void step_join(const StepArgs& a, const PagedWork& w,
   // The last CTA to arrive at a cut item sums its parts in the CTAs' order, so
   // that the result does not depend on who is last.  One fence a CTA, after
   // the barrier and so for all the warps' stores.
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 2) {  // a thread an item: their counters' round trips overlap
     __threadfence();
-    unsigned last = 0;
-    if (cut0.parts && !dead && atomicAdd(a.counters + cut0.c0, 1u) == (unsigned)(cut0.parts - 1)) last |= 1u;
-    if (cut1.parts && !dead && atomicAdd(a.counters + cut1.c0, 1u) == (unsigned)(cut1.parts - 1)) last |= 2u;
-    // ready for the next launch
-    if (last & 1u) a.counters[cut0.c0] = 0;
-    if (last & 2u) a.counters[cut1.c0] = 0;
-    m->last = last;
+    const StepCut cut = threadIdx.x ? cut1 : cut0;
+    const bool last = cut.parts && !dead && atomicAdd(a.counters + cut.c0, 1u) == (unsigned)(cut.parts - 1);
+    if (last) a.counters[cut.c0] = 0;  // ready for the next launch
+    const unsigned both = __ballot_sync(3u, last);
+    if (threadIdx.x == 0) m->last = both;
   }
   step_barrier<WARPS>();
   const unsigned last = m->last;

@@ -90,16 +90,40 @@ class Q4(Setup):
 GEOMETRY = [(32, 3, 16), (64, 2, 64), (128, 1, 32), (64, 1, 256), (32, 2, 128), (128, 2, 16)]
 
 
+class Bf16(Setup):
+    """Setup's bf16 pools, with what Q4 offers."""
+    slots = Q4.slots
+    read = Q4.read
+
+
 # ------------------------------------------------------------------- reading
-@pytest.mark.parametrize("d,heads,page", GEOMETRY)
+@pytest.mark.parametrize("kind", [Q4, Bf16])
+@pytest.mark.parametrize("d,heads,page", GEOMETRY + [(64, 5, 512)])
 @pytest.mark.parametrize("name", SHAPES)
-def test_read(name, d, heads, page):
+def test_read(name, d, heads, page, kind):
     hist, new, nt = SHAPES[name]
-    s = Q4(hist, new, page, heads, d, nt, seed=d + page, pad=2)
+    s = kind(hist, new, page, heads, d, nt, seed=d + page, pad=2)
     k, v = s.read()
     for t, pg, slot, _, _ in s.slots():
         assert torch.equal(k[t].cpu(), s.kp[pg, slot]) and torch.equal(v[t].cpu(), s.vp[pg, slot])
     assert (k[s.total:] == 7).all() and (v[s.total:] == 7).all()
+
+
+def test_bad_lengths_and_pages_of_a_bf16_cache_are_reported_by_the_reading():
+    s = Bf16([100, 40, 70], [2, 20, 1], 16, 2, 64, seed=7)
+    good = s.read()
+    assert binding.hstu_last_status() == (binding.HSTU_OK, 0)
+    for name, at, value, rows in (("kv_lens", 1, -1, slice(2, 22)), ("page_table", (1, 3), -1, slice(10, 22)),
+                                  ("page_table", (1, 3), s.num_pages, slice(10, 22))):
+        old = s.dev[name][at].clone()
+        s.dev[name][at] = value
+        k, v = s.read()
+        assert binding.hstu_last_status()[0] == binding.HSTU_ERR_INVALID_ARG
+        s.dev[name][at] = old
+        for x, y in zip((k, v), good):
+            left = 7 if name == "kv_lens" else 0  # not written, or read as zeros
+            assert (x[rows] == left).all()
+            assert torch.equal(x[:rows.start], y[:rows.start]) and torch.equal(x[22:], y[22:])
 
 
 @pytest.mark.parametrize("q4", [True, False])
@@ -219,6 +243,31 @@ def test_append_from_a_fused_projection_and_in_place():
     binding.hstu_cache_append(s.cache, s.batch, s.k.cuda(), s.v.cuda(), q=q3, q_out=q3, rotary=table)
     assert torch.equal(q3[:s.total], q_out[:s.total]) and torch.equal(first, s.pages)
     assert torch.equal(q3[s.total:].cpu(), s.q[s.total:])  # a padded batch's rows stay
+
+
+@pytest.mark.parametrize("d,heads,page,rot,pairs", [(32, 31, 16, 16, False), (64, 7, 256, 48, False),
+                                                    (128, 5, 64, 96, True), (64, 13, 32, 0, False)])
+def test_more_rows_than_warps(d, heads, page, rot, pairs):
+    # warps that take several heads, the last of them fewer
+    kv = [1700, 0, 2300, 1, 900]
+    s = Q4([0] * 5, kv, page, heads, d, [0, 0, 300, 1, 900], seed=16 + d, pad=5)
+    table = rotary_table(2400, rot) if rot else None
+    q_out = torch.full((s.rows, heads, d), 7.0, device="cuda", dtype=torch.bfloat16)
+    binding.hstu_cache_append(s.cache, s.batch, s.k.cuda(), s.v.cuda(), q=s.q.cuda(), q_out=q_out,
+                              rotary=None if table is None else table.cuda(), rotary_pairs=pairs)
+    k_back, v_back = s.read()
+    at = np.concatenate([np.minimum(np.arange(n), n - t) for n, t in zip(kv, [0, 0, 300, 1, 900])])
+    n, half = s.total, rot // 2
+    for x, got, held in ((s.q, q_out, lambda y: y), (s.k, k_back, layer.q4_held)):
+        x = x[:n].float().numpy()
+        y = x.copy()
+        if rot:
+            c, sn = table.numpy()[at, None, :half], table.numpy()[at, None, half:]
+            a, b = (slice(0, rot, 2), slice(1, rot, 2)) if pairs else (slice(0, half), slice(half, rot))
+            y[..., a], y[..., b] = x[..., a] * c - x[..., b] * sn, x[..., b] * c + x[..., a] * sn
+        assert np.array_equal(layer.f64(got)[:n], held(layer.f64(torch.from_numpy(y).bfloat16())))
+    assert np.array_equal(layer.f64(v_back)[:n], layer.q4_held(s.v[:n]))
+    assert all((x[n:] == 7).all() for x in (q_out, k_back, v_back))
 
 
 @pytest.mark.parametrize("pairs", [False, True])
