@@ -14,7 +14,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "hstu_attn.h"
 #include "hstu_internal.h"
