@@ -723,7 +723,9 @@ bool use_tiles(const PagedView& v, int d, int sms, long long units, bool q4) {
 // equal shares (either without this rule): 4.2 us and 3.9 on 64 keys, one
 // block, for which seven CTAs only start and meet; 4.2 and 6.0 on 513, 6.2 and
 // 7.7 on 4096, 8.9 and 9.3 on 8192, 14.6 and 13.3 on 16384; 9 sequences 17.1
-// and 18.5 on 8192.
+// and 18.5 on 8192.  A cache of 4-bit codes, likewise: 3.9 us and 5.7 on 513, 7.5
+// and 8.9 on 8100, 11.9 and 10.2 on 16000; 8 sequences of 8100, 16 tokens, 4
+// heads of 128, 21.1 and 24.5.
 bool use_clusters(const PagedView& v, int heads, int tiles, int clusters_at_once) {
   const long long items = (long long)tiles * v.batch * heads;
   const long long blocks = (((long long)v.max_pages << v.page_shift) + hstu::kStepKeys - 1) >> hstu::kStepShift;
