@@ -759,7 +759,7 @@ int hstu_cache_append(const hstu_cache* cache, const hstu_paged_batch* batch, co
  * takes them.  num_targets changes nothing but what is refused.
  *   k, v   bf16 device (rows, heads, d), rows k_stride / v_stride elements
  *          apart, as hstu_cache_append's; written for the rows of the
- *          sequences only.
+ *          sequences only.  They must not overlap one another or the pool.
  * Enqueues one kernel and allocates nothing.  Errors: as hstu_cache_append.
  */
 int hstu_cache_read(const hstu_cache* cache, const hstu_paged_batch* batch, void* k, int64_t k_stride,
