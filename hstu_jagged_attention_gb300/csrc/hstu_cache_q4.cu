@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(kQ4Threads)
   struct Codes {
     uint32_t kc[ITER], vc[ITER], kj[ITER], vj[ITER];
   };
+  // coherent loads: an append may write the pool until the wait above returns
   auto load = [&](Codes& x, int head) {
     const long long off = (long long)head * pool.tiles * pool.tile_bytes;
 #pragma unroll
@@ -272,10 +273,10 @@ __global__ void __launch_bounds__(kQ4Threads)
       const int row = place[i].row;
       if (row >= 0) {
         const uint8_t* tile = pool.pages + place[i].tile + off;
-        x.kc[i] = __ldg(reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 0, row) + c / 2));
-        x.vc[i] = __ldg(reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 1, row) + c / 2));
-        x.kj[i] = __ldg(tile + T::scales(pool.tile_shift, 0, row) + c / kQ4Group);
-        x.vj[i] = __ldg(tile + T::scales(pool.tile_shift, 1, row) + c / kQ4Group);
+        x.kc[i] = *reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 0, row) + c / 2);
+        x.vc[i] = *reinterpret_cast<const uint32_t*>(tile + T::codes(pool.tile_shift, 1, row) + c / 2);
+        x.kj[i] = tile[T::scales(pool.tile_shift, 0, row) + c / kQ4Group];
+        x.vj[i] = tile[T::scales(pool.tile_shift, 1, row) + c / kQ4Group];
       }
     }
   };

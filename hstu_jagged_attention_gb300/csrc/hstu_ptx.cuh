@@ -21,6 +21,8 @@ __host__ __device__ constexpr uint32_t make_idesc(int M, int N, int b_mn_major) 
 // kernel ends.  Every thread calls this before it touches global memory: it
 // returns when that kernel is done and its writes are visible.  What comes
 // before it (barriers, tensor maps) overlaps the previous kernel's end.
+// Visible to coherent loads: what a kernel of the library writes is not read
+// with __ldg, which is for memory that nobody writes while this kernel lives.
 __device__ __forceinline__ void after_previous_kernel() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

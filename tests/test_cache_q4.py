@@ -1,6 +1,8 @@
 """The cache of 4-bit codes without a GPU: the sizes and refusals of its entry
 points, and the 64-bit form of what is held."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -149,3 +151,26 @@ def test_zeroed_pages_hold_zeros_and_any_bytes_are_finite():
     assert np.all(k == -3840.0) and np.all(np.isfinite(v))
 
 
+# ------------------------------------------- loads of what kernels may write
+def test_only_inputs_that_no_kernel_writes_are_loaded_non_coherently():
+    # A kernel that starts while the stream's previous one ends sees that one's
+    # writes through coherent loads alone; __ldg is for memory that nobody
+    # writes while the kernel lives.  No kernel of the library writes rotation
+    # and page tables or the norm's weights; the caches' pages, and what is read
+    # back, are written by the append and the reading.
+    allowed = {"hstu_cache.cu": {"tab", "tab + a.rot / 2"}, "hstu_cache_q4.cu": {"tab", "tab + half"},
+               "hstu_norm.cu": {"p + at"}, "hstu_paged.cuh": {"row + p + lane", "row + p + 32 + lane"},
+               "hstu_step.cuh": set(), "hstu_q4.cuh": set(), "hstu_fwd_paged.cuh": set()}
+    for name, inputs in allowed.items():
+        with open(os.path.join(build.CSRC, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        assert "ld.global.nc" not in text and "__restrict__" not in text, name
+        met = set()
+        for m in re.finditer(r"__ldg\(", text):
+            depth, end = 1, m.end()
+            while depth:
+                depth += {"(": 1, ")": -1}.get(text[end], 0)
+                end += 1
+            arg = text[m.end():end - 1]
+            met.add(re.sub(r"reinterpret_cast<[^>]*>\((.*?)\)( \+ \w+)?$", r"\1", arg))
+        assert met == inputs, (name, met)

@@ -574,6 +574,54 @@ class Growing:
         assert np.all(np.abs(layer.f64(self.out) - ref) <= 2.0 ** -8 * np.abs(ref) + bound)
 
 
+@pytest.mark.parametrize("kind", ["q4", "bf16"])
+@pytest.mark.parametrize("d,heads,page,batch", [(64, 4, 64, 64), (32, 2, 16, 300), (128, 1, 128, 7)])
+def test_readings_between_appends_see_the_last_of_them(d, heads, page, batch, kind):
+    # append a token a sequence, read all histories, and again without a pause
+    # between any of them: a reading starts while the append before it writes
+    # codes and scales beside those that the reading before met
+    steps = 48
+    first = np.arange(batch) % 5  # tokens of the sequences before the first step
+    pages = -(-(int(first.max()) + steps) // page)
+    rng = np.random.default_rng(d)
+    table = torch.from_numpy(rng.permutation(batch * pages).reshape(batch, pages).astype(np.int32)).cuda()
+    if kind == "q4":
+        pool = torch.full((batch * pages, binding.hstu_cache_q4_page_bytes(page, heads, d)), 119, device="cuda",
+                          dtype=torch.uint8)
+        cache = binding.hstu_cache_create_q4(pool, page, heads, d)
+    else:
+        pool = torch.full((2, batch * pages, page, heads, d), 7.0, device="cuda", dtype=torch.bfloat16)
+        cache = binding.hstu_cache_create(pool[0], pool[1])
+    i32 = lambda x: torch.from_numpy(np.asarray(x, dtype=np.int32)).cuda()
+    gen = torch.Generator().manual_seed(d)
+    kv = torch.stack([randn(gen, batch, int(first.max()) + steps, heads, d) for _ in range(2)])
+    held = kv if kind == "bf16" else torch.from_numpy(np.stack([layer.q4_held(x) for x in kv])).bfloat16()
+    rows_of = lambda x, n: torch.cat([x[:, b, :m] for b, m in enumerate(n)], dim=1)
+    calls, seen = [], []
+    for i in range(steps):
+        n = first + i  # step 0: what stands there before
+        new = n if i == 0 else np.ones_like(n)
+        off, whole = (i32(np.concatenate([[0], np.cumsum(x)])) for x in (new, n))
+        at = lambda x: torch.cat([x[:, b, m - w:m] for b, (m, w) in enumerate(zip(n, new))], dim=1).cuda()
+        k, v = at(kv)
+        back = torch.full((2, int(n.sum()), heads, d), 7.0, device="cuda", dtype=torch.bfloat16)
+        calls.append((binding.PagedBatch(off, i32(n), table, int(new.max())),
+                      binding.PagedBatch(whole, i32(n), table, int(n.max())), k, v, back))
+        seen.append(rows_of(held, n).cuda())
+    for _ in range(3):
+        pool.fill_(119 if kind == "q4" else 7.0)
+        for *_, back in calls:
+            back.fill_(7.0)
+        torch.cuda.synchronize()
+        for new, whole, k, v, back in calls:
+            if len(k):
+                binding.hstu_cache_append(cache, new, k, v)
+            binding.hstu_cache_read(cache, whole, back[0], back[1])
+        torch.cuda.synchronize()
+        for i, ref in enumerate(seen):
+            assert torch.equal(calls[i][4], ref), i
+
+
 @pytest.mark.parametrize("own_workspace", [True, False])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("width,new", FORMS)
