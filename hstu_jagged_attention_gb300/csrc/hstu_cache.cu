@@ -906,6 +906,8 @@ int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int p
     return hstu::paged_units(w, hstu::paged_walk(s, e / v.batch, tile_rows, w.kb_shift).nb);
   };
   for (int e = 0; e < w.tiles * v.batch; ++e) w.total += units_of(e);
+  *n_segments = 0;
+  if (w.total == 0) return HSTU_OK;  // no item to share out
   w.per = hstu::paged_share(w, v.batch, grid, min_units);
   int n = 0;
   for (int cta = 0; cta < grid && (long long)cta * w.per < w.total; ++cta) {

@@ -3,6 +3,8 @@ points, and the 64-bit form of what is held."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -149,6 +151,18 @@ def test_zeroed_pages_hold_zeros_and_any_bytes_are_finite():
     ends = np.full((1, 16 * 72), 255, np.uint8)
     k, v = layer.q4_unpack(ends, 16, 1, 64)
     assert np.all(k == -3840.0) and np.all(np.isfinite(v))
+
+
+# ----------------------------------------------- the shares, without a GPU
+@pytest.mark.parametrize("hist,new", [([], []), ([5, 6], [0, 0]), ([0], [0])])
+@pytest.mark.parametrize("grid", [1, 15, 16, 500])
+def test_a_batch_without_work_has_no_shares(hist, new, grid):
+    # in a process of its own: it ended with a division by zero
+    code = (f"import numpy as np\nfrom hstu_jagged_attention_gb300 import binding\n"
+            f"from tests.test_cache import make_batch\n"
+            f"b, n, rows = make_batch(np.array({hist}, dtype=int), np.array({new}, dtype=int), 16)\n"
+            f"assert binding.hstu_cache_worklist(b, n, 16, rows, 2, 16, 128, {grid}).shape == (0, 8)\n")
+    assert subprocess.run([sys.executable, "-c", code], cwd=build.ROOT).returncode == 0
 
 
 # ------------------------------------------- loads of what kernels may write
