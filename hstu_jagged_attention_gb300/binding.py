@@ -139,6 +139,8 @@ _SIGNATURES = {
     "hstu_cache_slots": (_INT, [_PBP, _INT, _INT, ctypes.POINTER(_I64), _I32P]),
     "hstu_cache_worklist": (_INT, [_PBP, _INT, _INT, _INT, _INT, _INT, _INT, _INT, _INT, _I32P, _INT,
                                    _IP]),
+    "hstu_cache_worklist_ex": (_INT, [_PBP, _INT, _INT, _INT, _INT, _INT, _INT, _INT, _INT, _INT, _I32P,
+                                      _INT, _IP]),
     "hstu_cache_append": (_INT, [_VP, _PBP, _VP, _I64, _VP, _I64, _VP, _I64, _ROTP, _VP, _VP]),
     "hstu_attn_fwd_cache": (_INT, [_VP, _PBP, _VP, _I64, _F32, _F32, _VP, _VP, _VP]),
     "hstu_norm_fwd": (_INT, [_VP, _I64, _VP, _I64, _F32, _VP, _I64, _VP, _VP, _F32, _I64, _INT, _VP, _VP,
@@ -965,18 +967,19 @@ def hstu_cache_slots(batch: PagedBatch, num_pages: int, page_size: int, rows: in
 
 def hstu_cache_worklist(batch: PagedBatch, num_pages: int, page_size: int, rows: int, heads: int,
                         tile_rows: int, block_keys: int, grid: int, min_units: int = 1,
-                        extra: int = 1) -> np.ndarray:
+                        extra: int = 1, most_parts: int = 16) -> np.ndarray:
     """Host-only (no CUDA call; a batch of numpy arrays): the shares of
     hstu_attn_fwd_cache's CTAs, int32 (n, 8): CTA, sequence, head, tile, first
-    block, blocks, first CTA of the item, CTAs that share it."""
+    block, blocks, first CTA of the item, CTAs that share it.  ``most_parts``:
+    32 for 16-row tiles over a cache of 4-bit codes, else 16."""
     if not batch.host:
         raise ValueError("hstu_cache_worklist takes a batch of numpy arrays")
     args = (batch.struct(rows), int(num_pages), int(page_size), int(heads), int(tile_rows),
-            int(block_keys), int(extra), int(grid), int(min_units))
+            int(block_keys), int(extra), int(grid), int(min_units), int(most_parts))
     n = ctypes.c_int()
-    _check(lib().hstu_cache_worklist(*args, None, 0, ctypes.byref(n)), "hstu_cache_worklist")
+    _check(lib().hstu_cache_worklist_ex(*args, None, 0, ctypes.byref(n)), "hstu_cache_worklist")
     buf = np.zeros((max(n.value, 1), 8), dtype=np.int32)
-    _check(lib().hstu_cache_worklist(*args, buf.ctypes.data_as(_I32P), n.value, ctypes.byref(n)),
+    _check(lib().hstu_cache_worklist_ex(*args, buf.ctypes.data_as(_I32P), n.value, ctypes.byref(n)),
            "hstu_cache_worklist")
     return buf[:n.value]
 

@@ -884,10 +884,17 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
 int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int page_size, int heads,
                         int tile_rows, int block_keys, int extra, int grid, int min_units, int32_t* host_dst,
                         int capacity, int* n_segments) {
+  return hstu_cache_worklist_ex(host_batch, num_pages, page_size, heads, tile_rows, block_keys, extra, grid,
+                                min_units, kMostParts, host_dst, capacity, n_segments);
+}
+
+int hstu_cache_worklist_ex(const hstu_paged_batch* host_batch, int num_pages, int page_size, int heads,
+                           int tile_rows, int block_keys, int extra, int grid, int min_units, int most_parts,
+                           int32_t* host_dst, int capacity, int* n_segments) {
   int shift = 0;
   if (check_geometry(num_pages, page_size, &shift) != HSTU_OK) return HSTU_ERR_INVALID_ARG;
   if (!n_segments || heads < 1 || tile_rows < 1 || block_keys < 1 || (block_keys & (block_keys - 1)) ||
-      extra < 0 || extra > 64 || grid < 1 || min_units < 1 || capacity < 0)
+      extra < 0 || extra > 64 || grid < 1 || min_units < 1 || most_parts < 1 || capacity < 0)
     return HSTU_ERR_INVALID_ARG;
   PagedView v;
   const int rc = check_batch(host_batch, &v, num_pages, shift);
@@ -895,7 +902,7 @@ int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int p
   hstu::PagedWork w{};
   w.heads = heads;
   w.extra = extra;
-  w.most_parts = kMostParts;
+  w.most_parts = most_parts;
   w.tile_rows = tile_rows;
   w.tiles = v.rows > 0 && v.batch > 0 && v.max_q > 0 ? (v.max_q - 1) / tile_rows + 1 : 0;
   while ((1 << w.kb_shift) < block_keys) ++w.kb_shift;

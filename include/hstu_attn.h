@@ -690,7 +690,7 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
                      int64_t* host_slot, int32_t* host_pos);
 
 /*
- * hstu_cache_worklist -- the shares of work hstu_attn_fwd_cache gives its
+ * hstu_cache_worklist_ex -- the shares of work hstu_attn_fwd_cache gives its
  * CTAs, on the host only (no CUDA call; the batch's arrays are host memory).
  * (Calls that run without the workspace, see there, give each item's blocks
  * to eight CTAs instead: rank r takes blocks r nb / 8 .. (r + 1) nb / 8 - 1.)
@@ -700,20 +700,24 @@ int hstu_cache_slots(const hstu_paged_batch* host_batch, int num_pages, int page
  * hist that its last row may see, then its own keys' other blocks.  After an
  * item's blocks come `extra` (0 .. 64) units without work, for what an item
  * costs besides them.  CTA c of `grid` takes units [c per, (c + 1) per), per =
- * max(ceil(units / grid), min_units) or, with fewer than grid / 16 items =
- * tiles * batch * heads, at least ceil(units / (16 items)): no item is cut into
- * many more than 16.  (The kernels' min_units is 1, and a cache of 4-bit codes
- * allows 32 parts to an item of 16-row tiles.)  Segment i of host_dst is
- * eight numbers: (CTA, sequence, head, tile, index of its first block in the
- * walk, blocks, first CTA of the item, CTAs that share the item).
- * tile_rows >= 1, block_keys a power of two.
+ * max(ceil(units / grid), min_units) or, with fewer than grid / most_parts
+ * items = tiles * batch * heads, at least ceil(units / (most_parts items)): no
+ * item is cut into many more than most_parts.  The kernels' min_units is 1 and
+ * their most_parts 16, but 32 for 16-row tiles over a cache of 4-bit codes.
+ * Segment i of host_dst is eight numbers: (CTA, sequence, head, tile, index of
+ * its first block in the walk, blocks, first CTA of the item, CTAs that share
+ * the item).  tile_rows >= 1, block_keys a power of two, most_parts >= 1.
  *   capacity    segments host_dst holds; NULL host_dst: count only.
  *   *n_segments receives their number.
+ * hstu_cache_worklist is that with most_parts = 16.
  * Errors: HSTU_ERR_INVALID_ARG for bad arguments or a short capacity.
  */
 int hstu_cache_worklist(const hstu_paged_batch* host_batch, int num_pages, int page_size, int heads,
                         int tile_rows, int block_keys, int extra, int grid, int min_units, int32_t* host_dst,
                         int capacity, int* n_segments);
+int hstu_cache_worklist_ex(const hstu_paged_batch* host_batch, int num_pages, int page_size, int heads,
+                           int tile_rows, int block_keys, int extra, int grid, int min_units, int most_parts,
+                           int32_t* host_dst, int capacity, int* n_segments);
 
 /*
  * hstu_cache_append -- write the new tokens' keys and values into the cache,

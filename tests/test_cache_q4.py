@@ -11,6 +11,7 @@ import pytest
 
 from hstu_jagged_attention_gb300 import binding, build
 from oracle import layer
+from tests.test_cache import make_batch
 
 OK, BAD = binding.HSTU_OK, binding.HSTU_ERR_INVALID_ARG
 
@@ -163,6 +164,59 @@ def test_a_batch_without_work_has_no_shares(hist, new, grid):
             f"b, n, rows = make_batch(np.array({hist}, dtype=int), np.array({new}, dtype=int), 16)\n"
             f"assert binding.hstu_cache_worklist(b, n, 16, rows, 2, 16, 128, {grid}).shape == (0, 8)\n")
     assert subprocess.run([sys.executable, "-c", code], cwd=build.ROOT).returncode == 0
+
+
+@pytest.mark.parametrize("most_parts", [16, 32, 5])
+@pytest.mark.parametrize("seed", range(10))
+def test_the_shares_cover_every_block_once(seed, most_parts):
+    # up to three CTAs an SM, and few items on odd seeds, so that the rule on
+    # parts counts
+    rng = np.random.default_rng(70 + seed)
+    n, heads = (int(rng.integers(1, 3)), int(rng.integers(1, 5))) if seed % 2 else \
+        (int(rng.integers(1, 40)), int(rng.integers(1, 9)))
+    hist, new = rng.integers(0, 20000, size=n), rng.integers(0 if seed % 4 else 1, 18, size=n)
+    nt = [int(rng.integers(0, x + 1)) for x in new]
+    grid = int(rng.integers(150, 457)) if seed else 456
+    extra = int(rng.integers(0, 3))
+    batch, num_pages, rows = make_batch(hist, new, 64, nt, seed)
+    segs = binding.hstu_cache_worklist(batch, num_pages, 64, rows, heads, 16, 128, grid, extra=extra,
+                                       most_parts=most_parts)
+    if most_parts == 16:
+        assert np.array_equal(segs, binding.hstu_cache_worklist(batch, num_pages, 64, rows, heads, 16, 128,
+                                                                grid, extra=extra))
+    tiles = -(-int(new.max()) // 16)
+    blocks = {}  # of each item with any, in their order
+    for qt in range(tiles):
+        for b in range(n):
+            last = min(new[b], 16 * qt + 16) - 1
+            if 16 * qt <= last:
+                p0, p1, seen = hist[b] + 16 * qt, hist[b] + last, hist[b] + new[b] - nt[b]
+                m = len({j // 128 for j in range(min(p1 + 1, seen))} | {p // 128 for p in range(p0, p1 + 1)})
+                blocks.update({(b, h, qt): m for h in range(heads)})
+    total = sum(m + extra for m in blocks.values())
+    per, items = max(-(-total // grid), 1), tiles * n * heads
+    if 0 < items < grid // most_parts:
+        per = max(per, -(-total // (most_parts * items)))
+    at, want = 0, []
+    for (b, h, qt), m in blocks.items():  # CTA c has units [c per, (c + 1) per)
+        c0, c1 = at // per, (at + m - 1) // per
+        for c in range(c0, c1 + 1):
+            i0, i1 = max(c * per - at, 0), min((c + 1) * per - at, m)
+            want.append([c, b, h, qt, i0, i1 - i0, c0, c1 - c0 + 1])
+        at += m + extra
+    assert sorted(segs.tolist()) == sorted(want)
+    assert seed % 2 == 0 or max(x[7] for x in want) > min(most_parts, 16) // 2
+    # a CTA starts at most one item that it does not end: its counter is free
+    starts = [c for c, *_, c0, parts in want if c == c0 and parts > 1]
+    assert len(starts) == len(set(starts))
+
+
+def test_refusals_of_the_shares():
+    b, n, rows = make_batch(np.array([500]), np.array([3]), 16)
+    for most_parts in (0, -1):
+        with pytest.raises(binding.HstuError) as e:
+            binding.hstu_cache_worklist(b, n, 16, rows, 2, 16, 128, 100, most_parts=most_parts)
+        assert e.value.code == BAD
 
 
 # ------------------------------------------- loads of what kernels may write
