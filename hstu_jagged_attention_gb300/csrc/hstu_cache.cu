@@ -193,6 +193,8 @@ __global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) 
 // 168, one CTA of nine.
 __host__ __device__ constexpr int step_warps(int d) { return d == 128 ? 8 : 4; }
 __host__ __device__ constexpr int step_per_sm(int d) { return d == 128 ? 1 : 2; }
+static_assert(step_per_sm(32) <= kStepPerSm && step_per_sm(64) <= kStepPerSm && step_per_sm(128) <= kStepPerSm,
+              "the workspace's parts");
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -652,7 +654,9 @@ using hstu::PagedView;
 
 constexpr long long kCounterBytes = 8192;  // one counter a CTA, rounded up
 
-// Two parts a CTA: up to 2 CTAs an SM with tiles of 16 rows, or one with 128.
+// Two parts a CTA: up to kStepPerSm CTAs an SM with tiles of 16 rows, or one
+// with 128, which needs more.
+static_assert(hstu::kStepPerSm * hstu::kStepRows <= HSTU_BLOCK_M, "parts");
 long long part_bytes(const hstu_cache* c) {
   return (long long)c->sms * 2 * HSTU_BLOCK_M * c->d * (long long)sizeof(float);
 }

@@ -340,6 +340,7 @@ struct Q4Cfg {
   static constexpr int STAGES = RING / STAGEB < 15 ? RING / STAGEB : 15;
   static constexpr int MAX_STAGES = 16;
   static_assert(STAGES >= 2 && STAGES < MAX_STAGES, "stages");
+  static_assert(PER_SM <= kStepPerSm, "the workspace's parts");
 };
 __host__ __device__ constexpr int q4_red_bytes(int warps, int rows, int d) {
   return warps * rows * step_red_stride(d) * (int)sizeof(float);

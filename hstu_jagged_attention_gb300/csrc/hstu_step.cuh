@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kStepRows = 16;
 constexpr int kStepKeys = 128, kStepShift = 7;
+constexpr int kStepPerSm = 3;  // CTAs of such a kernel an SM, at most
 
 struct StepWait {
   unsigned long long limit_ns;
