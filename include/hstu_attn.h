@@ -738,10 +738,15 @@ int hstu_cache_worklist_ex(const hstu_paged_batch* host_batch, int num_pages, in
  *           the dim / 2 cosines of position p, then its sines.  dim: a
  *           multiple of 16, <= d.
  * A token is rotated at its position, a candidate at hist (each candidate
- * stands right behind the history, as in its own causal pass), and products
- * are taken in fp32 and rounded once to bf16.  A token whose position is not
- * in the table is skipped and reported like a page out of range.  The slots
- * of a call must differ from one another.
+ * stands right behind the history, as in its own causal pass), in fp32 and
+ * rounded to bf16 at the end.  Into a cache of 4-bit codes both products and
+ * their sum are rounded to fp32 one by one, keys' and queries' alike, so that
+ * the codes are defined to the bit; the other cache's append may round a
+ * product and the sum at once.  So q_out can differ between the two kinds of
+ * cache, where fp32 numbers up to 2^-22 of the two products' sizes apart round
+ * to different bf16 numbers.
+ * A token whose position is not in the table is skipped and reported like a
+ * page out of range.  The slots of a call must differ from one another.
  * Enqueues one kernel and allocates nothing.
  */
 typedef struct hstu_rotary {

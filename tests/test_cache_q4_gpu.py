@@ -289,6 +289,27 @@ def test_the_rotation_rounds_each_product(pairs):
         assert np.array_equal(layer.f64(got), held(layer.f64(torch.from_numpy(y).bfloat16())))
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+def test_queries_rotated_beside_either_cache(pairs):
+    # the same queries: fl(fl(x c) -+ fl(y s)) beside a cache of codes, and
+    # maybe fl(x c -+ fl(y s)) beside the other: 2^-24 |x c| and two roundings of
+    # the sum apart, 2^-22 (|x c| + |y s|) at most, then rounded to bf16 each
+    kinds = [kind([0] * 4, [4000] * 4, 128, 1, 64, seed=18) for kind in (Q4, Bf16)]
+    table, outs = rotary_table(4000, 64), []
+    for s in kinds:
+        outs.append(torch.full((s.rows, 1, 64), 7.0, device="cuda", dtype=torch.bfloat16))
+        binding.hstu_cache_append(s.cache, s.batch, s.k.cuda(), s.v.cuda(), q=kinds[0].q.cuda(), q_out=outs[-1],
+                                  rotary=table.cuda(), rotary_pairs=pairs)
+    x, y = (layer.f64(o) for o in outs)
+    at = np.tile(np.arange(4000), 4)
+    c, sn = layer.f64(table)[at, None, :32], layer.f64(table)[at, None, 32:]
+    a, b = (slice(0, 64, 2), slice(1, 64, 2)) if pairs else (slice(0, 32), slice(32, 64))
+    q, size = layer.f64(kinds[0].q), np.empty_like(x)
+    size[..., a] = np.abs(q[..., a] * c) + np.abs(q[..., b] * sn)
+    size[..., b] = np.abs(q[..., b] * c) + np.abs(q[..., a] * sn)
+    assert np.all(np.abs(x - y) <= 2.0 ** -22 * size + 2.0 ** -8 * (np.abs(x) + np.abs(y)))
+
+
 def test_every_sequence_is_checked():
     # more sequences than a CTA of the check has threads, wrong ones among them
     n = 700
