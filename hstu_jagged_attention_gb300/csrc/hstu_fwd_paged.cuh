@@ -451,7 +451,9 @@ __device__ void paged_mma_qk(const PagedFwdArgs& a, uint32_t steps, const PagedW
 
 // PV issuer: as role_mma_pv, with the block that holds the tile's last keys
 // cut at the first key that no row sees.
-// Q4: the values come from codes, and rows behind the last key are zeros.
+// Q4: the values come from codes.  Rows behind the last key hold what some
+// bytes stand for, but whatever bytes do is finite, and P is zero there: they
+// add nothing and need no clearing.
 template <int D, bool Q4>
 __device__ void paged_mma_pv(uint32_t steps, const PagedWords* words, uint32_t base, uint32_t tmem,
                              const WaitCtx& wt) {
