@@ -136,7 +136,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 }
 
 // ----------------------------------------------------------------- read back
-// As the append, the other way: one thread a (token, head, 16 channels).
+// As the append, the other way: one thread a (token, head, 16 channels).  Bound
+// by memory: 65,536 tokens of 4 heads of 64 take 24.9 us (134 MB, 5.4 TB/s),
+// 156,000 of 32 histories 52.2 (320 MB, 6.1 TB/s, 90% of a copy's rate; at d = 32
+// 28.2 us, 83%, at d = 128 98.8 us, 95%).
 __global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) {
   after_previous_kernel();
   const int per_head = a.d / 16, per_token = a.heads * per_head;
@@ -681,8 +684,12 @@ constexpr long long kMostUnits = 1 << 30;
 
 // Parts of an item, on average at most: the last of its CTAs sums them alone.
 // The 4-bit cache's CTAs take a block apart for longer than they wait for it, so
-// there more of them pay (four sequences of 10240 to 20480 tokens, 16 items:
-// 13.0 us with 32 parts, 15.6 with 16).
+// there more of them pay.  One token, histories of half of the keys named to all
+// of them, us with 16, 32 and 64 parts: one sequence of 4 heads, 9,000 keys, 7.8,
+// 7.5 and 8.4 at d = 32, 9.2, 8.5 and 9.0 at d = 64, 10.4, 9.2 and 10.0 at d =
+// 128; 60,000 keys 16.2, 11.8 and 10.7, 21.3, 14.5 and 11.9, 25.0, 16.8 and 13.8;
+// five sequences of 20,000, d = 64, 16.5, 14.7 and 14.7; 16 tokens of one head of
+// 128 over 9,000 keys 13.4, 13.7 and 18.7.
 constexpr int kMostParts = 16, kMostPartsQ4 = 32;
 
 // Units for what an item costs besides its blocks (its queries' load, the

@@ -28,12 +28,13 @@ namespace {
 constexpr int kQ4Threads = 256;
 // Accesses in flight, each to whole rows: of the append, which has three rows,
 // the next head's, and the rotation's angles in registers, and of the reading.
-// 65,536 tokens of 4 heads of 64: append 33.2 us with one, 34.1 with two;
-// reading 19.4 with one, 17.8 with two, 18.6 with four.
+// 65,536 tokens of 4 heads of 64: append 33.5 us with one, 33.8 with two;
+// reading 19.6 with one, 17.8 with two, 18.7 with four.
 constexpr int kQ4AppendIter = 1, kQ4ReadIter = 2;
-// Warps an SM below which a warp takes one head only: 6,400 tokens of 4 heads of
-// 128 are appended in 6.8 us with 16, 9.3 with 24 (the heads are not looped over
-// then), and 65,536 in 33.2 with the loop, 59 without.
+// Warps an SM below which a warp takes fewer heads: 6,700 tokens of 4 heads of
+// 128 are appended in 6.8 us with 8 and 16, 9.3 with 24 (three heads and one),
+// and read in 6.9, 5.5 and 6.2 with 8, 16 and 24 (four, two and one); 65,536 of
+// 4 heads of 64 are appended in 33.5 us, 56 with a head a warp.
 constexpr int kQ4Warps = 16;
 
 // How a warp of the append and of the reading works: a lane has 8 channels (a
@@ -136,8 +137,10 @@ __device__ __forceinline__ uint4 q4_turn(const uint4& x, const Q4Angles& g, int 
 }
 
 // 65,536 tokens of 4 heads of 64 with their queries, rotated, take 33.5 us (153
-// MB, 4.6 TB/s): about 230 instructions for 8 channels of k, v and q, half of
-// them on the integer pipe at half rate, weigh as much as the memory.
+// MB, 4.6 TB/s).  Bound by instructions and memory alike: a warp executes 398 for
+// its lanes' 8 channels of k, v and q (26.1 M, whose issue alone takes 21 us; 157
+// of them on the ALU pipe, 55% busy), the issue slots are 70% busy, and the bytes
+// take 22.6 us.
 template <int D>
 __global__ void __launch_bounds__(kQ4Threads)
     append_q4_kernel(const AppendArgs a, const Q4Pool pool, const int head_step) {
@@ -238,6 +241,10 @@ __global__ void __launch_bounds__(kQ4Threads)
   }
 }
 
+// 65,536 tokens of 4 heads of 64 take 17.8 us (86 MB, 4.8 TB/s), 156,000 of 32
+// histories 38.1 (205 MB, 5.4 TB/s, 79% of a copy's rate).  Bound by memory: 136
+// instructions for a lane's 8 channels of k and v keep 58% of the issue slots
+// busy, and what a warp waits for most are its loads (40% of its time).
 template <int D>
 __global__ void __launch_bounds__(kQ4Threads)
     read_q4_kernel(const ReadArgs a, const Q4Pool pool, const int head_step) {
@@ -320,10 +327,15 @@ __global__ void __launch_bounds__(kQ4Threads)
 // second terms: one product for both.
 // Keys past a row's last are masked by a select on p; whatever bytes lie
 // there, as codes they are finite, and so add nothing.
-// Bound by the instructions that make codes into numbers, at 0.55 a cycle and
-// scheduler, and by the way in and out: one token for 512 sequences (log-normal
-// lengths, 2 heads of 64, 59 MB) takes 27.4 us, 4 of them until the first codes
-// are there.  Four warps of 32 keys and three CTAs an SM: 29.3 us when two took
+// Bound by the latency of what a warp does one after the other, which the three
+// warps a scheduler has do not cover, and by the way in and out: one token for
+// 512 sequences (log-normal lengths, 2 heads of 64, 59 MB) takes 27.4 us, 4 of
+// them until the first codes are there and 1.5 to join the cut items.  Issuing
+// its 15.5 M instructions takes 12.3 us, the ALU pipe's share of them, 7.4 M at
+// half rate, 11.7; the slots are 54% busy.  For each instruction that it issues
+// (ncu, in issue cycles) a warp is ready but not chosen for 0.8, and waits 1.2 for
+// the one before it, 0.8 for global memory, 0.6 for a pipe, 0.5 for the other
+// warps, 0.4 for instructions and 0.3 for shared memory.  Four warps of 32 keys and three CTAs an SM: 29.3 us when two took
 // 31.6, four (96 registers a thread) 31.3, and two of eight warps of 16 keys
 // 34.6; at d = 128 registers allow two.
 template <int D>
