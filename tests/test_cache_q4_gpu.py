@@ -643,6 +643,59 @@ def test_readings_between_appends_see_the_last_of_them(d, heads, page, batch, ki
             assert torch.equal(calls[i][4], ref), i
 
 
+@pytest.mark.parametrize("kind", ["q4", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("width,new", FORMS)
+def test_steps_without_a_pause_are_the_steps_one_by_one(width, new, d, kind):
+    # append, attend, read back, step after step: each kernel starts while the
+    # one before it ends, and finds what that one wrote
+    heads, page, steps = 2, 16, 12
+    hist, new = np.array([30, 500, 62]), np.array(new)
+    of_each = -(-(hist + steps * new) // page)
+    pages = int(of_each.sum())
+    rng = np.random.default_rng(d)
+    order, at = rng.permutation(pages), 0
+    table = np.zeros((3, max(int(of_each.max()), width)), dtype=np.int32)
+    for b, n in enumerate(of_each):
+        table[b, :n] = order[at:at + n]
+        at += n
+    gen = torch.Generator().manual_seed(d)
+    first = torch.stack([randn(gen, pages, page, heads, d, sigma=0.5) for _ in range(2)])
+    if kind == "q4":
+        first = torch.from_numpy(layer.q4_pack(first[0], first[1])).cuda()
+        pool = first.clone()
+        cache = binding.hstu_cache_create_q4(pool, page, heads, d)
+    else:
+        first = first.cuda()
+        pool = first.clone()
+        cache = binding.hstu_cache_create(pool[0], pool[1])
+    i32 = lambda x: torch.from_numpy(np.asarray(x, dtype=np.int32)).cuda()
+    off, table = i32(np.concatenate([[0], np.cumsum(new)])), i32(table)
+    rows = int(new.sum())
+    qkv = randn(gen, steps, 3, rows, heads, d, sigma=0.5).cuda()
+    outs = torch.empty(steps, 3, rows, heads, d, device="cuda", dtype=torch.bfloat16)
+    ws = torch.zeros(binding.hstu_cache_workspace_bytes(cache), device="cuda", dtype=torch.uint8)
+    batches = [binding.PagedBatch(off, i32(hist + (i + 1) * new), table, int(new.max())) for i in range(steps)]
+
+    def run(pause):
+        pool.copy_(first)
+        outs.fill_(7.0)
+        torch.cuda.synchronize()
+        for batch, (q, k, v), (out, k_back, v_back) in zip(batches, qkv, outs):
+            for call in (lambda: binding.hstu_cache_append(cache, batch, k, v),
+                         lambda: binding.hstu_attn_fwd_cache(cache, batch, q, 0.125, 1 / 600, out, workspace=ws),
+                         lambda: binding.hstu_cache_read(cache, batch, k_back, v_back)):
+                call()
+                pause()
+        torch.cuda.synchronize()
+        return outs.clone(), pool.clone()
+
+    ref, held = run(torch.cuda.synchronize)
+    for _ in range(5):
+        got, now = run(lambda: None)
+        assert torch.equal(got, ref) and torch.equal(now, held)
+
+
 @pytest.mark.parametrize("own_workspace", [True, False])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("width,new", FORMS)
