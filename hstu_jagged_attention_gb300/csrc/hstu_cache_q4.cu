@@ -335,9 +335,9 @@ __global__ void __launch_bounds__(kQ4Threads)
 // half rate, 11.7; the slots are 54% busy.  For each instruction that it issues
 // (ncu, in issue cycles) a warp is ready but not chosen for 0.8, and waits 1.2 for
 // the one before it, 0.8 for global memory, 0.6 for a pipe, 0.5 for the other
-// warps, 0.4 for instructions and 0.3 for shared memory.  Four warps of 32 keys and three CTAs an SM: 29.3 us when two took
-// 31.6, four (96 registers a thread) 31.3, and two of eight warps of 16 keys
-// 34.6; at d = 128 registers allow two.
+// warps, 0.4 for instructions and 0.3 for shared memory.  Four warps of 32 keys
+// and three CTAs an SM: 29.3 us when two took 31.6, four (96 registers a thread)
+// 31.3, and two of eight warps of 16 keys 34.6; at d = 128 registers allow two.
 template <int D>
 struct Q4Cfg {
   static constexpr int WARPS = 4;
